@@ -1,0 +1,74 @@
+"""The 4-bit format of include/gemm_f16_q4.h in plain numpy / torch on the CPU,
+by the place of each element, and the operators' definitions in 64 bits.
+Test infrastructure; shares no code with the library."""
+import numpy as np
+import torch
+
+NIBBLE = np.array([0, 4, 1, 5, 2, 6, 3, 7])
+
+
+def round_groups(x, group, symmetric=False):
+    """(q, z, s) of the groups along x's last axis: float32 arithmetic as the header states it (each step is one
+    correctly rounded operation, so the results are exact).  x: float32 array, last axis a multiple of group."""
+    x = np.asarray(x, np.float32)
+    g = np.nan_to_num(x, nan=0.0, posinf=np.inf, neginf=-np.inf).reshape(*x.shape[:-1], -1, group)
+    with np.errstate(all="ignore"):
+        lo, hi = np.minimum(g.min(-1), np.float32(0)), np.maximum(g.max(-1), np.float32(0))
+        wide = np.abs(np.maximum(hi, -lo) / np.float32(7) if symmetric else (hi - lo) / np.float32(15))   # never -0
+        s = np.minimum(wide, np.float32(65504)).astype(np.float16).astype(np.float32)
+        some = s > 0
+        z = np.full_like(s, 8) if symmetric else np.clip(np.rint(np.where(some, -lo / s, 0)), 0, 15)
+        q = np.where(some[..., None], np.rint(g / s[..., None]), 0)
+    q = np.clip(q + z[..., None], 0, 15).reshape(x.shape)
+    return q.astype(np.int64), z.astype(np.int64), s.astype(np.float16)
+
+
+def words_of(s, z):
+    return (s.view(np.uint16).astype(np.uint32) | (z.astype(np.uint32) << 16))
+
+
+def scale_zero(words):
+    words = np.asarray(words).astype(np.uint32)
+    return (words & 0xFFFF).astype(np.uint16).view(np.float16).astype(np.float64), (words >> 16).astype(np.float64)
+
+
+def pack_weights(w, group, symmetric=False):
+    """codes and words (uint32 arrays in the header's order) of a float32 n x k matrix."""
+    n, k = w.shape
+    nb, kb = -(-n // 16), -(-k // 128)
+    full = np.zeros((16 * nb, 128 * kb), np.float32)
+    full[:n, :k] = w
+    q, z, s = round_groups(full, group, symmetric)
+    codes = np.zeros((nb, kb, 4, 16, 4), np.uint32)
+    for i in range(16 * nb):
+        for b in range(kb):
+            for g in range(4):
+                for j in range(4):
+                    eight = q[i, 128 * b + 32 * j + 8 * g:][:8]
+                    codes[i // 16, b, g, i % 16, j] = np.sum(eight.astype(np.uint32) << (4 * NIBBLE).astype(np.uint32))
+    words = words_of(s, z).reshape(nb, 16, kb, 128 // group).transpose(0, 2, 1, 3)
+    return codes, np.ascontiguousarray(words)
+
+
+def unpack_weights(codes, words, n, k, group):
+    """The float64 matrix that codes and words (tensors or arrays) stand for."""
+    codes, words = np.asarray(codes).astype(np.int64) & 0xFFFFFFFF, np.asarray(words).astype(np.int64) & 0xFFFFFFFF
+    i, x = np.arange(n)[:, None], np.arange(k)[None]
+    dword = codes[i // 16, x // 128, x % 32 // 8, i % 16, x % 128 // 32]
+    s, z = scale_zero(words[i // 16, x // 128, i % 16, x % 128 // group])
+    return s * ((dword >> (4 * NIBBLE[x % 8]) & 15) - z)
+
+
+def product(a, w, alpha=1.0, relu=False):
+    """(C in 64 bits, the same sum of magnitudes) for float64 a and w."""
+    c, size = a @ w.T * alpha, np.abs(a) @ np.abs(w).T * abs(alpha)
+    return (np.maximum(c, 0) if relu else c), size
+
+
+def half_steps(r):
+    """Largest error of one rounding of r to binary16: half a step of r's binade, 2^-25 below the normals."""
+    return np.maximum(np.abs(r) * 2.0 ** -11, 2.0 ** -25)
+
+
+def host(t: torch.Tensor) -> np.ndarray:
+    return t.detach().cpu().numpy()

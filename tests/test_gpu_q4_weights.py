@@ -1,0 +1,156 @@
+"""GPU tests of 4-bit weights: compression, expansion and the product.
+
+Compression and expansion are sequences of single correctly rounded
+operations, so they must equal tests/q4_reference.py bit for bit.
+
+The product's error against 64 bits: one rounding to binary16 (half a step)
+and fp32 sums.  A product a (q - z) is exact in fp32; it passes through at
+most 32 additions inside one matrix instruction, at most 3 further ones of its
+group, one per group of its wave's share of K, 8 across the waves, and the
+products with s and alpha: D = 32 + 3 + K / group + 8 + 2 roundings, each of at
+most 2^-23 of the sum of magnitudes (2^-24 for a rounding to nearest, twice
+that in case the matrix unit truncates).
+"""
+import numpy as np
+import pytest
+import torch
+
+import q4_reference as ref
+import tiled_dense_gemm_fp16_amd as g
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def weights(n, k, seed):
+    return (torch.randn(n, k, generator=gen(seed)) * (1.0 + torch.rand(n, 1, generator=gen(seed + 1)))).to(torch.float16)
+
+
+def bound(c, size, k, group):
+    depth = 45 + -(-k // group)
+    return ref.half_steps(c) * (1 + 2.0 ** -10) + depth * 2.0 ** -23 * size
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("symmetric", [False, True])
+@pytest.mark.parametrize("n,k", [(1, 1), (16, 128), (17, 129), (5, 300), (40, 1000), (33, 96)])
+def test_compress_and_expand_bit_exact(n, k, group, symmetric):
+    print(f"[q4] compress {n}x{k} group={group} symmetric={symmetric}", flush=True)
+    w = weights(n, k, n + k)
+    packed = g.q4_compress(w.to(DEV), group, symmetric=symmetric)
+    back = g.q4_expand(packed)
+    torch.cuda.synchronize()
+    codes, words = ref.pack_weights(w.float().numpy(), group, symmetric)
+    assert np.array_equal(ref.host(packed.words).view(np.uint32), words)
+    assert np.array_equal(ref.host(packed.codes).view(np.uint32), codes)
+    want = ref.unpack_weights(codes, words, n, k, group).astype(np.float16)
+    assert np.array_equal(ref.host(back), want)
+
+
+def test_compress_special_values():
+    w = torch.zeros(16, 256, dtype=torch.float16)
+    w[0, 3] = float("nan")
+    w[0, 4] = 3.0
+    w[1, 0], w[1, 1] = float("inf"), -2.0
+    w[2, 7] = float("-inf")
+    w[3, 0], w[3, 1] = 65504.0, -65504.0
+    w[4, 0] = 2.0 ** -24          # the scale underflows to 0: the group is held as zeros
+    w[5, :128] = 1.5              # one sign only
+    w[6, :128] = -1.5
+    w[7, :128] = -0.0
+    w[8, :15] = torch.arange(15).to(torch.float16) + 0.5    # ties
+    for symmetric in (False, True):
+        packed = g.q4_compress(w.to(DEV), 128, symmetric=symmetric)
+        back = ref.host(g.q4_expand(packed))
+        codes, words = ref.pack_weights(w.float().numpy(), 128, symmetric)
+        assert np.array_equal(ref.host(packed.words).view(np.uint32), words)
+        assert np.array_equal(ref.host(packed.codes).view(np.uint32), codes)
+        with np.errstate(over="ignore"):
+            want = ref.unpack_weights(codes, words, 16, 256, 128).astype(np.float16)
+        assert np.array_equal(back, want)
+
+
+def test_compress_unaligned_source():
+    buf = torch.empty(24 * 136 + 1, dtype=torch.float16, device=DEV)
+    w = weights(24, 136, 3)
+    at = buf[1:].view(24, 136)
+    at.copy_(w)
+    packed = g.q4_compress(at, 64)
+    codes, words = ref.pack_weights(w.float().numpy(), 64)
+    assert np.array_equal(ref.host(packed.codes).view(np.uint32), codes)
+    out = torch.full((24 * 136 + 3,), 7.0, dtype=torch.float16, device=DEV)
+    g.q4_expand(packed, out=out[1:-2].view(24, 136))
+    want = ref.unpack_weights(codes, words, 24, 136, 64).astype(np.float16)
+    assert np.array_equal(ref.host(out[1:-2]).reshape(24, 136), want)
+    assert bool((out[:1] == 7).all()) and bool((out[-2:] == 7).all())
+
+
+def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shift=0, seed=0):
+    a = torch.randn(m, k, generator=gen(seed + 5)).to(torch.float16)
+    packed = g.q4_compress(weights(n, k, seed).to(DEV), group)
+    room = torch.full((m * n + 2 * 64 + shift,), 9.0, dtype=torch.float16, device=DEV)
+    out = room[64 + shift:64 + shift + m * n].view(m, n)
+    buf = torch.empty(m * k + shift, dtype=torch.float16, device=DEV)
+    ad = buf[shift:].view(m, k)
+    ad.copy_(a)
+    got = g.gemm_q4(ad, packed, epilogue=epilogue, out=out, config=config, alpha=alpha)
+    torch.cuda.synchronize()
+    print(f"[q4] product {m}x{n}x{k} group={group} config={config} epi={epilogue} alpha={alpha} shift={shift}", flush=True)
+    w = ref.unpack_weights(ref.host(packed.codes), ref.host(packed.words), n, k, group)
+    want, size = ref.product(a.double().numpy(), w, float(np.float32(alpha)), epilogue == "relu")
+    err = np.abs(ref.host(got).astype(np.float64) - want)
+    assert (err <= bound(want, size, k, group)).all(), (err / bound(want, size, k, group)).max()
+    assert bool((room[:64 + shift] == 9).all()) and bool((room[64 + shift + m * n:] == 9).all())
+
+
+@pytest.mark.parametrize("config", range(g.q4_num_configs()))
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 16, 128), (1, 100, 2048), (3, 33, 1000), (16, 16, 1024), (17, 70, 1030),
+                                   (33, 48, 520), (64, 64, 256), (65, 40, 4100), (130, 264, 136)])
+def test_every_config(config, group, m, n, k):
+    check(m, n, k, group, config=config, seed=m + n + k)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 1024), (2, 5000, 4100), (13, 256, 8192), (40, 600, 3000), (300, 300, 300)])
+@pytest.mark.parametrize("epilogue,alpha", [("none", 1.0), ("relu", 0.125), ("none", -1.7)])
+def test_automatic_choice(m, n, k, epilogue, alpha):
+    check(m, n, k, 64, epilogue=epilogue, alpha=alpha)
+
+
+def test_unaligned_pointers():
+    check(5, 40, 264, 32, shift=1)
+    check(20, 40, 264, 128, shift=3)
+
+
+def test_long_k():
+    check(1, 20, 70000, 128)
+    check(18, 20, 40000, 64)
+
+
+def test_empty_and_zero_depth():
+    packed = g.q4_compress(torch.zeros(8, 0, dtype=torch.float16, device=DEV))
+    out = torch.full((3, 8), 5.0, dtype=torch.float16, device=DEV)
+    g.gemm_q4(torch.zeros(3, 0, dtype=torch.float16, device=DEV), packed, out=out, alpha=-1.0)
+    assert bool((out.view(torch.int16) == 0).all())
+    packed = g.q4_compress(weights(8, 128, 1).to(DEV))
+    assert g.gemm_q4(torch.zeros(0, 128, dtype=torch.float16, device=DEV), packed).shape == (0, 8)
+    packed = g.q4_compress(torch.zeros(0, 128, dtype=torch.float16, device=DEV))
+    assert g.gemm_q4(torch.zeros(2, 128, dtype=torch.float16, device=DEV), packed).shape == (2, 0)
+    assert g.q4_expand(packed).shape == (0, 128)
+
+
+def test_infinite_rows_stay_in_their_row():
+    a = torch.ones(20, 256, dtype=torch.float16)
+    a[3, 5] = float("inf")
+    a[7, 200] = float("nan")
+    packed = g.q4_compress(weights(40, 256, 2).to(DEV))
+    got = ref.host(g.gemm_q4(a.to(DEV), packed))
+    fine = np.ones(20, bool)
+    fine[[3, 7]] = False
+    assert np.isfinite(got[fine]).all()
+    assert np.isnan(got[7]).all() and not np.isfinite(got[3]).any()

@@ -72,6 +72,19 @@ SIGNATURES = {
     "gemm_f16_status_string": ([_int], ctypes.c_char_p),
 }
 
+# the products with 4-bit operands (mirrors include/gemm_f16_q4.h)
+_f32 = ctypes.c_float
+Q4_SIGNATURES = {
+    "gemm_f16_q4_codes_bytes": ([_i64, _i64], _i64),
+    "gemm_f16_q4_words_bytes": ([_i64, _i64, _int], _i64),
+    "gemm_f16_q4_compress": ([_i64, _i64, _int, _int, _vp, _vp, _vp, _vp], _int),
+    "gemm_f16_q4_expand": ([_i64, _i64, _int, _vp, _vp, _vp, _vp], _int),
+    "gemm_f16_q4": ([_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _f32, _int, _int, _vp], _int),
+    "gemm_f16_plan_q4": ([_i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)], _int),
+    "gemm_f16_q4_num_configs": ([], _int),
+    "gemm_f16_q4_config_name": ([_int], ctypes.c_char_p),
+}
+
 _lib = None
 
 
@@ -99,7 +112,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build the HIP library first "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         h = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in SIGNATURES.items():
+        for name, (args, res) in {**SIGNATURES, **Q4_SIGNATURES}.items():
             fn = getattr(h, name)
             fn.argtypes = args
             fn.restype = res
@@ -439,3 +452,9 @@ def probe_mfma_tflops(mode: int, seconds: float = 0.3, seed: int = 0) -> float:
     e.record(stream)
     torch.cuda.synchronize()
     return flops.value / (s.elapsed_time(e) * 1e-3) / 1e12
+
+
+# ---- products with 4-bit operands (include/gemm_f16_q4.h) ------------------
+
+from .q4 import (Q4Matrix, gemm_q4, plan_q4, q4_compress, q4_config_name, q4_expand,  # noqa: E402,F401
+                 q4_num_configs)

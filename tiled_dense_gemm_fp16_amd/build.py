@@ -16,11 +16,11 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgemm_f16.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "gemm_f16_api.cpp", "gemm_f16_kernels.hip", "gemm_f16_nn.hip", "gemm_f16_nt.hip", "gemm_f16_tn.hip",
-    "gemm_f16_tt.hip", "gemm_f16_sparse.hip")]
+    "gemm_f16_tt.hip", "gemm_f16_sparse.hip", "gemm_f16_q4_api.cpp", "gemm_f16_q4_weights.hip")]
 # what each kind of source includes (for incremental builds)
-HOST_DEPS = [os.path.join(CSRC, f) for f in ("gemm_f16_internal.h", "gemm_f16_tuned.inc")] + \
-    [os.path.join(INCLUDE, "gemm_f16.h")]
-KERNEL_DEPS = [os.path.join(CSRC, f) for f in ("gemm_f16_internal.h", "gemm_f16_tile.h")]
+HOST_DEPS = [os.path.join(CSRC, f) for f in ("gemm_f16_internal.h", "gemm_f16_tuned.inc", "gemm_f16_q4_format.h")] + \
+    [os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_f16_q4.h")]
+KERNEL_DEPS = [os.path.join(CSRC, f) for f in ("gemm_f16_internal.h", "gemm_f16_tile.h", "gemm_f16_q4_format.h")]
 PROBE_LIB = os.path.join(PKG, "libgemm_f16_probe.so")
 PROBE_SOURCES = [os.path.join(CSRC, "mfma_probe.hip")]
 

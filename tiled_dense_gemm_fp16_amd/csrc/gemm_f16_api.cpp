@@ -48,6 +48,39 @@ const ConfigDesc kSpConfigs[kNumSpConfigs] = {
     {"sp_256x256x64_s3_spread", 256, 256, 64, 3, 4, true, 8, 8, kNN | kNT, 1},
 };
 
+bool overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    if (a_bytes <= 0 || b_bytes <= 0)
+        return false;
+    uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+    return a0 < b0 + (uintptr_t)b_bytes && b0 < a0 + (uintptr_t)a_bytes;
+}
+
+namespace {
+// Per-device check that the device is gfx950, done once per device.
+constexpr int kMaxDevices = 64;
+std::mutex g_dev_mutex;
+int g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950, 2 other
+} // namespace
+
+gemm_f16_status_t check_device(int *device)
+{
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0)
+        return GEMM_F16_ERROR_NO_DEVICE;
+    if (dev >= kMaxDevices)
+        return GEMM_F16_ERROR_UNSUPPORTED_DEVICE;
+    *device = dev;
+    std::lock_guard<std::mutex> lock(g_dev_mutex);
+    if (g_dev_state[dev] == 0) {
+        hipDeviceProp_t prop;
+        if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
+            return GEMM_F16_ERROR_NO_DEVICE;
+        g_dev_state[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
+    }
+    return g_dev_state[dev] == 1 ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_DEVICE;
+}
+
 namespace {
 
 constexpr int kComputeUnits = 256;   // MI355X
@@ -69,14 +102,6 @@ int vec_width(const void *p, int64_t pitch)
         if (pitch % v == 0 && addr % (uintptr_t)(2 * v) == 0)
             return v;
     return 1;
-}
-
-bool overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
-{
-    if (a_bytes <= 0 || b_bytes <= 0)
-        return false;
-    uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + (uintptr_t)b_bytes && b0 < a0 + (uintptr_t)a_bytes;
 }
 
 gemm_f16_status_t validate(int64_t M, int64_t N, int64_t K, const void *A, bool trans_a, const void *B,
@@ -440,29 +465,6 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, const void *A, bool
     slot.status = st;
     slot.plan = *plan;
     return st;
-}
-
-// Per-device check that the device is gfx950, done once per device.
-constexpr int kMaxDevices = 64;
-std::mutex g_dev_mutex;
-int g_dev_state[kMaxDevices];   // 0 unknown, 1 gfx950, 2 other
-
-gemm_f16_status_t check_device(int *device)
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0)
-        return GEMM_F16_ERROR_NO_DEVICE;
-    if (dev >= kMaxDevices)
-        return GEMM_F16_ERROR_UNSUPPORTED_DEVICE;
-    *device = dev;
-    std::lock_guard<std::mutex> lock(g_dev_mutex);
-    if (g_dev_state[dev] == 0) {
-        hipDeviceProp_t prop;
-        if (hipGetDeviceProperties(&prop, dev) != hipSuccess)
-            return GEMM_F16_ERROR_NO_DEVICE;
-        g_dev_state[dev] = strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? 1 : 2;
-    }
-    return g_dev_state[dev] == 1 ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_DEVICE;
 }
 
 // Enqueue a planned call; W is the split-K workspace (plan->splits > 1).

@@ -7,7 +7,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "gemm_f16.h"
+
 namespace gemm_f16_impl {
+
+// Whether two byte ranges share a byte (null or empty ranges share none).
+bool overlaps(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes);
+
+// The current device, if it is a gfx950 (checked once per device).
+gemm_f16_status_t check_device(int *device);
 
 // Kernel arguments, passed by value.  All dimensions fit in int32 (the public
 // API limits M, N, K to 2^31 - 1 and K, N to 2^22).
