@@ -84,6 +84,111 @@ gemm_f16_status_t gemm_f16_plan_q4(int64_t M, int64_t N, int64_t K, int group, i
 int gemm_f16_q4_num_configs(void);
 const char *gemm_f16_q4_config_name(int config);
 
+/* ---- key/value cache ---------------------------------------------------------
+ * Keys and values of `heads` heads of `head_dim` (64, 128 or 256) in `pages`
+ * pages of `page_size` tokens (a multiple of 8), rounded per token and head
+ * in groups of `group` neighbours of the head dimension (group <= head_dim).
+ * Codes and words, uint32, contiguous, 16-byte aligned:
+ *   k_codes [pages][heads][page_size][head_dim / 8]; in every block of
+ *           b = min(head_dim, 128) the dword of d = 32 j + 8 g + 0..7 is at
+ *           g (b / 32) + j
+ *   v_codes [pages][heads][page_size / 8][16][head_dim / 16]: [d % 16][d / 16]
+ *           holds 8 successive tokens of one d, token i of the eight as value i
+ *   k_words, v_words [pages][heads][head_dim / group][page_size]
+ * A sequence's token t is in slot t % page_size of page table[t / page_size]
+ * of its row of the page table.
+ */
+typedef struct gemm_f16_q4_cache {
+    void *k_codes, *k_words, *v_codes, *v_words;
+    int64_t pages;
+    int32_t heads, page_size, head_dim, group;
+} gemm_f16_q4_cache_t;
+
+/* Limits: heads and q_heads, batch, max_pages, page_size, pages. */
+#define GEMM_F16_Q4_MAX_HEADS 4096
+#define GEMM_F16_Q4_MAX_BATCH ((int64_t)1 << 20)
+#define GEMM_F16_Q4_MAX_PAGE ((int64_t)1 << 16)
+#define GEMM_F16_Q4_MAX_LENGTH ((int64_t)1 << 30)   /* max_pages * page_size */
+#define GEMM_F16_Q4_MAX_TOKENS ((int64_t)1 << 30)   /* of one append or read */
+#define GEMM_F16_Q4_MAX_PAGES ((int64_t)1 << 30)
+
+/*
+ * Append new tokens' keys and values to the cache.
+ *   K, V    : tokens x heads x head_dim binary16; a token's heads are
+ *             contiguous, tokens k_stride / v_stride elements apart (slices
+ *             of a fused projection's output need no copy).
+ *   table   : int32 batch x max_pages.
+ *   lengths : int32 batch, tokens already in the cache.
+ *   starts  : int32 batch + 1: sequence i's new tokens are rows starts[i] up
+ *             to starts[i + 1] (not decreasing).  NULL: one token for each
+ *             sequence (tokens == batch).
+ *   cos, sin: fp32 positions x rotary_dim / 2, or NULL (no rotation):
+ *             rotation of the first rotary_dim (a multiple of 16) elements of
+ *             keys (and Q) by the angle of the token's position, of the pairs
+ *             (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with interleaved 1:
+ *             (a, b) -> (a cos - b sin, b cos + a sin), in fp32, rounded only
+ *             to codes (Q: to binary16).
+ *   Q, Q_out: queries of the same tokens, tokens x q_heads x head_dim
+ *             (q_stride elements apart), rotated into Q_out (contiguous);
+ *             both NULL: none.  Q_out may be Q when Q is contiguous.
+ * New token j of sequence i goes to position lengths[i] + j.  A token is not
+ * written, and its row of Q_out is zeroed, when its position is negative,
+ * past max_pages * page_size or (with cos) not below positions, or its page is
+ * not in [0, pages).  Rows of no sequence are left as they were, in the
+ * cache and in Q_out.  Sequences must not share the pages they append to.
+ */
+gemm_f16_status_t gemm_f16_q4_cache_append(const gemm_f16_q4_cache_t *cache, int64_t batch, int64_t tokens,
+                                           int64_t max_pages, const void *K, int64_t k_stride, const void *V,
+                                           int64_t v_stride, const int32_t *table, const int32_t *lengths,
+                                           const int32_t *starts, const void *Q, int64_t q_stride, void *Q_out,
+                                           int q_heads, const float *cos, const float *sin, int64_t positions,
+                                           int rotary_dim, int interleaved, void *stream);
+
+/*
+ * What the cache holds of each sequence: row starts[i] + j of K and V
+ * (tokens x heads x head_dim binary16, contiguous, 16-byte aligned) becomes
+ * position first[i] + j (first NULL: from 0), each value rounded once; zeros
+ * for a position or page out of range.  Rows of no sequence are left.
+ */
+gemm_f16_status_t gemm_f16_q4_cache_read(const gemm_f16_q4_cache_t *cache, int64_t batch, int64_t tokens,
+                                         int64_t max_pages, const int32_t *table, const int32_t *first,
+                                         const int32_t *starts, void *K, void *V, void *stream);
+
+/*
+ * Attention of one query token of each sequence over its cached keys and
+ * values, the score block scaled as gemm_f16_scaled's:
+ *   out[i][h] = sum_t softmax_t(scale * q[i][h] . k[t]) v[t],  t < lengths[i]
+ * with query head h reading cache head h / (q_heads / heads).
+ *   Q, out  : batch x q_heads x head_dim binary16; Q's sequences q_stride
+ *             elements apart, out contiguous (16-byte aligned both, q_stride
+ *             a multiple of 8); out overlaps nothing else.
+ *   lengths : int32 batch; a length below 1 gives a row of zeros, one beyond
+ *             max_pages * page_size counts as that.  Tokens whose page is not
+ *             in [0, pages) are left out, as by a mask.
+ *   splits  : parts the sequences are divided into, computed by separate
+ *             workgroups and joined in order by a second kernel:
+ *             GEMM_F16_SPLITS_AUTO or 1 .. GEMM_F16_Q4_MAX_SPLITS.
+ *   max_length : what no length exceeds, for the choice of splits only (0:
+ *             max_pages * page_size); any value gives right results.
+ *   workspace : caller-owned, 16-byte aligned, of at least the plan's
+ *             workspace_bytes, as gemm_f16_split's; NULL when the plan has 1
+ *             split.
+ * Scores, softmax and sums are fp32; codes enter the matrix cores exactly and
+ * probabilities in two binary16 parts; one rounding at the end.
+ */
+#define GEMM_F16_Q4_MAX_SPLITS 256
+gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_t batch, int q_heads,
+                                        int64_t max_pages, const void *Q, int64_t q_stride, const int32_t *table,
+                                        const int32_t *lengths, float scale, void *out, int splits,
+                                        int64_t max_length, void *workspace, int64_t workspace_bytes, void *stream);
+
+/* How that call would run, without any HIP call: splits, workspace_bytes,
+ * grid (workgroups of the first kernel), threads, lds_bytes, block_m (query
+ * heads of a workgroup), block_n (tokens of a wave's step); flops and
+ * min_bytes of max_length tokens in every sequence. */
+gemm_f16_status_t gemm_f16_plan_q4_attention(int64_t batch, int q_heads, int heads, int head_dim, int group,
+                                             int64_t max_length, int splits, gemm_f16_plan_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

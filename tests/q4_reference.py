@@ -72,3 +72,51 @@ def half_steps(r):
 
 def host(t: torch.Tensor) -> np.ndarray:
     return t.detach().cpu().numpy()
+
+
+# ---- the paged cache ---------------------------------------------------------------------------------------------
+
+def key_place(d, dim):
+    """Dword of a token's row that holds element d."""
+    b = min(dim, 128)
+    return d // b * (b // 8) + d % 32 // 8 * (b // 32) + d % b // 32
+
+
+class Cache:
+    """A cache as plain arrays: codes and zero points and scales by [page, slot, head, d]."""
+
+    def __init__(self, k_codes, k_words, v_codes, v_words, group):
+        u = [np.asarray(x).astype(np.int64) & 0xFFFFFFFF for x in (k_codes, k_words, v_codes, v_words)]
+        pages, heads, slots, d8 = u[0].shape
+        dim = 8 * d8
+        d, t = np.arange(dim), np.arange(slots)[:, None]
+        self.group = group
+        self.q = {"k": np.stack([u[0][:, :, :, key_place(i, dim)] >> (4 * NIBBLE[i % 8]) & 15 for i in d], -1).transpose(0, 2, 1, 3),
+                  "v": (u[2][:, :, t // 8, d % 16, d // 16] >> (4 * NIBBLE[t % 8]) & 15).transpose(0, 2, 1, 3)}
+        self.word = {"k": u[1].transpose(0, 3, 1, 2), "v": u[3].transpose(0, 3, 1, 2)}
+
+    def values(self, which):
+        """float64 [page, slot, head, d]"""
+        s, z = scale_zero(self.word[which])
+        return np.repeat(s, self.group, -1) * (self.q[which] - np.repeat(z, self.group, -1))
+
+
+def rotate(x, cos, sin, interleaved):
+    """float32 rotation of x [rows, heads, d] with cos, sin [rows, half]: every product and sum rounded by itself."""
+    x = np.asarray(x, np.float32).copy()
+    half = cos.shape[1]
+    a, b = (slice(0, 2 * half, 2), slice(1, 2 * half, 2)) if interleaved else (slice(0, half), slice(half, 2 * half))
+    c, s = cos[:, None].astype(np.float32), sin[:, None].astype(np.float32)
+    p, q = x[..., a].copy(), x[..., b].copy()
+    x[..., a], x[..., b] = p * c - q * s, q * c + p * s
+    return x
+
+
+def attention(q, k, v, scale):
+    """(out, sum of p |v|, largest sum of magnitudes of a score) of one head's query q [d] over k, v [n, d], 64 bits."""
+    if not len(k):
+        return np.zeros_like(q), np.zeros_like(q)
+    x = k @ q * scale
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    return p @ v, p @ np.abs(v)

@@ -130,3 +130,132 @@ def test_reference_rounding_and_layout():
         back = (s[..., None] * (q.reshape(7, -1, group) - z[..., None])).reshape(x.shape)
         step = np.repeat(s.astype(np.float64), group, -1)
         assert (np.abs(back - x) <= step * (0.5 + 16 * 2.0 ** -11 + (0.5 if not symmetric else 0))).all()
+
+
+def cache_struct(**over):
+    from tiled_dense_gemm_fp16_amd.q4 import _CacheStruct
+    f = {**dict(k_codes=at(10), k_words=at(11), v_codes=at(12), v_words=at(13), pages=4, heads=2, page_size=16, head_dim=128,
+                group=64), **over}
+    return _CacheStruct(*(f[n] for n, _ in _CacheStruct._fields_))
+
+
+BAD_CACHES = [dict(k_codes=None), dict(k_words=None), dict(v_codes=None), dict(v_words=None), dict(pages=-1), dict(heads=0),
+              dict(page_size=0), dict(page_size=12), dict(page_size=-8), dict(head_dim=96), dict(head_dim=0), dict(group=16),
+              dict(head_dim=64, group=128)]
+LARGE_CACHES = [dict(heads=4097), dict(page_size=(1 << 16) + 8), dict(pages=(1 << 30) + 1)]
+
+
+def append(cache=None, batch=3, tokens=6, max_pages=2, k=at(0), ks=256, v=at(1), vs=256, table=at(2), lengths=at(3),
+           starts=at(4), q=at(5), qs=512, out=at(6), heads=4, cos=at(7), sin=at(8), positions=32, rotary=128, inter=0):
+    c = cache_struct() if cache is None else cache
+    return g.lib().gemm_f16_q4_cache_append(ctypes.byref(c), batch, tokens, max_pages, k, ks, v, vs, table, lengths, starts, q, qs,
+                                            out, heads, cos, sin, positions, rotary, inter, None)
+
+
+def read(cache=None, batch=3, tokens=6, max_pages=2, table=at(2), first=at(3), starts=at(4), k=at(0), v=at(1)):
+    c = cache_struct() if cache is None else cache
+    return g.lib().gemm_f16_q4_cache_read(ctypes.byref(c), batch, tokens, max_pages, table, first, starts, k, v, None)
+
+
+def attention(cache=None, batch=3, heads=4, max_pages=2, q=at(0), qs=512, table=at(1), lengths=at(2), out=at(3), splits=1,
+              max_length=0, ws=None, size=0):
+    c = cache_struct() if cache is None else cache
+    return g.lib().gemm_f16_q4_attention(ctypes.byref(c), batch, heads, max_pages, q, qs, table, lengths, 0.1, out, splits,
+                                         max_length, ws, size, None)
+
+
+@pytest.mark.parametrize("call", [append, read, attention])
+def test_cache_refusals(call):
+    for bad in BAD_CACHES:
+        assert call(cache_struct(**bad)) == INVALID, bad
+    for bad in LARGE_CACHES:
+        assert call(cache_struct(**bad)) == SIZE, bad
+    for bad in (dict(k_codes=at(10) + 8), dict(v_words=at(13) + 4)):
+        assert call(cache_struct(**bad)) == MISALIGNED, bad
+    assert call(batch=-1) == INVALID and call(max_pages=-1) == INVALID and call(batch=(1 << 20) + 1) == SIZE
+    assert call(max_pages=1 << 27) == SIZE and call(table=None) == INVALID and call(table=at(2) + 2) == MISALIGNED
+    assert call(batch=0) == 0 or call is not attention
+    if not torch.cuda.is_available():
+        assert call() == NO_DEVICE
+
+
+def test_append_refusals():
+    for bad in (dict(tokens=-1), dict(starts=None), dict(k=None), dict(v=None), dict(lengths=None), dict(ks=255), dict(vs=0),
+                dict(qs=511), dict(q=None), dict(out=None), dict(heads=0), dict(cos=None), dict(sin=None), dict(rotary=8),
+                dict(rotary=24), dict(rotary=144), dict(rotary=0), dict(positions=-1), dict(inter=2),
+                dict(cos=None, sin=None, rotary=16), dict(out=at(0)), dict(out=at(1)), dict(out=at(5), qs=520),
+                dict(out=at(5) + 2), dict(out=at(10)), dict(out=at(7)), dict(out=at(2)), dict(k=at(12)), dict(q=at(13)),
+                dict(cache=cache_struct(v_codes=at(10)))):
+        assert append(**bad) == INVALID, bad
+    for bad in (dict(k=at(0) + 1), dict(q=at(5) + 1), dict(lengths=at(3) + 2), dict(starts=at(4) + 1), dict(cos=at(7) + 2)):
+        assert append(**bad) == MISALIGNED, bad
+    assert append(tokens=(1 << 30) + 1) == SIZE and append(heads=4097, qs=4097 * 128) == SIZE
+    assert append(tokens=0) == 0 and append(batch=0) == 0
+    if not torch.cuda.is_available():
+        assert append(out=at(5)) == NO_DEVICE and append(batch=6, starts=None) == NO_DEVICE
+        assert append(q=None, out=None, cos=None, sin=None, rotary=0) == NO_DEVICE
+
+
+def test_read_refusals():
+    for bad in (dict(tokens=-1), dict(k=None), dict(v=None), dict(starts=None), dict(k=at(1)), dict(k=at(10)), dict(v=at(2)),
+                dict(v=at(4)), dict(k=at(3))):
+        assert read(**bad) == INVALID, bad
+    for bad in (dict(k=at(0) + 8), dict(v=at(1) + 2), dict(first=at(3) + 1), dict(starts=at(4) + 2)):
+        assert read(**bad) == MISALIGNED, bad
+    assert read(tokens=(1 << 30) + 1) == SIZE and read(tokens=0) == 0
+    if not torch.cuda.is_available():
+        assert read(first=None) == NO_DEVICE
+
+
+def test_attention_refusals():
+    for bad in (dict(heads=0), dict(heads=3), dict(heads=-2), dict(q=None), dict(out=None), dict(lengths=None), dict(qs=511),
+                dict(splits=-1), dict(splits=257), dict(max_length=-1), dict(size=-1), dict(ws=None, size=4), dict(out=at(0)),
+                dict(out=at(11)), dict(out=at(1)), dict(out=at(2)), dict(cache=cache_struct(pages=0))):
+        assert attention(**bad) == INVALID, bad
+    for bad in (dict(q=at(0) + 8), dict(qs=516), dict(out=at(3) + 8), dict(lengths=at(2) + 1)):
+        assert attention(**bad) == MISALIGNED, bad
+    need = g.plan_attention_q4(3, 4, 2, 128, 64, 32, 2)["workspace_bytes"]
+    assert need == 3 * 4 * 2 * (128 + 2) * 4
+    assert attention(splits=2) == 7 and attention(splits=2, ws=at(4), size=need - 1) == 7
+    assert attention(splits=2, ws=at(4) + 4, size=need) == MISALIGNED
+    assert attention(splits=2, ws=at(3), size=need) == INVALID and attention(splits=2, ws=at(13), size=need) == INVALID
+    if not torch.cuda.is_available():
+        assert attention(splits=2, ws=at(4), size=need) == NO_DEVICE and attention(max_pages=0, table=None) == NO_DEVICE
+
+
+def test_attention_plans():
+    for batch, heads, length in [(1, 1, 1), (1, 8, 131000), (64, 8, 4096), (0, 4, 10), (1, 2, 0)]:
+        p = g.plan_attention_q4(batch, heads, heads, 128, 64, length)
+        assert 1 <= p["splits"] <= 256 and p["lds_bytes"] <= 163840
+        assert p["workspace_bytes"] == (batch * heads * p["splits"] * 130 * 4 if p["splits"] > 1 else 0)
+    assert g.plan_attention_q4(1, 8, 8, 128, 64, 131000)["splits"] > 1
+    assert g.plan_attention_q4(1, 8, 8, 128, 64, 100)["splits"] == 1
+    with pytest.raises(g.GemmError):
+        g.plan_attention_q4(1, 5, 2, 128, 64, 100)
+
+
+def test_cache_binding_refusals():
+    with pytest.raises(ValueError):
+        g.q4_cache(4, 2, 12, 128, device="cpu")
+    with pytest.raises(ValueError):
+        g.q4_cache(4, 2, 16, 64, 128, device="cpu")
+    c = g.q4_cache(4, 2, 16, 128, device="cpu")
+    i = torch.zeros(1, 1, dtype=torch.int32)
+    q = torch.zeros(1, 2, 128, dtype=torch.float16)
+    for fn in (lambda: g.attention_q4(q, c, i, i[0]), lambda: g.q4_cache_append(c, q, q, i, i[0]),
+               lambda: g.q4_cache_read(c, i, torch.zeros(2, dtype=torch.int32), 1)):
+        with pytest.raises(ValueError):
+            fn()                                           # not on the GPU
+
+
+def test_reference_cache_layout():
+    # one token's key and value, by hand: d = 70 of 128 is dword 2 * 4 + ... of block 0 (j = 2, g = 0, i = 6)
+    assert ref.key_place(70, 128) == 2 and ref.key_place(40, 64) == 3 and ref.key_place(200, 256) == 16 + 1 * 4 + 2
+    codes = np.zeros((1, 1, 8, 16), np.uint32)
+    codes[0, 0, 5, 2] = 9 << (4 * 3)                       # value 6 of the eight is nibble 3
+    values = np.zeros((1, 1, 1, 16, 8), np.uint32)
+    values[0, 0, 0, 70 % 16, 70 // 16] = 11 << (4 * 6)     # token 5 of the eight is nibble 6
+    words = np.full((1, 1, 2, 8), 0x3C00, np.uint32)       # scale 1, zero point 0
+    c = ref.Cache(codes, words, values, words, 64)
+    k, v = c.values("k"), c.values("v")
+    assert k[0, 5, 0, 70] == 9 and k.sum() == 9 and v[0, 5, 0, 70] == 11 and v.sum() == 11

@@ -81,6 +81,11 @@ Q4_SIGNATURES = {
     "gemm_f16_q4_expand": ([_i64, _i64, _int, _vp, _vp, _vp, _vp], _int),
     "gemm_f16_q4": ([_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _f32, _int, _int, _vp], _int),
     "gemm_f16_plan_q4": ([_i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)], _int),
+    "gemm_f16_q4_cache_append": ([_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _int, _vp, _vp,
+                                  _i64, _int, _int, _vp], _int),
+    "gemm_f16_q4_cache_read": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "gemm_f16_q4_attention": ([_vp, _i64, _int, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _int, _i64, _vp, _i64, _vp], _int),
+    "gemm_f16_plan_q4_attention": ([_i64, _int, _int, _int, _int, _i64, _int, ctypes.POINTER(Plan)], _int),
     "gemm_f16_q4_num_configs": ([], _int),
     "gemm_f16_q4_config_name": ([_int], ctypes.c_char_p),
 }
@@ -456,5 +461,5 @@ def probe_mfma_tflops(mode: int, seconds: float = 0.3, seed: int = 0) -> float:
 
 # ---- products with 4-bit operands (include/gemm_f16_q4.h) ------------------
 
-from .q4 import (Q4Matrix, gemm_q4, plan_q4, q4_compress, q4_config_name, q4_expand,  # noqa: E402,F401
-                 q4_num_configs)
+from .q4 import (Q4Cache, Q4Matrix, attention_q4, gemm_q4, plan_attention_q4, plan_q4, q4_cache,  # noqa: E402,F401
+                 q4_cache_append, q4_cache_read, q4_compress, q4_config_name, q4_expand, q4_num_configs)

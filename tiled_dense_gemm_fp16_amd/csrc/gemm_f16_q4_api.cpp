@@ -62,6 +62,111 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, int conf
     return GEMM_F16_SUCCESS;
 }
 
+// The cache's description and the page table's shape.
+gemm_f16_status_t validate_cache(const gemm_f16_q4_cache_t *c, int64_t batch, int64_t max_pages)
+{
+    if (!c || c->pages < 0 || c->heads < 1 || batch < 0 || max_pages < 0 || !known_group(c->group) ||
+        (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) || c->group > c->head_dim || c->page_size < 8 ||
+        c->page_size % 8 != 0)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (c->heads > GEMM_F16_Q4_MAX_HEADS || batch > GEMM_F16_Q4_MAX_BATCH || c->page_size > GEMM_F16_Q4_MAX_PAGE ||
+        c->pages > GEMM_F16_Q4_MAX_PAGES || max_pages > GEMM_F16_Q4_MAX_LENGTH / c->page_size)
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
+    if (c->pages > 0 && (!c->k_codes || !c->k_words || !c->v_codes || !c->v_words))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (((uintptr_t)c->k_codes | (uintptr_t)c->k_words | (uintptr_t)c->v_codes | (uintptr_t)c->v_words) % 16)
+        return GEMM_F16_ERROR_MISALIGNED;
+    return GEMM_F16_SUCCESS;
+}
+
+// Bytes of k_codes (and v_codes), and of k_words (and v_words); sizes are
+// within the limits, so the products fit.
+int64_t cache_codes_bytes(const gemm_f16_q4_cache_t *c)
+{
+    return c->pages * c->heads * c->page_size * (c->head_dim / 2);
+}
+int64_t cache_words_bytes(const gemm_f16_q4_cache_t *c)
+{
+    return c->pages * c->heads * c->page_size * (c->head_dim / c->group) * 4;
+}
+
+// Whether a range shares a byte with any of the cache's buffers.
+bool overlaps_cache(const void *p, int64_t bytes, const gemm_f16_q4_cache_t *c)
+{
+    const int64_t cb = cache_codes_bytes(c), wb = cache_words_bytes(c);
+    return overlaps(p, bytes, c->k_codes, cb) || overlaps(p, bytes, c->v_codes, cb) ||
+           overlaps(p, bytes, c->k_words, wb) || overlaps(p, bytes, c->v_words, wb);
+}
+
+bool buffers_apart(const gemm_f16_q4_cache_t *c)
+{
+    const int64_t cb = cache_codes_bytes(c), wb = cache_words_bytes(c);
+    return !overlaps(c->k_codes, cb, c->v_codes, cb) && !overlaps(c->k_codes, cb, c->k_words, wb) &&
+           !overlaps(c->k_codes, cb, c->v_words, wb) && !overlaps(c->v_codes, cb, c->k_words, wb) &&
+           !overlaps(c->v_codes, cb, c->v_words, wb) && !overlaps(c->k_words, wb, c->v_words, wb);
+}
+
+Q4Pages pages_of(const gemm_f16_q4_cache_t *c, const int32_t *table, int64_t batch, int64_t max_pages)
+{
+    Q4Pages p;
+    p.k_codes = (uint32_t *)c->k_codes;
+    p.k_words = (uint32_t *)c->k_words;
+    p.v_codes = (uint32_t *)c->v_codes;
+    p.v_words = (uint32_t *)c->v_words;
+    p.pages = c->pages;
+    p.heads = c->heads;
+    p.page_size = c->page_size;
+    p.head_dim = c->head_dim;
+    p.group = c->group;
+    p.table = table;
+    p.batch = (int)batch;
+    p.max_pages = (int)max_pages;
+    return p;
+}
+
+// Rows of `heads` heads at a pitch of `stride` elements: long enough, 2-byte
+// aligned, and whether 16-byte loads are.
+bool rows_fit(int64_t stride, int64_t heads, int head_dim) { return stride >= heads * head_dim; }
+bool rows_aligned(const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
+int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0; }
+
+// Parts of the sequences: as many as give every CU four workgroups, while
+// each wave of a part keeps at least two blocks of tokens.
+gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
+                                 int splits, gemm_f16_plan_t *p)
+{
+    if (batch < 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0 || max_length < 0 || splits < 0 ||
+        splits > GEMM_F16_Q4_MAX_SPLITS || !known_group(group) || group > head_dim ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (batch > GEMM_F16_Q4_MAX_BATCH || q_heads > GEMM_F16_Q4_MAX_HEADS || max_length > GEMM_F16_Q4_MAX_LENGTH)
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
+    const int64_t tiles = (q_heads / heads + 15) / 16, units = batch * heads * tiles;
+    if (splits == GEMM_F16_SPLITS_AUTO) {
+        const int64_t blocks = (max_length + kQ4AttentionTokens - 1) / kQ4AttentionTokens;
+        const int64_t fill = units > 0 ? (4 * 256 + units - 1) / units : 1;
+        const int64_t most = blocks / (2 * kQ4AttentionWaves);
+        splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
+    }
+    memset(p, 0, sizeof(*p));
+    p->block_m = 16;
+    p->block_n = kQ4AttentionTokens;
+    p->block_k = head_dim;
+    p->stages = 1;
+    p->threads = 64 * kQ4AttentionWaves;
+    p->vec_a = p->vec_c = 8;
+    p->vec_b = 32;
+    p->tiles_m = batch * heads * tiles;
+    p->tiles_n = splits;
+    p->grid = units * splits;
+    p->lds_bytes = q4_attention_lds_bytes(head_dim);
+    p->flops = 4.0 * (double)batch * (double)max_length * (double)q_heads * (double)head_dim;
+    p->min_bytes = (double)batch * ((double)max_length * heads * (head_dim + 8.0 * head_dim / group) + 4.0 * q_heads * head_dim);
+    p->splits = splits;
+    p->workspace_bytes = splits > 1 ? batch * q_heads * splits * (head_dim + 2) * 4 : 0;
+    return p->grid > 0x7fffffff ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
+}
+
 } // namespace
 } // namespace gemm_f16_impl
 
@@ -191,6 +296,181 @@ const char *gemm_f16_q4_config_name(int config)
     if (config < 0 || config >= kNumQ4Configs)
         return nullptr;
     return kQ4Configs[config].name;
+}
+
+gemm_f16_status_t gemm_f16_q4_cache_append(const gemm_f16_q4_cache_t *cache, int64_t batch, int64_t tokens,
+                                           int64_t max_pages, const void *K, int64_t k_stride, const void *V,
+                                           int64_t v_stride, const int32_t *table, const int32_t *lengths,
+                                           const int32_t *starts, const void *Q, int64_t q_stride, void *Q_out,
+                                           int q_heads, const float *cos, const float *sin, int64_t positions,
+                                           int rotary_dim, int interleaved, void *stream)
+{
+    gemm_f16_status_t st = validate_cache(cache, batch, max_pages);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    const int D = cache->head_dim;
+    if (tokens < 0 || (!starts && tokens != batch) || !Q != !Q_out || (Q && q_heads < 1) || !cos != !sin ||
+        (interleaved != 0 && interleaved != 1))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (cos ? (positions < 0 || rotary_dim < 16 || rotary_dim > D || rotary_dim % 16 != 0) : rotary_dim != 0)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (tokens > GEMM_F16_Q4_MAX_TOKENS || (Q && q_heads > GEMM_F16_Q4_MAX_HEADS))
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
+    if (tokens == 0 || batch == 0)
+        return GEMM_F16_SUCCESS;
+    if (!K || !V || !lengths || (max_pages > 0 && !table))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (!rows_fit(k_stride, cache->heads, D) || !rows_fit(v_stride, cache->heads, D) || (Q && !rows_fit(q_stride, q_heads, D)))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (((uintptr_t)K | (uintptr_t)V | (uintptr_t)Q | (uintptr_t)Q_out) & 1u ||
+        ((uintptr_t)table | (uintptr_t)lengths | (uintptr_t)starts | (uintptr_t)cos | (uintptr_t)sin) & 3u)
+        return GEMM_F16_ERROR_MISALIGNED;
+    const int64_t width = (int64_t)cache->heads * D, q_width = (int64_t)q_heads * D, out_bytes = Q ? 2 * tokens * q_width : 0;
+    const int64_t k_bytes = rows_bytes(tokens, k_stride, width), v_bytes = rows_bytes(tokens, v_stride, width);
+    const bool in_place = Q && Q == Q_out && q_stride == q_width;
+    const int64_t turn_bytes = cos ? positions * (rotary_dim / 2) * 4 : 0;
+    if (!buffers_apart(cache) || overlaps_cache(K, k_bytes, cache) || overlaps_cache(V, v_bytes, cache) ||
+        overlaps_cache(Q_out, out_bytes, cache) || overlaps_cache(table, batch * max_pages * 4, cache) ||
+        overlaps_cache(lengths, batch * 4, cache) || (starts && overlaps_cache(starts, (batch + 1) * 4, cache)) ||
+        (Q && overlaps_cache(Q, rows_bytes(tokens, q_stride, q_width), cache)) || overlaps_cache(cos, turn_bytes, cache) ||
+        overlaps_cache(sin, turn_bytes, cache) || overlaps(Q_out, out_bytes, K, k_bytes) ||
+        overlaps(Q_out, out_bytes, V, v_bytes) || overlaps(Q_out, out_bytes, cos, turn_bytes) ||
+        overlaps(Q_out, out_bytes, sin, turn_bytes) || overlaps(Q_out, out_bytes, table, batch * max_pages * 4) ||
+        overlaps(Q_out, out_bytes, lengths, batch * 4) || (starts && overlaps(Q_out, out_bytes, starts, (batch + 1) * 4)) ||
+        (!in_place && Q && overlaps(Q_out, out_bytes, Q, rows_bytes(tokens, q_stride, q_width))))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    int dev = -1;
+    st = check_device(&dev);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    Q4AppendArgs a;
+    a.c = pages_of(cache, table, batch, max_pages);
+    a.K = (const _Float16 *)K;
+    a.V = (const _Float16 *)V;
+    a.Q = (const _Float16 *)Q;
+    a.Q_out = (_Float16 *)Q_out;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.q_stride = q_stride;
+    a.lengths = lengths;
+    a.starts = starts;
+    a.cos = cos;
+    a.sin = sin;
+    a.positions = positions;
+    a.tokens = (int)tokens;
+    a.q_heads = Q ? q_heads : 0;
+    a.rotary = rotary_dim;
+    a.interleaved = interleaved;
+    a.vec_k = rows_aligned(K, k_stride);
+    a.vec_v = rows_aligned(V, v_stride);
+    a.vec_q = rows_aligned(Q, q_stride);
+    a.vec_out = (uintptr_t)Q_out % 16 == 0;
+    return status_of(launch_q4_append(a, (hipStream_t)stream));
+}
+
+gemm_f16_status_t gemm_f16_q4_cache_read(const gemm_f16_q4_cache_t *cache, int64_t batch, int64_t tokens,
+                                         int64_t max_pages, const int32_t *table, const int32_t *first,
+                                         const int32_t *starts, void *K, void *V, void *stream)
+{
+    gemm_f16_status_t st = validate_cache(cache, batch, max_pages);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    if (tokens < 0)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (tokens > GEMM_F16_Q4_MAX_TOKENS)
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
+    if (tokens == 0 || batch == 0)
+        return GEMM_F16_SUCCESS;
+    if (!K || !V || !starts || (max_pages > 0 && !table))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (((uintptr_t)K | (uintptr_t)V) % 16 || ((uintptr_t)table | (uintptr_t)first | (uintptr_t)starts) & 3u)
+        return GEMM_F16_ERROR_MISALIGNED;
+    const int64_t bytes = 2 * tokens * cache->heads * cache->head_dim;
+    for (const void *out : {K, V})
+        if (overlaps_cache(out, bytes, cache) || overlaps(out, bytes, table, batch * max_pages * 4) ||
+            overlaps(out, bytes, starts, (batch + 1) * 4) || (first && overlaps(out, bytes, first, batch * 4)))
+            return GEMM_F16_ERROR_INVALID_VALUE;
+    if (overlaps(K, bytes, V, bytes))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    int dev = -1;
+    st = check_device(&dev);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    Q4ReadArgs a;
+    a.c = pages_of(cache, table, batch, max_pages);
+    a.first = first;
+    a.starts = starts;
+    a.K = (_Float16 *)K;
+    a.V = (_Float16 *)V;
+    a.tokens = (int)tokens;
+    return status_of(launch_q4_read(a, (hipStream_t)stream));
+}
+
+gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_t batch, int q_heads, int64_t max_pages,
+                                        const void *Q, int64_t q_stride, const int32_t *table, const int32_t *lengths,
+                                        float scale, void *out, int splits, int64_t max_length, void *workspace,
+                                        int64_t workspace_bytes, void *stream)
+{
+    gemm_f16_status_t st = validate_cache(cache, batch, max_pages);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    if (workspace_bytes < 0 || (!workspace && workspace_bytes != 0) || max_length < 0)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    const int64_t room = max_pages * cache->page_size;
+    gemm_f16_plan_t plan;
+    st = plan_attention(batch, q_heads, cache->heads, cache->head_dim, cache->group,
+                        max_length > 0 ? std::min(max_length, room) : room, splits, &plan);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    if (batch == 0)
+        return GEMM_F16_SUCCESS;
+    const int64_t width = (int64_t)q_heads * cache->head_dim;
+    if (!Q || !out || !lengths || (max_pages > 0 && !table) || (max_pages > 0 && cache->pages == 0) || q_stride < width)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (!rows_aligned(Q, q_stride) || (uintptr_t)out % 16 || ((uintptr_t)table | (uintptr_t)lengths) & 3u)
+        return GEMM_F16_ERROR_MISALIGNED;
+    const int64_t out_bytes = 2 * batch * width, q_bytes = rows_bytes(batch, q_stride, width);
+    if (overlaps(out, out_bytes, Q, q_bytes) || overlaps_cache(out, out_bytes, cache) ||
+        overlaps(out, out_bytes, table, batch * max_pages * 4) || overlaps(out, out_bytes, lengths, batch * 4))
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    if (plan.splits > 1) {
+        if (!workspace)
+            return GEMM_F16_ERROR_WORKSPACE;
+        if ((uintptr_t)workspace % 16)
+            return GEMM_F16_ERROR_MISALIGNED;
+        if (workspace_bytes < plan.workspace_bytes)
+            return GEMM_F16_ERROR_WORKSPACE;
+        const int64_t wb = plan.workspace_bytes;
+        if (overlaps(workspace, wb, Q, q_bytes) || overlaps(workspace, wb, out, out_bytes) ||
+            overlaps_cache(workspace, wb, cache) || overlaps(workspace, wb, table, batch * max_pages * 4) ||
+            overlaps(workspace, wb, lengths, batch * 4))
+            return GEMM_F16_ERROR_INVALID_VALUE;
+    }
+    int dev = -1;
+    st = check_device(&dev);
+    if (st != GEMM_F16_SUCCESS)
+        return st;
+    Q4AttentionArgs a;
+    a.c = pages_of(cache, table, batch, max_pages);
+    a.Q = (const _Float16 *)Q;
+    a.q_stride = q_stride;
+    a.lengths = lengths;
+    a.out = (_Float16 *)out;
+    a.parts = (float *)workspace;
+    a.scale = scale;
+    a.q_heads = q_heads;
+    a.ratio = q_heads / cache->heads;
+    a.row_tiles = (a.ratio + 15) / 16;
+    a.splits = plan.splits;
+    return status_of(launch_q4_attention(a, plan.grid, (hipStream_t)stream));
+}
+
+gemm_f16_status_t gemm_f16_plan_q4_attention(int64_t batch, int q_heads, int heads, int head_dim, int group,
+                                             int64_t max_length, int splits, gemm_f16_plan_t *plan)
+{
+    if (!plan)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    return plan_attention(batch, q_heads, heads, head_dim, group, max_length, splits, plan);
 }
 
 } // extern "C"

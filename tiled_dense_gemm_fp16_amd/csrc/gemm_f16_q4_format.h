@@ -40,6 +40,52 @@ hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *word
 hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float16 *W, int64_t N, int64_t K, int group,
                             bool vec, hipStream_t s);
 
+// The paged cache (include/gemm_f16_q4.h) as the kernels see it.
+struct Q4Pages {
+    uint32_t *k_codes, *k_words, *v_codes, *v_words;
+    int64_t pages;
+    int heads, page_size, head_dim, group;
+    const int32_t *table;     // batch x max_pages
+    int batch, max_pages;
+};
+
+struct Q4AppendArgs {
+    Q4Pages c;
+    const _Float16 *K, *V, *Q;
+    _Float16 *Q_out;
+    int64_t k_stride, v_stride, q_stride;
+    const int32_t *lengths, *starts;
+    const float *cos, *sin;
+    int64_t positions;
+    int tokens, q_heads, rotary, interleaved;
+    int vec_k, vec_v, vec_q, vec_out;   // rows are 16-byte aligned
+};
+hipError_t launch_q4_append(const Q4AppendArgs &a, hipStream_t s);
+
+struct Q4ReadArgs {
+    Q4Pages c;
+    const int32_t *first, *starts;
+    _Float16 *K, *V;
+    int tokens;
+};
+hipError_t launch_q4_read(const Q4ReadArgs &a, hipStream_t s);
+
+struct Q4AttentionArgs {
+    Q4Pages c;
+    const _Float16 *Q;
+    int64_t q_stride;
+    const int32_t *lengths;
+    _Float16 *out;
+    float *parts;             // splits > 1: batch x q_heads x splits x head_dim sums, then as many (max, sum) pairs
+    float scale;
+    int q_heads, ratio;       // query heads; query heads of a cache head
+    int row_tiles, splits;
+};
+constexpr int kQ4AttentionWaves = 4;
+constexpr int kQ4AttentionTokens = 32;   // a wave's step
+int64_t q4_attention_lds_bytes(int head_dim);
+hipError_t launch_q4_attention(const Q4AttentionArgs &a, int64_t grid, hipStream_t s);
+
 #ifdef __HIPCC__
 
 typedef _Float16 q4_half2 __attribute__((ext_vector_type(2)));
@@ -114,6 +160,75 @@ struct q4_rounder {
 
 // Position of value i of eight in a dword, in bits.
 __device__ __forceinline__ constexpr int q4_shift(int i) { return 4 * (i / 2 + 4 * (i & 1)); }
+
+// ---- the paged cache ---------------------------------------------------------------
+// Page of the granule of 8 tokens that holds position pos of sequence b, or -1
+// where the table or the pool has none.
+__device__ __forceinline__ int q4_page(const Q4Pages &c, int b, int64_t pos)
+{
+    const int64_t i = pos / c.page_size;
+    if (pos < 0 || i >= c.max_pages)
+        return -1;
+    const int id = c.table[(int64_t)b * c.max_pages + i];
+    return id >= 0 && id < c.pages ? id : -1;
+}
+
+// Work of an append or a read: a granule is 8 positions, a multiple of 8 on,
+// that one wave handles for one head (a dword of v_codes holds the 8 tokens
+// of one d, so nobody else may write it).  n rows of a sequence touch at most
+// n / 8 + 2 granules, so units starts[b] / 8 + 2 b up to the next sequence's
+// are enough for sequence b; the rest of them is empty.
+struct q4_granule {
+    int b, row, slot, count;   // sequence, first row, its slot in the granule, rows
+    int64_t pos;               // position of slot 0
+};
+
+__device__ __forceinline__ q4_granule q4_find(int64_t unit, const int32_t *starts, const int32_t *first, int tokens,
+                                              int batch)
+{
+    q4_granule r = {0, 0, 0, 0, 0};
+    int lo = 0, row0, rows;
+    int64_t local;
+    if (!starts) {             // one row for each sequence
+        lo = row0 = (int)unit;
+        rows = 1;
+        local = 0;
+    } else {
+        // the last sequence whose units begin at or before this one: 64 at a time
+        const int lane = threadIdx.x & 63;
+        for (int n = batch; n > 1;) {
+            const int step = (n + 63) / 64;
+            const bool before = lane * step < n && starts[lo + lane * step] / 8 + 2 * (int64_t)(lo + lane * step) <= unit;
+            const int k = __popcll(__ballot(before)) - 1;
+            if (k < 0)
+                return r;
+            n = min(step, n - k * step);
+            lo += k * step;
+        }
+        row0 = min(max(starts[lo], 0), tokens);
+        rows = min(max(starts[lo + 1], row0), tokens) - row0;
+        local = unit - (starts[lo] / 8 + 2 * (int64_t)lo);
+        if (local < 0)
+            return r;
+    }
+    const int64_t p0 = first ? first[lo] : 0, granule = (p0 >= 0 ? p0 / 8 : -((7 - p0) / 8)) + local;
+    const int64_t begin = p0 > granule * 8 ? p0 : granule * 8, end = p0 + rows < granule * 8 + 8 ? p0 + rows : granule * 8 + 8;
+    r.b = lo;
+    r.pos = granule * 8;
+    r.row = (int)(row0 + (begin - p0));
+    r.slot = (int)(begin - granule * 8);
+    r.count = begin < end ? (int)(end - begin) : 0;
+    return r;
+}
+
+// Place of the dword of d = 8 c .. 8 c + 7 in a token's row of k_codes.
+template <int D>
+__device__ __forceinline__ int q4_key_dword(int c)
+{
+    constexpr int B = D < 128 ? D : 128;
+    const int in = c % (B / 8);
+    return c / (B / 8) * (B / 8) + in % 4 * (B / 32) + in / 4;
+}
 
 #endif // __HIPCC__
 
