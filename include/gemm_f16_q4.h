@@ -68,17 +68,24 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
  * row-major and W held as (codes, words).  Meant for few rows (M = 1 is one
  * token through a layer: each code is read once) and right for any M >= 0.
  * A and C need 2-byte alignment, codes and words 16-byte; C overlaps none of
- * them.  K = 0 writes +0.  config: GEMM_F16_CONFIG_AUTO or an index below
- * gemm_f16_q4_num_configs(); every configuration runs every shape.
- * Limits: M <= GEMM_F16_MAX_DIM, N and K as gemm_f16.
+ * them.  K = 0 writes +0.  Limits: M <= GEMM_F16_MAX_DIM, N and K as gemm_f16.
+ *   config : GEMM_F16_CONFIG_AUTO or an index below gemm_f16_q4_num_configs().
+ *            The tile configurations (block_m of 64 and 128 with direct_lds 1)
+ *            need A's rows 4-byte aligned (K even), the others nothing.  The
+ *            last one rounds each weight to binary16 (the value
+ *            gemm_f16_q4_expand gives) before the product; all others use
+ *            it exactly.  AUTO takes it for many rows.
+ *   splits, workspace, workspace_bytes : as gemm_f16_split (tile
+ *            configurations only; splits 1 needs no workspace).
  */
 gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, const void *codes,
-                              const void *words, void *C, float alpha, int epilogue, int config, void *stream);
+                              const void *words, void *C, float alpha, int epilogue, int config, int splits,
+                              void *workspace, int64_t workspace_bytes, void *stream);
 
-/* How that call would run (no HIP call).  block_k is the k of one step of a
- * wave, k_tiles the steps of all of K; flops 2 M N K; min_bytes the codes and
- * words, A and C once. */
-gemm_f16_status_t gemm_f16_plan_q4(int64_t M, int64_t N, int64_t K, int group, int config,
+/* How that call would run (no HIP call; A only for its alignment, NULL for an
+ * aligned one).  block_k is the k of one step, k_tiles the steps of a split;
+ * flops 2 M N K; min_bytes the codes and words, A and C once. */
+gemm_f16_status_t gemm_f16_plan_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, int config, int splits,
                                    gemm_f16_plan_t *plan);
 
 int gemm_f16_q4_num_configs(void);

@@ -9,7 +9,10 @@ most 32 additions inside one matrix instruction, at most 3 further ones of its
 group, one per group of its wave's share of K, 8 across the waves, and the
 products with s and alpha: D = 32 + 3 + K / group + 8 + 2 roundings, each of at
 most 2^-23 of the sum of magnitudes (2^-24 for a rounding to nearest, twice
-that in case the matrix unit truncates).
+that in case the matrix unit truncates).  (A split adds fewer than it takes
+off a wave's share.)  The configuration that rounds the weights to binary16
+adds half a step of each: 2^-11 of the sum of magnitudes (no weight here is
+below binary16's normals).
 """
 import numpy as np
 import pytest
@@ -31,9 +34,9 @@ def weights(n, k, seed):
     return (torch.randn(n, k, generator=gen(seed)) * (1.0 + torch.rand(n, 1, generator=gen(seed + 1)))).to(torch.float16)
 
 
-def bound(c, size, k, group):
+def bound(c, size, k, group, rounded=False):
     depth = 45 + -(-k // group)
-    return ref.half_steps(c) * (1 + 2.0 ** -10) + depth * 2.0 ** -23 * size
+    return ref.half_steps(c) * (1 + 2.0 ** -10) + (depth * 2.0 ** -23 + (2.0 ** -11 if rounded else 0.0)) * size
 
 
 @pytest.mark.parametrize("group", [32, 64, 128])
@@ -90,7 +93,10 @@ def test_compress_unaligned_source():
     assert bool((out[:1] == 7).all()) and bool((out[-2:] == 7).all())
 
 
-def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shift=0, seed=0):
+ROUNDED = g.q4_num_configs() - 1      # the configuration that rounds the weights
+
+
+def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shift=0, seed=0, splits=None):
     a = torch.randn(m, k, generator=gen(seed + 5)).to(torch.float16)
     packed = g.q4_compress(weights(n, k, seed).to(DEV), group)
     room = torch.full((m * n + 2 * 64 + shift,), 9.0, dtype=torch.float16, device=DEV)
@@ -98,13 +104,15 @@ def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shif
     buf = torch.empty(m * k + shift, dtype=torch.float16, device=DEV)
     ad = buf[shift:].view(m, k)
     ad.copy_(a)
-    got = g.gemm_q4(ad, packed, epilogue=epilogue, out=out, config=config, alpha=alpha)
+    got = g.gemm_q4(ad, packed, epilogue=epilogue, out=out, config=config, alpha=alpha, splits=splits)
     torch.cuda.synchronize()
     print(f"[q4] product {m}x{n}x{k} group={group} config={config} epi={epilogue} alpha={alpha} shift={shift}", flush=True)
     w = ref.unpack_weights(ref.host(packed.codes), ref.host(packed.words), n, k, group)
     want, size = ref.product(a.double().numpy(), w, float(np.float32(alpha)), epilogue == "relu")
     err = np.abs(ref.host(got).astype(np.float64) - want)
-    assert (err <= bound(want, size, k, group)).all(), (err / bound(want, size, k, group)).max()
+    chosen = g.plan_q4(m, n, k, group, config, splits, ad.data_ptr())["config"]
+    tol = bound(want, size, k, group, chosen == ROUNDED)
+    assert (err <= tol).all(), (err / tol).max()
     assert bool((room[:64 + shift] == 9).all()) and bool((room[64 + shift + m * n:] == 9).all())
 
 
@@ -113,10 +121,37 @@ def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shif
 @pytest.mark.parametrize("m,n,k", [(1, 1, 1), (1, 16, 128), (1, 100, 2048), (3, 33, 1000), (16, 16, 1024), (17, 70, 1030),
                                    (33, 48, 520), (64, 64, 256), (65, 40, 4100), (130, 264, 136)])
 def test_every_config(config, group, m, n, k):
+    if k % 2 and g.plan_q4(m, n, k + 1, group, config=config)["direct_lds"]:
+        with pytest.raises(g.GemmError):                # rows of odd length: not for the tile configurations
+            check(m, n, k, group, config=config)
+        return
     check(m, n, k, group, config=config, seed=m + n + k)
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 1024, 1024), (2, 5000, 4100), (13, 256, 8192), (40, 600, 3000), (300, 300, 300)])
+@pytest.mark.parametrize("config", [c for c in range(g.q4_num_configs()) if g.plan_q4(64, 64, 128, config=c)["direct_lds"]])
+@pytest.mark.parametrize("m,n,k,splits", [(1, 16, 384, 3), (70, 140, 1030, 2), (64, 128, 4100, 7), (130, 300, 2048, 64),
+                                          (129, 257, 132, 2), (300, 520, 514, None)])
+def test_splits(config, m, n, k, splits):
+    check(m, n, k, 32, config=config, splits=splits, epilogue="relu", alpha=0.7)
+    check(m, n, k, 128, config=config, splits=splits)
+
+
+@pytest.mark.parametrize("config", range(g.q4_num_configs()))
+def test_last_chunk_keeps_to_its_row(config):
+    # infinities at the start of every row: the row before ends inside a 16-byte chunk that holds them
+    for k in (130, 132, 262, 646):
+        a = torch.randn(70, k, generator=gen(k)).to(torch.float16)
+        a[1::2, 0] = float("inf")
+        packed = g.q4_compress(weights(48, k, k).to(DEV), 64)
+        got = ref.host(g.gemm_q4(a.to(DEV), packed, config=config)).astype(np.float64)
+        w = ref.unpack_weights(ref.host(packed.codes), ref.host(packed.words), 48, k, 64)
+        want, size = ref.product(a[::2].double().numpy(), w)
+        assert (np.abs(got[::2] - want) <= bound(want, size, k, 64, config == ROUNDED)).all()
+        assert not np.isfinite(got[1::2]).any() or (w[:, 0] == 0).any()
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1024, 1024), (2, 5000, 4100), (13, 256, 8192), (40, 600, 3000), (300, 300, 300),
+                                   (70, 64, 9000), (520, 700, 1000)])
 @pytest.mark.parametrize("epilogue,alpha", [("none", 1.0), ("relu", 0.125), ("none", -1.7)])
 def test_automatic_choice(m, n, k, epilogue, alpha):
     check(m, n, k, 64, epilogue=epilogue, alpha=alpha)
@@ -125,6 +160,7 @@ def test_automatic_choice(m, n, k, epilogue, alpha):
 def test_unaligned_pointers():
     check(5, 40, 264, 32, shift=1)
     check(20, 40, 264, 128, shift=3)
+    check(33, 40, 261, 64, shift=1)
 
 
 def test_long_k():

@@ -53,8 +53,9 @@ def test_buffer_sizes():
 def test_product_refusals():
     h = g.lib()
 
-    def call(m=4, n=32, k=256, group=64, a=at(0), codes=at(1), words=at(2), c=at(3), epi=0, config=-1):
-        return h.gemm_f16_q4(m, n, k, group, a, codes, words, c, 1.0, epi, config, None)
+    def call(m=4, n=32, k=256, group=64, a=at(0), codes=at(1), words=at(2), c=at(3), epi=0, config=-1,
+             splits=1, ws=None, size=0):
+        return h.gemm_f16_q4(m, n, k, group, a, codes, words, c, 1.0, epi, config, splits, ws, size, None)
 
     for bad in (dict(m=-1), dict(n=-1), dict(k=-1), dict(group=16), dict(group=0), dict(a=None), dict(codes=None),
                 dict(words=None), dict(c=None), dict(epi=2), dict(epi=-1), dict(config=g.q4_num_configs()), dict(config=-2),
@@ -64,6 +65,22 @@ def test_product_refusals():
         assert call(**bad) == MISALIGNED, bad
     for bad in (dict(m=1 << 31), dict(n=(1 << 22) + 1), dict(k=(1 << 22) + 1)):
         assert call(**bad) == SIZE, bad
+    # the tile configurations: A's rows 4-byte aligned, and a workspace for a split
+    tile = [c for c in range(g.q4_num_configs()) if g.plan_q4(64, 32, 4096, 64, config=c)["direct_lds"]]
+    assert tile
+    for c in range(g.q4_num_configs()):
+        if c in tile:
+            assert call(config=c, a=at(0) + 2) == INVALID and call(config=c, k=255) == INVALID
+            need = g.plan_q4(4, 32, 4096, 64, config=c, splits=3)["workspace_bytes"]
+            assert need == 3 * 4 * 32 * 4
+            assert call(config=c, k=4096, splits=3) == 7
+            assert call(config=c, k=4096, splits=3, ws=at(4), size=need - 1) == 7
+            assert call(config=c, k=4096, splits=3, ws=at(4) + 8, size=need) == MISALIGNED
+            for p in (at(0), at(1), at(2), at(3)):
+                assert call(config=c, k=4096, splits=3, ws=p, size=need) == INVALID
+        else:
+            assert call(config=c, splits=2, k=4096, ws=at(4), size=1 << 20) == INVALID
+    assert call(splits=-1) == INVALID and call(splits=65) == INVALID and call(ws=None, size=8) == INVALID
     assert call(m=0, a=None, c=None) == 0 and call(n=0, codes=None, words=None, c=None) == 0
     if not torch.cuda.is_available():
         assert call() == NO_DEVICE and call(c=at(0) + 2 * 4 * 256) == NO_DEVICE
@@ -88,9 +105,15 @@ def test_plans():
         assert g.q4_config_name(c)
         for m, n, k in [(1, 16, 128), (5, 1000, 4100), (64, 8192, 8192), (2048, 5000, 300), (1, 1, 1 << 22)]:
             p = g.plan_q4(m, n, k, 64, config=c)
-            assert p["config"] == c and p["lds_bytes"] <= 163840 and p["threads"] <= 1024
+            assert p["config"] == c and p["splits"] == 1 and p["workspace_bytes"] == 0 and p["lds_bytes"] <= 163840 and p["threads"] <= 1024
             assert p["tiles_m"] * p["block_m"] >= m and p["tiles_n"] * p["block_n"] >= n
             assert p["flops"] == 2.0 * m * n * k
+    for m in (1, 16, 17, 33, 100, 300, 5000):
+        for n, k in [(16, 128), (1000, 4100), (8192, 8192), (64, 100000)]:
+            p = g.plan_q4(m, n, k, 64, splits=None)
+            assert p["splits"] * p["k_split"] >= k and (p["splits"] - 1) * p["k_split"] < k
+            assert p["workspace_bytes"] == (p["splits"] * m * n * 4 if p["splits"] > 1 else 0)
+            assert g.plan_q4(m, n, k, 64, splits=None, A_ptr=2)["direct_lds"] == 0
     assert g.q4_config_name(-1) is None and g.q4_config_name(g.q4_num_configs()) is None
     for bad in (dict(m=-1), dict(group=31), dict(k=1 << 23), dict(config=99)):
         with pytest.raises(g.GemmError):

@@ -79,8 +79,8 @@ Q4_SIGNATURES = {
     "gemm_f16_q4_words_bytes": ([_i64, _i64, _int], _i64),
     "gemm_f16_q4_compress": ([_i64, _i64, _int, _int, _vp, _vp, _vp, _vp], _int),
     "gemm_f16_q4_expand": ([_i64, _i64, _int, _vp, _vp, _vp, _vp], _int),
-    "gemm_f16_q4": ([_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _f32, _int, _int, _vp], _int),
-    "gemm_f16_plan_q4": ([_i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)], _int),
+    "gemm_f16_q4": ([_i64, _i64, _i64, _int, _vp, _vp, _vp, _vp, _f32, _int, _int, _int, _vp, _i64, _vp], _int),
+    "gemm_f16_plan_q4": ([_i64, _i64, _i64, _int, _vp, _int, _int, ctypes.POINTER(Plan)], _int),
     "gemm_f16_q4_cache_append": ([_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _int, _vp, _vp,
                                   _i64, _int, _int, _vp], _int),
     "gemm_f16_q4_cache_read": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _vp], _int),

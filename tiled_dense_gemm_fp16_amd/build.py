@@ -16,7 +16,7 @@ OBJDIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgemm_f16.so")
 SOURCES = [os.path.join(CSRC, f) for f in (
     "gemm_f16_api.cpp", "gemm_f16_kernels.hip", "gemm_f16_nn.hip", "gemm_f16_nt.hip", "gemm_f16_tn.hip",
-    "gemm_f16_tt.hip", "gemm_f16_sparse.hip", "gemm_f16_q4_api.cpp", "gemm_f16_q4_weights.hip",
+    "gemm_f16_tt.hip", "gemm_f16_sparse.hip", "gemm_f16_q4_api.cpp", "gemm_f16_q4_weights.hip", "gemm_f16_q4_tile.hip",
     "gemm_f16_q4_cache.hip", "gemm_f16_q4_attention.hip")]
 # what each kind of source includes (for incremental builds)
 HOST_DEPS = [os.path.join(CSRC, f) for f in ("gemm_f16_internal.h", "gemm_f16_tuned.inc", "gemm_f16_q4_format.h")] + \

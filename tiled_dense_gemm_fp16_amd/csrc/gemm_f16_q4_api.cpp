@@ -12,6 +12,25 @@
 #include "gemm_f16_q4_format.h"
 
 namespace gemm_f16_impl {
+
+const Q4Config kQ4Configs[kNumQ4Configs] = {
+    {"q4_16x16_w8", 1, 1, 8, 0},
+    {"q4_16x32_w8", 1, 2, 8, 0},
+    {"q4_32x32_w8", 2, 2, 8, 0},
+    {"q4_64x32_w8", 4, 2, 8, 0},
+    {"q4_64x128_s4", 4, 8, 4, 4},
+    {"q4_128x256_s3", 8, 16, 4, 3},
+};
+
+int64_t q4_lds_bytes(const Q4Config &c, int group)
+{
+    if (c.stages == 0)
+        return (int64_t)c.waves * c.m_blocks * c.n_blocks * 1024;
+    const int64_t word_loads = (c.n_blocks / c.waves * (128 / group) + 3) / 4;
+    return std::max<int64_t>(c.stages * (c.m_blocks * 4096 + c.n_blocks * 1024 + c.waves * word_loads * 256),
+                             16 * c.m_blocks * (16 * c.n_blocks + 8) * 2);
+}
+
 namespace {
 
 bool known_group(int group) { return group == 32 || group == 64 || group == 128; }
@@ -32,34 +51,54 @@ gemm_f16_status_t validate_weights(int64_t N, int64_t K, int group, const void *
     return GEMM_F16_SUCCESS;
 }
 
-gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, int config, gemm_f16_plan_t *p)
+// Whether the tile kernels' direct loads can read A's rows.
+bool rows_4_aligned(const void *A, int64_t K) { return (uintptr_t)A % 4 == 0 && K % 2 == 0; }
+
+gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool aligned, int config, int splits,
+                            gemm_f16_plan_t *p)
 {
-    if (config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumQ4Configs))
+    if ((config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumQ4Configs)) || splits < 0 ||
+        splits > GEMM_F16_MAX_SPLITS)
         return GEMM_F16_ERROR_INVALID_VALUE;
-    const int c = config != GEMM_F16_CONFIG_AUTO ? config : M <= 16 ? 0 : M <= 32 ? 1 : 2;
+    int c = config;
+    if (c == GEMM_F16_CONFIG_AUTO)
+        c = M <= 16 ? (N <= 8192 ? 0 : 1) : !aligned ? (M <= 32 ? 2 : 3) : M <= 256 ? 4 : 5;
     const Q4Config &d = kQ4Configs[c];
+    if (d.stages > 0 && !aligned)
+        return GEMM_F16_ERROR_INVALID_VALUE;
     memset(p, 0, sizeof(*p));
     p->config = c;
     p->block_m = 16 * d.m_blocks;
     p->block_n = 16 * d.n_blocks;
     p->block_k = 128;
-    p->stages = 1;
+    p->stages = d.stages > 0 ? d.stages : 1;
     p->threads = 64 * d.waves;
-    p->vec_a = 8;
+    p->direct_lds = d.stages > 0;
+    p->vec_a = d.stages > 0 ? 2 : 1;
     p->vec_b = 32;
-    p->vec_c = 1;
+    p->vec_c = 8;
     p->tiles_m = (M + p->block_m - 1) / p->block_m;
     p->tiles_n = (N + p->block_n - 1) / p->block_n;
-    p->grid = p->tiles_m * p->tiles_n;
-    p->k_tiles = (K + 127) / 128;
-    p->lds_bytes = M > 0 ? q4_lds_bytes(d, M, q4_chunk(d, M, K)) : 0;
+    const int64_t blocks = (K + 127) / 128, tiles = p->tiles_m * p->tiles_n;
+    if (splits == GEMM_F16_SPLITS_AUTO) {
+        splits = 1;
+        if (d.stages > 0 && tiles > 0 && tiles < 256)   // a split keeps at least 8 blocks, as long as CUs are left
+            splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / 8), GEMM_F16_MAX_SPLITS));
+    }
+    if (splits > 1 && d.stages == 0)
+        return GEMM_F16_ERROR_INVALID_VALUE;
+    const int64_t per = blocks > 0 ? (blocks + splits - 1) / splits : 0;
+    p->splits = per > 0 ? (int)((blocks + per - 1) / per) : 1;   // none empty
+    p->grid = tiles * p->splits;
+    p->k_tiles = per;
+    p->k_split = p->splits > 1 ? per * 128 : K;
+    p->lds_bytes = q4_lds_bytes(d, group);
     p->flops = 2.0 * (double)M * (double)N * (double)K;
     p->min_bytes = 0.5 * (double)N * (double)K + 4.0 * (double)N * (double)((K + group - 1) / group) +
                    2.0 * (double)M * ((double)N + (double)K);
     p->trans_b = 1;
-    p->splits = 1;
-    p->k_split = K;
-    return GEMM_F16_SUCCESS;
+    p->workspace_bytes = p->splits > 1 ? (int64_t)p->splits * M * N * 4 : 0;
+    return p->grid > 0x7fffffff ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
 }
 
 // The cache's description and the page table's shape.
@@ -210,7 +249,7 @@ gemm_f16_status_t gemm_f16_q4_compress(int64_t N, int64_t K, int group, int symm
     if (st != GEMM_F16_SUCCESS)
         return st;
     return status_of(launch_q4_compress((const _Float16 *)W, (uint32_t *)codes, (uint32_t *)words, N, K, group,
-                                        symmetric != 0, K % 8 == 0 && (uintptr_t)W % 16 == 0, (hipStream_t)stream));
+                                        symmetric != 0, (hipStream_t)stream));
 }
 
 gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void *codes, const void *words, void *W,
@@ -233,16 +272,18 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
     if (st != GEMM_F16_SUCCESS)
         return st;
     return status_of(launch_q4_expand((const uint32_t *)codes, (const uint32_t *)words, (_Float16 *)W, N, K, group,
-                                      K % 8 == 0 && (uintptr_t)W % 16 == 0, (hipStream_t)stream));
+                                      (hipStream_t)stream));
 }
 
 gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, const void *codes,
-                              const void *words, void *C, float alpha, int epilogue, int config, void *stream)
+                              const void *words, void *C, float alpha, int epilogue, int config, int splits,
+                              void *workspace, int64_t workspace_bytes, void *stream)
 {
     gemm_f16_status_t st = validate_weights(N, K, group, codes, words);
     if (st != GEMM_F16_SUCCESS)
         return st;
-    if (M < 0 || (epilogue != GEMM_F16_EPILOGUE_NONE && epilogue != GEMM_F16_EPILOGUE_RELU))
+    if (M < 0 || (epilogue != GEMM_F16_EPILOGUE_NONE && epilogue != GEMM_F16_EPILOGUE_RELU) || workspace_bytes < 0 ||
+        (!workspace && workspace_bytes != 0))
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (M > GEMM_F16_MAX_DIM)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
@@ -254,11 +295,24 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
         overlaps(C, 2 * M * N, words, gemm_f16_q4_words_bytes(N, K, group)))
         return GEMM_F16_ERROR_INVALID_VALUE;
     gemm_f16_plan_t plan;
-    st = make_plan(M, N, K, group, config, &plan);
+    st = make_plan(M, N, K, group, rows_4_aligned(A, K), config, splits, &plan);
     if (st != GEMM_F16_SUCCESS)
         return st;
     if (M == 0 || N == 0)
         return GEMM_F16_SUCCESS;
+    if (plan.splits > 1) {
+        if (!workspace)
+            return GEMM_F16_ERROR_WORKSPACE;
+        if ((uintptr_t)workspace % 16)
+            return GEMM_F16_ERROR_MISALIGNED;
+        if (workspace_bytes < plan.workspace_bytes)
+            return GEMM_F16_ERROR_WORKSPACE;
+        const int64_t wb = plan.workspace_bytes;
+        if (overlaps(workspace, wb, A, 2 * M * K) || overlaps(workspace, wb, C, 2 * M * N) ||
+            overlaps(workspace, wb, codes, gemm_f16_q4_codes_bytes(N, K)) ||
+            overlaps(workspace, wb, words, gemm_f16_q4_words_bytes(N, K, group)))
+            return GEMM_F16_ERROR_INVALID_VALUE;
+    }
     int dev = -1;
     st = check_device(&dev);
     if (st != GEMM_F16_SUCCESS)
@@ -273,20 +327,29 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     a.K = (int)K;
     a.n_blocks = (int)((N + 15) / 16);
     a.k_blocks = (int)((K + 127) / 128);
-    a.chunk = q4_chunk(kQ4Configs[plan.config], M, K);
-    a.vec_a = K % 8 == 0 && (uintptr_t)A % 16 == 0;
+    a.tiles_m = (int)plan.tiles_m;
+    a.tiles_n = (int)plan.tiles_n;
+    a.split_blocks = (int)plan.k_tiles;
+    a.W = plan.splits > 1 ? (float *)workspace : nullptr;
     a.alpha = K == 0 ? 1.0f : alpha;   // the empty sum is +0 whatever alpha
     a.relu = epilogue == GEMM_F16_EPILOGUE_RELU ? 1 : 0;
-    return status_of(launch_q4(plan.config, group, a, plan.tiles_n, plan.tiles_m, (hipStream_t)stream));
+    if (kQ4Configs[plan.config].stages == 0)
+        return status_of(launch_q4(plan.config, group, a, (hipStream_t)stream));
+    const hipError_t e = launch_q4_tile(plan.config, group, a, plan.grid, (hipStream_t)stream);
+    if (e != hipSuccess || plan.splits == 1)
+        return status_of(e);
+    return status_of(launch_reduce(a.W, a.C, M, N, plan.splits, a.alpha, a.relu, N % 4 == 0 && (uintptr_t)C % 8 == 0,
+                                   (hipStream_t)stream));
 }
 
-gemm_f16_status_t gemm_f16_plan_q4(int64_t M, int64_t N, int64_t K, int group, int config, gemm_f16_plan_t *plan)
+gemm_f16_status_t gemm_f16_plan_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, int config, int splits,
+                                   gemm_f16_plan_t *plan)
 {
     if (!plan || M < 0 || N < 0 || K < 0 || !known_group(group))
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (M > GEMM_F16_MAX_DIM || N > GEMM_F16_MAX_N || K > GEMM_F16_MAX_K)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
-    return make_plan(M, N, K, group, config, plan);
+    return make_plan(M, N, K, group, rows_4_aligned(A, K), config, splits, plan);
 }
 
 int gemm_f16_q4_num_configs(void) { return kNumQ4Configs; }

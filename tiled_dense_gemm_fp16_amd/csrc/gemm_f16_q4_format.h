@@ -17,8 +17,9 @@ struct Q4Args {
     _Float16 *C;             // M x N
     int M, N, K;
     int n_blocks, k_blocks;  // tiles of 16 rows of W, of 128 k
-    int chunk;               // k staged in LDS at a time, a multiple of 128 waves
-    int vec_a;               // A's rows are 16-byte aligned
+    int tiles_m, tiles_n;    // workgroups
+    int split_blocks;        // tile kernels: k blocks of a split
+    float *W;                // a split's partial sums, splits x M x N; null: unsplit
     float alpha;
     int relu;
 };
@@ -27,18 +28,21 @@ struct Q4Config {
     const char *name;
     int m_blocks;            // rows of A of a workgroup, in 16s
     int n_blocks;            // rows of W of a workgroup, in 16s
-    int waves;               // they share the workgroup's k blocks in turn
+    int waves;
+    int stages;              // LDS stages of a tile kernel, each of 128 k; 0: the kernel for few rows
 };
-constexpr int kNumQ4Configs = 3;
+constexpr int kNumQ4Configs = 6;
 extern const Q4Config kQ4Configs[kNumQ4Configs];
 
-int64_t q4_lds_bytes(const Q4Config &c, int64_t M, int chunk);
-int q4_chunk(const Q4Config &c, int64_t M, int64_t K);
-hipError_t launch_q4(int config, int group, const Q4Args &a, int64_t grid_n, int64_t grid_m, hipStream_t s);
+int64_t q4_lds_bytes(const Q4Config &c, int group);
+// The kernel for few rows: tiles_n x tiles_m workgroups.
+hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s);
+// Tile kernels: tiles_m x tiles_n x splits workgroups; A's rows 4-byte aligned.
+hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s);
 hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *words, int64_t N, int64_t K, int group,
-                              bool symmetric, bool vec, hipStream_t s);
+                              bool symmetric, hipStream_t s);
 hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float16 *W, int64_t N, int64_t K, int group,
-                            bool vec, hipStream_t s);
+                            hipStream_t s);
 
 // The paged cache (include/gemm_f16_q4.h) as the kernels see it.
 struct Q4Pages {

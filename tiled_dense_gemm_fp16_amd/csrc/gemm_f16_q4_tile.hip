@@ -1,0 +1,302 @@
+// gemm_f16_q4_tile.hip -- the product with 4-bit weights, C = epi(alpha A W^T),
+// for more rows of A than one matrix instruction takes: LDS-staged tiles.
+//
+// A workgroup of 4 waves owns 16 MB rows of A and 64 NW rows of W.  A stage
+// holds 128 k: A's rows (256 bytes each), the waves' tiles of codes (1 KiB for
+// each 16 rows of W) and their words, all moved straight from memory to LDS by
+// buffer_load ... lds, STAGES - 1 stages ahead, with one barrier a stage.
+// Every wave multiplies all of A's rows by its own 16 NW rows of W, so codes
+// are unpacked once in a workgroup, and A is read from memory once.
+//
+// A's rows lie in LDS as 16 chunks of 16 bytes, chunk c of row r in place
+// c ^ (r & 15): a fragment read takes one chunk of 16 rows, which then lie in
+// 16 different 16-byte slots of the 256-byte bank window.  The lanes of a
+// direct load fill LDS in order, so the permutation is made by the global
+// address each lane loads.
+//
+// Scales.  With ROUND false the products of a group are summed in fp32 and
+// enter the total times the scale, as in the kernel for few rows: one fused
+// multiply-add per output and group.  With ROUND true the scale multiplies
+// q - z in binary16 (one rounding of the weight, to the value that q4_expand
+// gives) and the matrix cores add up everything: for many rows that
+// multiply-add costs more than it gives, since the weight's rounding is of
+// the size of the result's own (2^-11 of each weight, at random signs).
+#include "gemm_f16_q4_format.h"
+#include "gemm_f16_tile.h"
+
+namespace gemm_f16_impl {
+
+typedef _Float16 half8_any __attribute__((ext_vector_type(8), aligned(2)));
+
+template <int GROUP, int MB, int NW, int STAGES, bool ROUND>
+struct Q4Tile {
+    static constexpr int WAVES = 4, GROUPS = 128 / GROUP, PER = GROUP / 32;
+    static constexpr int BM = 16 * MB, BN = 16 * NW * WAVES;
+    static constexpr int A_BYTES = BM * 256, CODE_BYTES = WAVES * NW * 1024;
+    static constexpr int WORD_LOADS = (NW * GROUPS + 3) / 4;   // of 64 words, for each wave
+    static constexpr int STAGE_BYTES = A_BYTES + CODE_BYTES + WAVES * WORD_LOADS * 256;
+    static constexpr int LOADS = MB + NW + WORD_LOADS;         // of a stage, for each wave
+    static constexpr int PITCH = BN + 8;                       // of the staged output, in halves
+    static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > BM * PITCH * 2 ? STAGES * STAGE_BYTES : BM * PITCH * 2;
+    static_assert(LDS_BYTES <= 163840, "LDS of a CU");
+};
+
+// A pointer that every lane of the wave has alike, in scalar registers.
+__device__ __forceinline__ const uint32_t *uniform_pointer(const uint32_t *p)
+{
+    const uint64_t v = (uint64_t)p;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
+    return reinterpret_cast<const uint32_t *>((uint64_t)hi << 32 | lo);
+}
+
+// One stage's loads of a wave.
+template <class T, int MB, int NW>
+struct Q4Loads {
+    __amdgpu_buffer_rsrc_t a, codes, words;
+    uint32_t a_off[MB];       // row and chunk of each load of A
+    int chunk[MB];
+    uint32_t code_off[NW], word_off[T::WORD_LOADS];
+    int wave, lane, K, kb_end;
+
+    __device__ __forceinline__ void init(const Q4Args &p, int m0, int nb0, int end)
+    {
+        lane = threadIdx.x & 63;
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        K = p.K;
+        kb_end = end;
+        const int rows = min(p.M - m0, T::BM);
+        a = make_rsrc(p.A + (int64_t)m0 * p.K, (uint32_t)rows * (uint32_t)p.K * 2u);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const int row = 4 * (wave + T::WAVES * i) + lane / 16;
+            chunk[i] = (lane & 15) ^ (row & 15);
+            a_off[i] = (uint32_t)row * (uint32_t)p.K * 2u + (uint32_t)chunk[i] * 16u;
+        }
+        const int nb = nb0 + wave * NW;
+        const int here = __builtin_amdgcn_readfirstlane(max(0, min(NW, p.n_blocks - nb)));   // past N: nothing is read
+        const int64_t tile = (int64_t)min(nb, p.n_blocks - 1) * p.k_blocks;
+        codes = make_rsrc(uniform_pointer(p.codes + tile * 256), (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
+        words = make_rsrc(uniform_pointer(p.words + tile * (16 * T::GROUPS)), (uint32_t)here * (uint32_t)p.k_blocks * (64u * T::GROUPS));
+#pragma unroll
+        for (int i = 0; i < NW; ++i)
+            code_off[i] = (uint32_t)i * (uint32_t)p.k_blocks * 1024u + (uint32_t)lane * 16u;
+#pragma unroll
+        for (int i = 0; i < T::WORD_LOADS; ++i) {
+            const int w = 64 * i + lane, nw = w / (16 * T::GROUPS);
+            word_off[i] = (nw < NW ? (uint32_t)nw * (uint32_t)p.k_blocks * (64u * T::GROUPS) : 0x80000000u) +
+                          (uint32_t)(w % (16 * T::GROUPS)) * 4u;
+        }
+    }
+
+    // block kb into the stage at `to`; blocks past the range bring zeros
+    __device__ __forceinline__ void issue(int kb, unsigned char *to) const
+    {
+        const uint32_t gone = oob_unless(kb < kb_end);
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            LDS_AS void *d = (LDS_AS void *)(to + (wave + T::WAVES * i) * 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(a, d, 16, a_off[i] | gone | oob_unless(kb * 128 + chunk[i] * 8 < K),
+                                                     (uint32_t)kb * 256u, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < NW; ++i) {
+            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + (wave * NW + i) * 1024);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(codes, d, 16, code_off[i] | gone, (uint32_t)kb * 1024u, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < T::WORD_LOADS; ++i) {
+            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + T::CODE_BYTES + (wave * T::WORD_LOADS + i) * 256);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(words, d, 4, word_off[i] | gone, (uint32_t)kb * (64u * T::GROUPS), 0, 0);
+        }
+    }
+
+    // clear what the chunk that straddles the end of a row brought of the next row
+    __device__ __forceinline__ void clear_tail(unsigned char *stage) const
+    {
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+            if (chunk[i] == K % 128 / 8) {
+                unsigned char *c = stage + (wave + T::WAVES * i) * 1024 + lane * 16;
+                for (int e = K % 8; e < 8; e += 2)
+                    *reinterpret_cast<uint32_t *>(c + 2 * e) = 0u;
+            }
+    }
+};
+
+template <int GROUP, int MB, int NW, int STAGES, bool ROUND>
+__global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
+{
+    typedef Q4Tile<GROUP, MB, NW, STAGES, ROUND> T;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
+    int tm, tn, split;
+    tile_coords(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, 4, tm, tn, split);
+    const int m0 = tm * T::BM, nb0 = tn * (NW * T::WAVES);
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int begin = split * p.split_blocks, end = min(p.k_blocks, begin + p.split_blocks);
+
+    Q4Loads<T, MB, NW> in;
+    in.init(p, m0, nb0, end);
+    const int wave = in.wave;
+
+    float4v acc[MB][NW];
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+        for (int nw = 0; nw < NW; ++nw)
+            acc[mb][nw] = float4v{0, 0, 0, 0};
+
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        in.issue(begin + s, lds + s * T::STAGE_BYTES);
+
+    // One stage: request block kb into `fill`, multiply the one in `from`.
+    // (restrict: the stage being filled is not the one being read, so the
+    // reads need not wait for the loads.)
+    const auto step = [&](const unsigned char *__restrict__ from, unsigned char *__restrict__ fill, int kb)
+                          __attribute__((always_inline)) {
+        in.issue(kb, fill);
+        const unsigned char *wc = from + T::A_BYTES + wave * (NW * 1024) + lane * 16;
+        const uint32_t *ww = reinterpret_cast<const uint32_t *>(from + T::A_BYTES + T::CODE_BYTES + wave * (T::WORD_LOADS * 256)) +
+                             col * T::GROUPS;
+        uint4 codes[NW];
+        unsigned word[NW][T::GROUPS];
+#pragma unroll
+        for (int nw = 0; nw < NW; ++nw) {
+            codes[nw] = *reinterpret_cast<const uint4 *>(wc + nw * 1024);
+#pragma unroll
+            for (int q = 0; q < T::GROUPS; ++q)
+                word[nw][q] = ww[nw * (16 * T::GROUPS) + q];
+        }
+        float4v sum[MB][NW];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int q = j / T::PER;
+            const unsigned char *x = from + col * 256 + (((4 * j + g) ^ col) * 16);
+            half8 w[NW];
+#pragma unroll
+            for (int nw = 0; nw < NW; ++nw) {
+                const unsigned dw = j == 0 ? codes[nw].x : j == 1 ? codes[nw].y : j == 2 ? codes[nw].z : codes[nw].w;
+                w[nw] = q4_codes(dw, q4_zero(word[nw][q]));
+                if constexpr (ROUND) {
+                    const half_t s = __builtin_bit_cast(q4_half2, word[nw][q])[0];
+                    w[nw] *= half8{s, s, s, s, s, s, s, s};
+                }
+            }
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const half8 a = *reinterpret_cast<const half8 *>(x + mb * 4096);
+#pragma unroll
+                for (int nw = 0; nw < NW; ++nw) {
+                    if constexpr (ROUND)
+                        acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
+                    else
+                        sum[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            a, w[nw], j % T::PER == 0 ? float4v{0, 0, 0, 0} : sum[mb][nw], 0, 0, 0);
+                }
+            }
+            if constexpr (!ROUND) {
+                if (j % T::PER == T::PER - 1) {
+#pragma unroll
+                    for (int nw = 0; nw < NW; ++nw) {
+                        const float s = q4_scale(word[nw][q]);
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                acc[mb][nw][r] = __builtin_fmaf(s, sum[mb][nw][r], acc[mb][nw][r]);
+                    }
+                }
+            }
+        }
+    };
+
+    int slot = 0;
+    for (int kb = begin; kb < end; ++kb) {
+        // this wave's loads of the stage have landed; and its reads of the
+        // stage that is refilled next are done
+        wait_vm_lgkm0<(STAGES - 2) * T::LOADS>();
+        if (p.K % 8 != 0 && kb == p.k_blocks - 1) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            in.clear_tail(lds + slot * T::STAGE_BYTES);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        const int fill = slot == 0 ? STAGES - 1 : slot - 1;
+        step(lds + slot * T::STAGE_BYTES, lds + fill * T::STAGE_BYTES, kb + STAGES - 1);
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
+    wait_vmcnt<0>();   // the last requests' zeros land before LDS is used again or given back
+
+    // lane (g, col) holds rows 16 mb + 4 g + r of A, column col of each block
+    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16;
+    if (p.W) {         // partial sums of a split, joined by the reduction kernel
+        float *out = p.W + ((int64_t)split * p.M + m0) * p.N;
+#pragma unroll
+        for (int nw = 0; nw < NW; ++nw) {
+            const int n = n0 + (wave * NW + nw) * 16 + col;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int m = 16 * mb + 4 * g + r;
+                    if (m < rows && n < p.N)
+                        out[(int64_t)m * p.N + n] = acc[mb][nw][r];
+                }
+        }
+        return;
+    }
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    half_t *c = reinterpret_cast<half_t *>(lds);
+#pragma unroll
+    for (int nw = 0; nw < NW; ++nw)
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float v = acc[mb][nw][r] * p.alpha;
+                if (p.relu)
+                    v = __builtin_fmaxf(v, 0.0f);
+                c[(16 * mb + 4 * g + r) * T::PITCH + (wave * NW + nw) * 16 + col] = (half_t)v;
+            }
+    __syncthreads();
+    constexpr int CHUNKS = T::BN / 8;
+    for (int e = threadIdx.x; e < rows * CHUNKS; e += 256) {
+        const int m = e / CHUNKS, n = e % CHUNKS * 8;
+        const half8 v = *reinterpret_cast<const half8 *>(c + m * T::PITCH + n);
+        half_t *to = p.C + (int64_t)(m0 + m) * p.N + n0 + n;
+        if (n0 + n + 8 <= p.N) {
+            __builtin_nontemporal_store(v, reinterpret_cast<half8_any *>(to));   // C streams out
+        } else {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (n0 + n + i < p.N)
+                    to[i] = v[i];
+        }
+    }
+}
+
+template <int MB, int NW, int STAGES, bool ROUND>
+static hipError_t launch_tile(const Q4Args &a, int group, int64_t grid, hipStream_t s)
+{
+    const dim3 blocks((unsigned)grid);
+    if (group == 32)
+        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+    else if (group == 64)
+        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
+{
+    switch (config) {
+    case 4: return launch_tile<4, 2, 4, false>(a, group, grid, s);
+    case 5: return launch_tile<8, 4, 3, true>(a, group, grid, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+} // namespace gemm_f16_impl

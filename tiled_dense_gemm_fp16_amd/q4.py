@@ -109,11 +109,30 @@ def q4_expand(w: Q4Matrix, out=None, stream=None):
     return out
 
 
+_plans: dict = {}
+
+
+def _planned(key):
+    """(splits, workspace bytes) of a product, by shape, alignment and request."""
+    hit = _plans.get(key)
+    if hit is None:
+        m, n, k, group, odd, config, splits = key
+        p = plan_q4(m, n, k, group, config, splits, 2 if odd else 0)
+        hit = (p["splits"], p["workspace_bytes"])
+        if len(_plans) > 4096:
+            _plans.clear()
+        _plans[key] = hit
+    return hit
+
+
 def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONFIG_AUTO, stream=None,
-            alpha: float = 1.0):
+            splits: int | None = None, workspace=None, alpha: float = 1.0):
     """C = epi(alpha * (a @ w^T)) for a (m x k float16) and a 4-bit n x k
     matrix: the product of a layer whose weights are held in 4 bits.  Sums are
-    fp32 and rounded once; one row reads each code once."""
+    fp32 and rounded once; one row reads each code once.
+
+    ``splits`` and ``workspace`` as in gemm(): None lets the planner split K
+    when that pays, with a workspace from torch's caching allocator."""
     import torch
 
     if epilogue not in _EPILOGUES:
@@ -127,16 +146,32 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
         out = torch.empty((m, w.n), dtype=torch.float16, device=a.device)
     else:
         _check_buffer(out, "out", torch.float16, (m, w.n), a.device)
+    if stream is None:
+        stream = torch.cuda.current_stream(a.device)
+    request = SPLITS_AUTO if splits is None else int(splits)
+    size = 0
+    if workspace is not None:
+        if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != a.device:
+            raise ValueError(f"workspace must be a contiguous tensor on {a.device}")
+        size = workspace.numel() * workspace.element_size()
+    elif m > 0 and w.n > 0:
+        size = _planned((m, w.n, k, w.group, a.data_ptr() % 4 != 0, config, request))[1]
+        if size:
+            with torch.cuda.device(a.device), torch.cuda.stream(stream):
+                workspace = torch.empty(size // 4, dtype=torch.float32, device=a.device)
     _call(a.device, "gemm_f16_q4", lib().gemm_f16_q4, m, w.n, k, w.group, a.data_ptr() or None,
           w.codes.data_ptr() or None, w.words.data_ptr() or None, out.data_ptr() or None, float(alpha),
-          _EPILOGUES[epilogue], config, _stream(stream, a.device))
+          _EPILOGUES[epilogue], config, request, workspace.data_ptr() if size else None, size, stream.cuda_stream or None)
     return out
 
 
-def plan_q4(m: int, n: int, k: int, group: int = 128, config: int = CONFIG_AUTO) -> dict:
-    """How gemm_f16_q4 would run this shape (host logic only)."""
+def plan_q4(m: int, n: int, k: int, group: int = 128, config: int = CONFIG_AUTO, splits: int | None = 1,
+            A_ptr: int = 0) -> dict:
+    """How gemm_f16_q4 would run this shape (host logic only); the pointer
+    only matters for its alignment."""
     p = Plan()
-    st = lib().gemm_f16_plan_q4(m, n, k, group, config, ctypes.byref(p))
+    st = lib().gemm_f16_plan_q4(m, n, k, group, A_ptr or None, config, SPLITS_AUTO if splits is None else int(splits),
+                                ctypes.byref(p))
     if st != SUCCESS:
         raise GemmError(st, "gemm_f16_plan_q4")
     return p.as_dict()
