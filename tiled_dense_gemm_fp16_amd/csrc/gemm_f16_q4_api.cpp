@@ -160,6 +160,13 @@ Q4Pages pages_of(const gemm_f16_q4_cache_t *c, const int32_t *table, int64_t bat
     p.table = table;
     p.batch = (int)batch;
     p.max_pages = (int)max_pages;
+    // t / d = floor(t m / 2^(31 + n)) with 2^(n-1) < d <= 2^n and m = floor(2^(31 + n) / d) + 1: m d exceeds
+    // 2^(31 + n) by at most d, so the quotient is off by at most t / 2^(31 + n) < 1 / d for t < 2^31
+    int n = 3;
+    while ((1 << n) < c->page_size)
+        ++n;
+    p.page_magic = (uint32_t)(((uint64_t)1 << (31 + n)) / (uint64_t)c->page_size + 1);
+    p.page_shift = n - 1;
     return p;
 }
 
@@ -169,8 +176,9 @@ bool rows_fit(int64_t stride, int64_t heads, int head_dim) { return stride >= he
 bool rows_aligned(const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
 int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0; }
 
-// Parts of the sequences: as many as give every CU four workgroups, while
-// each wave of a part keeps at least two blocks of tokens.
+// Parts of the sequences: as many as give every CU two workgroups (the
+// registers hold two to three), while each wave of a part keeps at least two
+// blocks of tokens.
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {
@@ -183,7 +191,7 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
     const int64_t tiles = (q_heads / heads + 15) / 16, units = batch * heads * tiles;
     if (splits == GEMM_F16_SPLITS_AUTO) {
         const int64_t blocks = (max_length + kQ4AttentionTokens - 1) / kQ4AttentionTokens;
-        const int64_t fill = units > 0 ? (4 * 256 + units - 1) / units : 1;
+        const int64_t fill = units > 0 ? (2 * 256 + units - 1) / units : 1;
         const int64_t most = blocks / (2 * kQ4AttentionWaves);
         splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
     }

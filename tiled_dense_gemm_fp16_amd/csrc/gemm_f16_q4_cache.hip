@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArg
     if (gr.count == 0)
         return;
     const int page = q4_page(a.c, gr.b, gr.pos);
-    const int in_page = (int)(gr.pos % a.c.page_size);
+    const int in_page = page >= 0 ? (int)gr.pos - q4_page_of(a.c, (int)gr.pos) * a.c.page_size : 0;
     // positions a rotation table covers (all without one); a negative
     // position has no page
     const int64_t covered = a.cos ? a.positions : INT64_MAX;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_read_kernel(Q4ReadArgs a)
     if (gr.count == 0)
         return;
     const int page = q4_page(a.c, gr.b, gr.pos);
-    const int in_page = (int)(gr.pos % a.c.page_size);
+    const int in_page = page >= 0 ? (int)gr.pos - q4_page_of(a.c, (int)gr.pos) * a.c.page_size : 0;
     const bool value = job >= H;
     const int h = value ? job - H : job;
     const int64_t head = (int64_t)page * H + h;

@@ -51,6 +51,8 @@ struct Q4Pages {
     int heads, page_size, head_dim, group;
     const int32_t *table;     // batch x max_pages
     int batch, max_pages;
+    uint32_t page_magic;      // t / page_size = (t page_magic >> 32) >> page_shift for 0 <= t < 2^31
+    int page_shift;
 };
 
 struct Q4AppendArgs {
@@ -122,14 +124,45 @@ __device__ __forceinline__ q4_half2 q4_pair(unsigned bits, unsigned zero)
     return __builtin_bit_cast(q4_half2, bits) + __builtin_bit_cast(q4_half2, zero);
 }
 
-// q - z of a dword's eight codes, exact: nine instructions.
-__device__ __forceinline__ q4_half8 q4_codes(unsigned w, const q4_zero &z)
+// The masks and the numbers that are OR-ed in.  v_and_or_b32 does both, but
+// takes no literal and one scalar operand: the values are kept from the
+// compiler's constant folding, the masks in scalar registers and the numbers
+// in vector registers, or it would emit an AND and an OR with a literal each.
+struct q4_bits {
+    unsigned low, high, low_one, high_one;
+    __device__ __forceinline__ q4_bits()
+    {
+        asm("s_mov_b32 %0, 0x000F000F" : "=s"(low));
+        asm("s_mov_b32 %0, 0x00F000F0" : "=s"(high));
+        asm("v_mov_b32 %0, 0x64006400" : "=v"(low_one));
+        asm("v_mov_b32 %0, 0x54005400" : "=v"(high_one));
+    }
+};
+
+// q - z of a dword's eight codes, exact, with the addends of the value pairs
+// 0-1, 2-3, 4-5 and 6-7: nine instructions.
+__device__ __forceinline__ q4_half8 q4_codes(unsigned w, const q4_bits &m, unsigned z0, unsigned z1, unsigned z2, unsigned z3)
 {
-    const q4_half2 p0 = q4_pair((w & 0x000F000Fu) | 0x64006400u, z.a);
-    const q4_half2 p1 = q4_pair((w & 0x00F000F0u) | 0x54005400u, z.b);
+    const q4_half2 p0 = q4_pair((w & m.low) | m.low_one, z0);
+    const q4_half2 p1 = q4_pair((w & m.high) | m.high_one, z1);
     w >>= 8;
-    const q4_half2 p2 = q4_pair((w & 0x000F000Fu) | 0x64006400u, z.a);
-    const q4_half2 p3 = q4_pair((w & 0x00F000F0u) | 0x54005400u, z.b);
+    const q4_half2 p2 = q4_pair((w & m.low) | m.low_one, z2);
+    const q4_half2 p3 = q4_pair((w & m.high) | m.high_one, z3);
+    return q4_half8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+__device__ __forceinline__ q4_half8 q4_codes(unsigned w, const q4_bits &m, const q4_zero &z)
+{
+    return q4_codes(w, m, z.a, z.b, z.a, z.b);
+}
+
+// 64 + q of a dword's eight codes: seven instructions, for products whose sum
+// of the other operand is known and takes the 64 off again.
+__device__ __forceinline__ q4_half8 q4_codes_64(unsigned w, const q4_bits &m)
+{
+    const q4_half2 p0 = __builtin_bit_cast(q4_half2, (w << 4 & m.high) | m.high_one);
+    const q4_half2 p1 = __builtin_bit_cast(q4_half2, (w & m.high) | m.high_one);
+    const q4_half2 p2 = __builtin_bit_cast(q4_half2, (w >> 4 & m.high) | m.high_one);
+    const q4_half2 p3 = __builtin_bit_cast(q4_half2, (w >> 8 & m.high) | m.high_one);
     return q4_half8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
@@ -166,14 +199,19 @@ struct q4_rounder {
 __device__ __forceinline__ constexpr int q4_shift(int i) { return 4 * (i / 2 + 4 * (i & 1)); }
 
 // ---- the paged cache ---------------------------------------------------------------
+// Index in the page table of position t, 0 <= t < 2^31.
+__device__ __forceinline__ int q4_page_of(const Q4Pages &c, int t)
+{
+    return (int)(__umulhi((uint32_t)t, c.page_magic) >> c.page_shift);
+}
+
 // Page of the granule of 8 tokens that holds position pos of sequence b, or -1
 // where the table or the pool has none.
 __device__ __forceinline__ int q4_page(const Q4Pages &c, int b, int64_t pos)
 {
-    const int64_t i = pos / c.page_size;
-    if (pos < 0 || i >= c.max_pages)
+    if (pos < 0 || pos >= (int64_t)c.max_pages * c.page_size)
         return -1;
-    const int id = c.table[(int64_t)b * c.max_pages + i];
+    const int id = c.table[(int64_t)b * c.max_pages + q4_page_of(c, (int)pos)];
     return id >= 0 && id < c.pages ? id : -1;
 }
 

@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
     Q4Loads<T, MB, NW> in;
     in.init(p, m0, nb0, end);
     const int wave = in.wave;
+    const q4_bits bits;
 
     float4v acc[MB][NW];
 #pragma unroll
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
 #pragma unroll
             for (int nw = 0; nw < NW; ++nw) {
                 const unsigned dw = j == 0 ? codes[nw].x : j == 1 ? codes[nw].y : j == 2 ? codes[nw].z : codes[nw].w;
-                w[nw] = q4_codes(dw, q4_zero(word[nw][q]));
+                w[nw] = q4_codes(dw, bits, q4_zero(word[nw][q]));
                 if constexpr (ROUND) {
                     const half_t s = __builtin_bit_cast(q4_half2, word[nw][q])[0];
                     w[nw] *= half8{s, s, s, s, s, s, s, s};

@@ -97,6 +97,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const uint32_t *__restri
                                                         int64_t N, int64_t K, int64_t k_blocks, int64_t tiles)
 {
     constexpr int GROUPS = 128 / GROUP, PER = GROUP / 32;
+    const q4_bits bits;
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     const int64_t stride = (int64_t)gridDim.x * 4;
     for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += stride) {
@@ -107,7 +108,7 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const uint32_t *__restri
         for (int j = 0; j < 4; ++j) {
             const uint32_t word = words[(tile * 16 + n) * GROUPS + j / PER];
             const float s = q4_scale(word);
-            const half8 q = q4_codes(dw[j], q4_zero(word));
+            const half8 q = q4_codes(dw[j], bits, q4_zero(word));
             half8 v;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -205,6 +206,7 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
     const int m0 = blockIdx.y * (16 * MB), nb0 = blockIdx.x * NW;
     const int rows = min(p.M - m0, 16 * MB);
+    const q4_bits bits;
 
     const uint32_t *codes[NW], *words[NW];
 #pragma unroll
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
                 float4v sum[MB];
 #pragma unroll
                 for (int j = q * PER; j < (q + 1) * PER; ++j) {
-                    const half8 w = q4_codes(dw[j], zero);
+                    const half8 w = q4_codes(dw[j], bits, zero);
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
                         sum[mb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
