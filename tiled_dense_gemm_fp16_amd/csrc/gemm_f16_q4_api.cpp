@@ -16,9 +16,10 @@ namespace gemm_f16_impl {
 const Q4Config kQ4Configs[kNumQ4Configs] = {
     {"q4_16x16_w8", 1, 1, 8, 0},
     {"q4_16x32_w8", 1, 2, 8, 0},
+    {"q4_16x64_w8", 1, 4, 8, 0},
     {"q4_32x32_w8", 2, 2, 8, 0},
     {"q4_64x32_w8", 4, 2, 8, 0},
-    {"q4_64x128_s4", 4, 8, 4, 4},
+    {"q4_64x128_s4", 4, 8, 8, 4},
     {"q4_128x256_s3", 8, 16, 4, 3},
 };
 
@@ -26,7 +27,7 @@ int64_t q4_lds_bytes(const Q4Config &c, int group)
 {
     if (c.stages == 0)
         return (int64_t)c.waves * c.m_blocks * c.n_blocks * 1024;
-    const int64_t word_loads = (c.n_blocks / c.waves * (128 / group) + 3) / 4;
+    const int64_t word_loads = (c.n_blocks * (128 / group) / 4 + c.waves - 1) / c.waves;
     return std::max<int64_t>(c.stages * (c.m_blocks * 4096 + c.n_blocks * 1024 + c.waves * word_loads * 256),
                              16 * c.m_blocks * (16 * c.n_blocks + 8) * 2);
 }
@@ -61,8 +62,22 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
         splits > GEMM_F16_MAX_SPLITS)
         return GEMM_F16_ERROR_INVALID_VALUE;
     int c = config;
-    if (c == GEMM_F16_CONFIG_AUTO)
-        c = M <= 16 ? (N <= 8192 ? 0 : 1) : !aligned ? (M <= 32 ? 2 : 3) : M <= 256 ? 4 : 5;
+    if (c == GEMM_F16_CONFIG_AUTO) {
+        // Up to 16 rows: wider workgroups read A less often but leave CUs
+        // idle when they are fewer than those.  us at (M, N x K), 16 / 32 /
+        // 64 columns: (1, 4096 x 4096) 4.2 / 5.3 / 6.8, (1, 8192 x 8192) 10.6 / 9.1
+        // / 13.5, (1, 28672 x 8192) 33.9 / 27.6 / 29.9, (16, 28672 x 8192) 59.3 / 41.9 / 35.2.
+        // Above, the tiles: 64 rows against 128 take 21.1 / 28.4 at (64,
+        // 8192 x 8192), 31.5 / 34.0 at 128 rows, 98.8 / 77.2 at 512; the kernels for
+        // few rows (for A's rows that are only 2-byte aligned) 22 and more at 32 rows.
+        const int64_t n_blocks = (N + 15) / 16;
+        if (M <= 16)
+            c = M > 8 && n_blocks > 4 * 256 ? 2 : n_blocks > 256 ? 1 : 0;
+        else if (!aligned)
+            c = M <= 32 ? 3 : 4;
+        else
+            c = M <= 128 ? 5 : 6;
+    }
     const Q4Config &d = kQ4Configs[c];
     if (d.stages > 0 && !aligned)
         return GEMM_F16_ERROR_INVALID_VALUE;

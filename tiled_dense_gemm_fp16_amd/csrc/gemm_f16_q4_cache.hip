@@ -57,9 +57,10 @@ __device__ __forceinline__ void load_rotated(const half_t *row, int c, bool vec,
     }
 }
 
-// x's codes as a dword and the group's word (the same in all its lanes).
+// x's codes as a dword and the group's word (the same in all its lanes);
+// half: x holds binary16 values.
 template <int GROUP>
-__device__ __forceinline__ unsigned round_chunk(float x[8], unsigned &word)
+__device__ __forceinline__ unsigned round_chunk(float x[8], unsigned &word, bool half)
 {
     float lo = 0.0f, hi = 0.0f;
 #pragma unroll
@@ -76,9 +77,15 @@ __device__ __forceinline__ unsigned round_chunk(float x[8], unsigned &word)
     const q4_rounder r(lo, hi, false);
     word = r.word();
     unsigned dw = 0;
+    if (half) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        dw |= r.code(x[i]) << q4_shift(i);
+        for (int i = 0; i < 8; ++i)
+            dw |= r.code16(x[i]) << q4_shift(i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dw |= r.code(x[i]) << q4_shift(i);
+    }
     return dw;
 }
 
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArg
             }
         }
         unsigned word;
-        const unsigned dw = round_chunk<GROUP>(x, word);
+        const unsigned dw = round_chunk<GROUP>(x, word, value);
         if (mine) {
             uint32_t *words = value ? a.c.v_words : a.c.k_words;
             if (chunk % (GROUP / 8) == 0)

@@ -31,7 +31,7 @@ struct Q4Config {
     int waves;
     int stages;              // LDS stages of a tile kernel, each of 128 k; 0: the kernel for few rows
 };
-constexpr int kNumQ4Configs = 6;
+constexpr int kNumQ4Configs = 7;
 extern const Q4Config kQ4Configs[kNumQ4Configs];
 
 int64_t q4_lds_bytes(const Q4Config &c, int group);
@@ -171,10 +171,10 @@ __device__ __forceinline__ float q4_scale(unsigned word)
     return (float)__builtin_bit_cast(q4_half2, word)[0];
 }
 
-// Scale word and codes of a group, from its extreme values; no contraction
-// to fused multiply-adds, so that the results are those of the formulas.
+// Scale word and codes of a group, from its extreme values.  NaN has been
+// replaced by 0 before.
 struct q4_rounder {
-    float s, z;
+    float s, z, r;
     __device__ __forceinline__ q4_rounder(float lo, float hi, bool symmetric)
     {
         lo = __builtin_fminf(lo, 0.0f);
@@ -182,16 +182,30 @@ struct q4_rounder {
         const float wide = symmetric ? __builtin_fmaxf(hi, -lo) / 7.0f : (hi - lo) / 15.0f;
         s = (float)(_Float16)__builtin_fminf(__builtin_fabsf(wide), 65504.0f);   // |.|: never -0
         z = symmetric ? 8.0f : s > 0.0f ? __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f) : 0.0f;
+        r = s > 0.0f ? 1.0f / s : 0.0f;
     }
     __device__ __forceinline__ unsigned word() const
     {
         const _Float16 h = (_Float16)s;
         return (unsigned)__builtin_bit_cast(unsigned short, h) | (unsigned)z << 16;
     }
+    __device__ __forceinline__ unsigned clamped(float t) const
+    {
+        return (unsigned)__builtin_amdgcn_fmed3f(t + z, 0.0f, 15.0f);
+    }
+    // code of any x
     __device__ __forceinline__ unsigned code(float x) const
     {
-        const float t = s > 0.0f ? __builtin_rintf(x / s) : 0.0f;
-        return (unsigned)__builtin_fminf(__builtin_fmaxf(t + z, 0.0f), 15.0f);
+        return clamped(s > 0.0f ? __builtin_rintf(x / s) : 0.0f);
+    }
+    // Code of a binary16 x, the same without the division: for x and s of 11
+    // bits the quotient either is a multiple of 1/2 or at least 2^-13 from one
+    // (where it matters, between codes), and x r is within 2^-18 of it, so
+    // rounding x r to a multiple of 2^-14 (adding 768 and taking it off) puts
+    // it on the multiple or leaves it on its side.
+    __device__ __forceinline__ unsigned code16(float x) const
+    {
+        return clamped(__builtin_rintf(__builtin_fmaf(x, r, 768.0f) - 768.0f));
     }
 };
 

@@ -21,6 +21,8 @@
 // gives) and the matrix cores add up everything: for many rows that
 // multiply-add costs more than it gives, since the weight's rounding is of
 // the size of the result's own (2^-11 of each weight, at random signs).
+#include <type_traits>
+
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
@@ -28,34 +30,30 @@ namespace gemm_f16_impl {
 
 typedef _Float16 half8_any __attribute__((ext_vector_type(8), aligned(2)));
 
-template <int GROUP, int MB, int NW, int STAGES, bool ROUND>
+// WM x WN waves: wave (wm, wn) multiplies 16 MB rows of A by 16 NW rows of W.
+template <int GROUP, int MB, int NW, int WM, int WN, int STAGES, bool ROUND>
 struct Q4Tile {
-    static constexpr int WAVES = 4, GROUPS = 128 / GROUP, PER = GROUP / 32;
-    static constexpr int BM = 16 * MB, BN = 16 * NW * WAVES;
-    static constexpr int A_BYTES = BM * 256, CODE_BYTES = WAVES * NW * 1024;
-    static constexpr int WORD_LOADS = (NW * GROUPS + 3) / 4;   // of 64 words, for each wave
+    static constexpr int WAVES = WM * WN, GROUPS = 128 / GROUP, PER = GROUP / 32;
+    static constexpr int BM = 16 * MB * WM, BN = 16 * NW * WN, N_BLOCKS = NW * WN;
+    static constexpr int A_BYTES = BM * 256, CODE_BYTES = N_BLOCKS * 1024;
+    static constexpr int A_LOADS = BM / 4 / WAVES, CODE_LOADS = N_BLOCKS / WAVES;   // of 1 KiB, for each wave
+    static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;  // of 64 words
     static constexpr int STAGE_BYTES = A_BYTES + CODE_BYTES + WAVES * WORD_LOADS * 256;
-    static constexpr int LOADS = MB + NW + WORD_LOADS;         // of a stage, for each wave
+    static constexpr int LOADS = A_LOADS + CODE_LOADS + WORD_LOADS;
     static constexpr int PITCH = BN + 8;                       // of the staged output, in halves
     static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > BM * PITCH * 2 ? STAGES * STAGE_BYTES : BM * PITCH * 2;
+    static_assert(BM / 4 % WAVES == 0 && N_BLOCKS % WAVES == 0, "whole loads for each wave");
     static_assert(LDS_BYTES <= 163840, "LDS of a CU");
 };
 
-// A pointer that every lane of the wave has alike, in scalar registers.
-__device__ __forceinline__ const uint32_t *uniform_pointer(const uint32_t *p)
-{
-    const uint64_t v = (uint64_t)p;
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v), hi = __builtin_amdgcn_readfirstlane((int)(v >> 32));
-    return reinterpret_cast<const uint32_t *>((uint64_t)hi << 32 | lo);
-}
-
-// One stage's loads of a wave.
-template <class T, int MB, int NW>
+// One stage's loads of a wave: 1 KiB pieces (of A: 4 rows; of the codes: a
+// tile) and 256-byte pieces of the words, dealt out to the waves in turn.
+template <class T>
 struct Q4Loads {
     __amdgpu_buffer_rsrc_t a, codes, words;
-    uint32_t a_off[MB];       // row and chunk of each load of A
-    int chunk[MB];
-    uint32_t code_off[NW], word_off[T::WORD_LOADS];
+    uint32_t a_off[T::A_LOADS];       // row and chunk of each load of A
+    int chunk[T::A_LOADS];
+    uint32_t code_off[T::CODE_LOADS], word_off[T::WORD_LOADS];
     int wave, lane, K, kb_end;
 
     __device__ __forceinline__ void init(const Q4Args &p, int m0, int nb0, int end)
@@ -67,23 +65,22 @@ struct Q4Loads {
         const int rows = min(p.M - m0, T::BM);
         a = make_rsrc(p.A + (int64_t)m0 * p.K, (uint32_t)rows * (uint32_t)p.K * 2u);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < T::A_LOADS; ++i) {
             const int row = 4 * (wave + T::WAVES * i) + lane / 16;
             chunk[i] = (lane & 15) ^ (row & 15);
             a_off[i] = (uint32_t)row * (uint32_t)p.K * 2u + (uint32_t)chunk[i] * 16u;
         }
-        const int nb = nb0 + wave * NW;
-        const int here = __builtin_amdgcn_readfirstlane(max(0, min(NW, p.n_blocks - nb)));   // past N: nothing is read
-        const int64_t tile = (int64_t)min(nb, p.n_blocks - 1) * p.k_blocks;
-        codes = make_rsrc(uniform_pointer(p.codes + tile * 256), (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
-        words = make_rsrc(uniform_pointer(p.words + tile * (16 * T::GROUPS)), (uint32_t)here * (uint32_t)p.k_blocks * (64u * T::GROUPS));
+        const int here = min(T::N_BLOCKS, p.n_blocks - nb0);   // past N: nothing is read
+        const int64_t tile = (int64_t)nb0 * p.k_blocks;
+        codes = make_rsrc(p.codes + tile * 256, (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
+        words = make_rsrc(p.words + tile * (16 * T::GROUPS), (uint32_t)here * (uint32_t)p.k_blocks * (64u * T::GROUPS));
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
-            code_off[i] = (uint32_t)i * (uint32_t)p.k_blocks * 1024u + (uint32_t)lane * 16u;
+        for (int i = 0; i < T::CODE_LOADS; ++i)
+            code_off[i] = (uint32_t)(wave + T::WAVES * i) * (uint32_t)p.k_blocks * 1024u + (uint32_t)lane * 16u;
 #pragma unroll
         for (int i = 0; i < T::WORD_LOADS; ++i) {
-            const int w = 64 * i + lane, nw = w / (16 * T::GROUPS);
-            word_off[i] = (nw < NW ? (uint32_t)nw * (uint32_t)p.k_blocks * (64u * T::GROUPS) : 0x80000000u) +
+            const int w = 64 * (wave + T::WAVES * i) + lane, nb = w / (16 * T::GROUPS);
+            word_off[i] = (nb < T::N_BLOCKS ? (uint32_t)nb * (uint32_t)p.k_blocks * (64u * T::GROUPS) : 0x80000000u) +
                           (uint32_t)(w % (16 * T::GROUPS)) * 4u;
         }
     }
@@ -93,19 +90,19 @@ struct Q4Loads {
     {
         const uint32_t gone = oob_unless(kb < kb_end);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < T::A_LOADS; ++i) {
             LDS_AS void *d = (LDS_AS void *)(to + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(a, d, 16, a_off[i] | gone | oob_unless(kb * 128 + chunk[i] * 8 < K),
                                                      (uint32_t)kb * 256u, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
-            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + (wave * NW + i) * 1024);
+        for (int i = 0; i < T::CODE_LOADS; ++i) {
+            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(codes, d, 16, code_off[i] | gone, (uint32_t)kb * 1024u, 0, 0);
         }
 #pragma unroll
         for (int i = 0; i < T::WORD_LOADS; ++i) {
-            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + T::CODE_BYTES + (wave * T::WORD_LOADS + i) * 256);
+            LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + T::CODE_BYTES + (wave + T::WAVES * i) * 256);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(words, d, 4, word_off[i] | gone, (uint32_t)kb * (64u * T::GROUPS), 0, 0);
         }
     }
@@ -113,30 +110,31 @@ struct Q4Loads {
     // clear what the chunk that straddles the end of a row brought of the next row
     __device__ __forceinline__ void clear_tail(unsigned char *stage) const
     {
-#pragma unroll
-        for (int i = 0; i < MB; ++i)
-            if (chunk[i] == K % 128 / 8) {
-                unsigned char *c = stage + (wave + T::WAVES * i) * 1024 + lane * 16;
+#pragma unroll 1
+        for (int i = 0; i < T::A_LOADS; ++i) {
+            const int piece = wave + T::WAVES * i, row = 4 * piece + lane / 16;
+            if (((lane & 15) ^ (row & 15)) == K % 128 / 8) {
+                unsigned char *c = stage + piece * 1024 + lane * 16;
                 for (int e = K % 8; e < 8; e += 2)
                     *reinterpret_cast<uint32_t *>(c + 2 * e) = 0u;
             }
+        }
     }
 };
 
-template <int GROUP, int MB, int NW, int STAGES, bool ROUND>
-__global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
+// TAIL: rows of A end inside a 16-byte chunk (K % 8 != 0).
+template <class T, int MB, int NW, int WN, int STAGES, bool ROUND, bool TAIL>
+__device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
 {
-    typedef Q4Tile<GROUP, MB, NW, STAGES, ROUND> T;
-    __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
     int tm, tn, split;
     tile_coords(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, 4, tm, tn, split);
-    const int m0 = tm * T::BM, nb0 = tn * (NW * T::WAVES);
+    const int m0 = tm * T::BM, nb0 = tn * T::N_BLOCKS;
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int begin = split * p.split_blocks, end = min(p.k_blocks, begin + p.split_blocks);
 
-    Q4Loads<T, MB, NW> in;
+    Q4Loads<T> in;
     in.init(p, m0, nb0, end);
-    const int wave = in.wave;
+    const int wm = in.wave / WN, wn = in.wave % WN;
     const q4_bits bits;
 
     float4v acc[MB][NW];
@@ -156,9 +154,9 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
     const auto step = [&](const unsigned char *__restrict__ from, unsigned char *__restrict__ fill, int kb)
                           __attribute__((always_inline)) {
         in.issue(kb, fill);
-        const unsigned char *wc = from + T::A_BYTES + wave * (NW * 1024) + lane * 16;
-        const uint32_t *ww = reinterpret_cast<const uint32_t *>(from + T::A_BYTES + T::CODE_BYTES + wave * (T::WORD_LOADS * 256)) +
-                             col * T::GROUPS;
+        const unsigned char *wc = from + T::A_BYTES + wn * (NW * 1024) + lane * 16;
+        const uint32_t *ww = reinterpret_cast<const uint32_t *>(from + T::A_BYTES + T::CODE_BYTES) +
+                             (wn * (NW * 16) + col) * T::GROUPS;
         uint4 codes[NW];
         unsigned word[NW][T::GROUPS];
 #pragma unroll
@@ -172,7 +170,7 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int q = j / T::PER;
-            const unsigned char *x = from + col * 256 + (((4 * j + g) ^ col) * 16);
+            const unsigned char *x = from + wm * (MB * 4096) + col * 256 + (((4 * j + g) ^ col) * 16);
             half8 w[NW];
 #pragma unroll
             for (int nw = 0; nw < NW; ++nw) {
@@ -216,10 +214,12 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
         // this wave's loads of the stage have landed; and its reads of the
         // stage that is refilled next are done
         wait_vm_lgkm0<(STAGES - 2) * T::LOADS>();
-        if (p.K % 8 != 0 && kb == p.k_blocks - 1) {
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-            in.clear_tail(lds + slot * T::STAGE_BYTES);
-            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        if constexpr (TAIL) {
+            if (kb == p.k_blocks - 1) {
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+                in.clear_tail(lds + slot * T::STAGE_BYTES);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            }
         }
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -229,18 +229,18 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
     }
     wait_vmcnt<0>();   // the last requests' zeros land before LDS is used again or given back
 
-    // lane (g, col) holds rows 16 mb + 4 g + r of A, column col of each block
-    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16;
+    // lane (g, col) holds rows 16 mb + 4 g + r of the wave's rows of A, column col of each block
+    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16, wave_m = wm * (16 * MB), wave_n = wn * (16 * NW);
     if (p.W) {         // partial sums of a split, joined by the reduction kernel
         float *out = p.W + ((int64_t)split * p.M + m0) * p.N;
 #pragma unroll
         for (int nw = 0; nw < NW; ++nw) {
-            const int n = n0 + (wave * NW + nw) * 16 + col;
+            const int n = n0 + wave_n + nw * 16 + col;
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int m = 16 * mb + 4 * g + r;
+                    const int m = wave_m + 16 * mb + 4 * g + r;
                     if (m < rows && n < p.N)
                         out[(int64_t)m * p.N + n] = acc[mb][nw][r];
                 }
@@ -259,11 +259,11 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
                 float v = acc[mb][nw][r] * p.alpha;
                 if (p.relu)
                     v = __builtin_fmaxf(v, 0.0f);
-                c[(16 * mb + 4 * g + r) * T::PITCH + (wave * NW + nw) * 16 + col] = (half_t)v;
+                c[(wave_m + 16 * mb + 4 * g + r) * T::PITCH + wave_n + nw * 16 + col] = (half_t)v;
             }
     __syncthreads();
     constexpr int CHUNKS = T::BN / 8;
-    for (int e = threadIdx.x; e < rows * CHUNKS; e += 256) {
+    for (int e = threadIdx.x; e < rows * CHUNKS; e += 64 * T::WAVES) {
         const int m = e / CHUNKS, n = e % CHUNKS * 8;
         const half8 v = *reinterpret_cast<const half8 *>(c + m * T::PITCH + n);
         half_t *to = p.C + (int64_t)(m0 + m) * p.N + n0 + n;
@@ -278,26 +278,40 @@ __global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
     }
 }
 
-template <int MB, int NW, int STAGES, bool ROUND>
+template <int GROUP, int MB, int NW, int WM, int WN, int STAGES, bool ROUND, bool TAIL>
+__global__ void __launch_bounds__(64 * WM * WN) q4_tile_kernel(Q4Args p)
+{
+    typedef Q4Tile<GROUP, MB, NW, WM, WN, STAGES, ROUND> T;
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
+    q4_tile<T, MB, NW, WN, STAGES, ROUND, TAIL>(p, lds);
+}
+
+template <int MB, int NW, int WM, int WN, int STAGES, bool ROUND, bool TAIL>
 static hipError_t launch_tile(const Q4Args &a, int group, int64_t grid, hipStream_t s)
 {
-    const dim3 blocks((unsigned)grid);
+    const dim3 blocks((unsigned)grid), threads(64 * WM * WN);
     if (group == 32)
-        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
     else if (group == 64)
-        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
     else
-        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, STAGES, ROUND>), blocks, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
     return hipGetLastError();
+}
+
+template <bool TAIL>
+static hipError_t launch_config(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
+{
+    switch (config) {
+    case 5: return launch_tile<4, 1, 1, 8, 4, false, TAIL>(a, group, grid, s);
+    case 6: return launch_tile<8, 4, 1, 4, 3, true, TAIL>(a, group, grid, s);
+    default: return hipErrorInvalidValue;
+    }
 }
 
 hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
 {
-    switch (config) {
-    case 4: return launch_tile<4, 2, 4, false>(a, group, grid, s);
-    case 5: return launch_tile<8, 4, 3, true>(a, group, grid, s);
-    default: return hipErrorInvalidValue;
-    }
+    return a.K % 8 != 0 ? launch_config<true>(config, group, a, grid, s) : launch_config<false>(config, group, a, grid, s);
 }
 
 } // namespace gemm_f16_impl

@@ -40,32 +40,46 @@ __global__ void __launch_bounds__(256) q4_compress_kernel(const half_t *__restri
     const int64_t stride = (int64_t)gridDim.x * 4;
     for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += stride) {
         const int64_t row = tile / k_blocks * 16 + n, k0 = tile % k_blocks * 128 + 8 * g;
-        float x[4][8];
+        half8 x[4];
+        half8 sum = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            half8 v = {};
+            x[j] = half8{};
             const int64_t k = k0 + 32 * j;
             if (row < N)
-                v = row_piece(W + row * K + k, (int)(K - k));
+                x[j] = row_piece(W + row * K + k, (int)(K - k));
+            sum += x[j];
+        }
+        // a NaN (or an infinity, or an overflow) shows in the sum: rare, so
+        // the replacement of NaN is skipped without one
+        bool odd = false;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float f = (float)v[i];
-                x[j][i] = f == f ? f : 0.0f;
-            }
+        for (int i = 0; i < 8; ++i)
+            odd |= !(__builtin_fabsf((float)sum[i]) < 65504.0f);
+        if (__any(odd)) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[j][i] = x[j][i] == x[j][i] ? x[j][i] : (half_t)0.0f;
         }
         uint32_t word[GROUPS];
         uint4 out;
         unsigned dw[4];
 #pragma unroll
         for (int q = 0; q < GROUPS; ++q) {
+            half8 low = x[q * PER], high = low;
+#pragma unroll
+            for (int j = q * PER + 1; j < (q + 1) * PER; ++j) {
+                low = __builtin_elementwise_min(low, x[j]);
+                high = __builtin_elementwise_max(high, x[j]);
+            }
             float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-            for (int j = q * PER; j < (q + 1) * PER; ++j)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    lo = __builtin_fminf(lo, x[j][i]);
-                    hi = __builtin_fmaxf(hi, x[j][i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                lo = __builtin_fminf(lo, (float)low[i]);
+                hi = __builtin_fmaxf(hi, (float)high[i]);
+            }
 #pragma unroll
             for (int m = 16; m < 64; m *= 2) {
                 lo = __builtin_fminf(lo, __shfl_xor(lo, m));
@@ -78,7 +92,7 @@ __global__ void __launch_bounds__(256) q4_compress_kernel(const half_t *__restri
                 dw[j] = 0;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dw[j] |= r.code(x[j][i]) << q4_shift(i);
+                    dw[j] |= r.code16((float)x[j][i]) << q4_shift(i);
             }
         }
         out = make_uint4(dw[0], dw[1], dw[2], dw[3]);
@@ -171,76 +185,89 @@ hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float
 // group's scale, in fp32, so nothing is rounded before the end.  With W as
 // the second operand a lane holds results of the W row whose codes it
 // unpacked: zero point and scale are its own, with no exchange of lanes.
-// The next step's loads are issued before the present step's products.
+//
+// DEPTH steps are in flight: the kernel is bound by the latency and bandwidth
+// of the codes' loads.  They are buffer loads, so that steps past the end,
+// rows past M and rows of W past N read nothing (and return zeros) without a
+// branch, which would make the compiler wait for more than it needs.  A whose
+// rows are only 2-byte aligned is read by plain loads instead (ALIGNED false).
 
 template <int GROUPS>
-__device__ __forceinline__ void load_words(const uint32_t *p, unsigned (&w)[GROUPS])
+__device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t at, unsigned (&w)[GROUPS])
 {
     if constexpr (GROUPS == 1) {
-        w[0] = p[0];
+        w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, off, at, 0);
     } else if constexpr (GROUPS == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
+        const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, off, at, 0);
+        w[0] = v[0];
+        w[1] = v[1];
     } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
+        const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, off, at, 0);
+        w[0] = v[0];
+        w[1] = v[1];
+        w[2] = v[2];
+        w[3] = v[3];
     }
 }
 
 template <int GROUPS, int MB, int NW>
 struct ProductStep {
-    uint4 codes[NW];
+    unsigned codes[NW][4];
     unsigned words[NW][GROUPS];
     half8 x[MB][4];
 };
 
-template <int GROUP, int MB, int NW, int WAVES>
+template <int GROUP, int MB, int NW, int WAVES, int DEPTH, bool ALIGNED>
 __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
 {
     constexpr int GROUPS = 128 / GROUP, PER = GROUP / 32;
     extern __shared__ __attribute__((aligned(16))) unsigned char q4_lds[];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int m0 = blockIdx.y * (16 * MB), nb0 = blockIdx.x * NW;
-    const int rows = min(p.M - m0, 16 * MB);
+    const int rows = min(p.M - m0, 16 * MB), here = min(NW, p.n_blocks - nb0);
     const q4_bits bits;
 
-    const uint32_t *codes[NW], *words[NW];
-#pragma unroll
-    for (int nw = 0; nw < NW; ++nw) {
-        const int64_t tile = (int64_t)min(nb0 + nw, p.n_blocks - 1) * p.k_blocks;   // past N: repeats, not stored
-        codes[nw] = p.codes + (tile * 64 + lane) * 4;
-        words[nw] = p.words + (tile * 16 + (lane & 15)) * GROUPS;
-    }
+    const __amdgpu_buffer_rsrc_t codes = make_rsrc(p.codes + (int64_t)nb0 * p.k_blocks * 256,
+                                                   (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
+    const __amdgpu_buffer_rsrc_t words = make_rsrc(p.words + (int64_t)nb0 * p.k_blocks * (16 * GROUPS),
+                                                   (uint32_t)here * (uint32_t)p.k_blocks * (64u * GROUPS));
+    const __amdgpu_buffer_rsrc_t a = make_rsrc(p.A + (int64_t)m0 * p.K, (uint32_t)rows * (uint32_t)p.K * 2u);
     const half_t *row[MB];
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
-        row[mb] = p.A + (int64_t)(m0 + min(16 * mb + (lane & 15), rows - 1)) * p.K + 8 * g;   // past M: likewise
+        row[mb] = p.A + (int64_t)(m0 + min(16 * mb + col, rows - 1)) * p.K + 8 * g;
 
     typedef ProductStep<GROUPS, MB, NW> Step;
-    const auto load = [&](int kb, Step &s) {
+    const auto load_w = [&](int kb, uint32_t gone, Step &s) {
 #pragma unroll
         for (int nw = 0; nw < NW; ++nw) {
-            s.codes[nw] = *reinterpret_cast<const uint4 *>(codes[nw] + (int64_t)kb * 256);
-            load_words<GROUPS>(words[nw] + (int64_t)kb * (16 * GROUPS), s.words[nw]);
+            const uint32_t tile = (uint32_t)nw * (uint32_t)p.k_blocks;
+            const auto v = __builtin_amdgcn_raw_buffer_load_b128(codes, (tile * 1024u + lane * 16u) | gone,
+                                                                 (uint32_t)kb * 1024u, 0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                s.codes[nw][i] = v[i];
+            load_words<GROUPS>(words, (tile * (64u * GROUPS) + col * (4u * GROUPS)) | gone, (uint32_t)kb * (64u * GROUPS),
+                               s.words[nw]);
         }
-        const int left = p.K - kb * 128 - 8 * g;
-        if (kb * 128 + 128 <= p.K) {
+    };
+    const int whole = p.K / 128;   // k blocks that A's rows fill
+    const auto load = [&](int kb, Step &s) {
+        const uint32_t gone = oob_unless(kb < whole);
+        load_w(kb, gone, s);
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s.x[mb][j] = *reinterpret_cast<const half8_any *>(row[mb] + kb * 128 + 32 * j);
-        } else {
-#pragma unroll
-            for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    s.x[mb][j] = row_piece(row[mb] + kb * 128 + 32 * j, left - 32 * j);
-        }
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (ALIGNED) {
+                    const uint32_t off = (uint32_t)(16 * mb + col) * (uint32_t)p.K * 2u + 16u * g + 64u * j;
+                    s.x[mb][j] = __builtin_bit_cast(
+                        half8, __builtin_amdgcn_raw_buffer_load_b128(a, off | gone, (uint32_t)kb * 256u, 0));
+                } else {
+                    s.x[mb][j] = *reinterpret_cast<const half8_any *>(row[mb] + max(0, min(kb, whole - 1)) * 128 + 32 * j);
+                }
+            }
     };
 
     float4v acc[MB][NW];
@@ -253,7 +280,6 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
     const auto multiply = [&](const Step &s) {
 #pragma unroll
         for (int nw = 0; nw < NW; ++nw) {
-            const unsigned dw[4] = {s.codes[nw].x, s.codes[nw].y, s.codes[nw].z, s.codes[nw].w};
 #pragma unroll
             for (int q = 0; q < GROUPS; ++q) {
                 const q4_zero zero(s.words[nw][q]);
@@ -261,7 +287,7 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
                 float4v sum[MB];
 #pragma unroll
                 for (int j = q * PER; j < (q + 1) * PER; ++j) {
-                    const half8 w = q4_codes(dw[j], bits, zero);
+                    const half8 w = q4_codes(s.codes[nw][j], bits, zero);
 #pragma unroll
                     for (int mb = 0; mb < MB; ++mb)
                         sum[mb] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
@@ -276,25 +302,35 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
         }
     };
 
-    int kb = wave;
-    if (kb < p.k_blocks) {
-        Step a, b;
-        load(kb, a);
-        for (;;) {
-            if (kb + WAVES >= p.k_blocks) {
-                multiply(a);
-                break;
+    if (wave < whole) {
+        Step s[DEPTH];
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d)
+            load(wave + d * WAVES, s[d]);
+        for (int kb = wave;; kb += DEPTH * WAVES) {
+            bool done = false;
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d) {
+                multiply(s[d]);
+                if (kb + (d + 1) * WAVES >= whole) {
+                    done = true;
+                    break;
+                }
+                load(kb + (d + DEPTH) * WAVES, s[d]);
             }
-            load(kb + WAVES, b);
-            multiply(a);
-            kb += 2 * WAVES;
-            if (kb >= p.k_blocks) {
-                multiply(b);
+            if (done)
                 break;
-            }
-            load(kb, a);
-            multiply(b);
         }
+    }
+    if (whole < p.k_blocks && wave == whole % WAVES) {   // the k block that A's rows end in
+        Step s;
+        load_w(whole, 0u, s);
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                s.x[mb][j] = row_piece(row[mb] + whole * 128 + 32 * j, p.K - whole * 128 - 8 * g - 32 * j);
+        multiply(s);
     }
 
     // add the waves' sums in wave order; lane (g, n) holds rows 4 g + r of
@@ -324,17 +360,37 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
     }
 }
 
-template <int GROUP>
+template <int GROUP, bool ALIGNED>
 static hipError_t launch_group(int config, const Q4Args &a, dim3 grid, unsigned lds, hipStream_t s)
 {
+    // steps in flight: no more than the waves have
+    const bool one = a.K <= 8 * 128;
     switch (config) {
-    case 0: hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 1, 8>), grid, dim3(512), lds, s, a); break;
-    case 1: hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 2, 8>), grid, dim3(512), lds, s, a); break;
-    case 2: hipLaunchKernelGGL((q4_product_kernel<GROUP, 2, 2, 8>), grid, dim3(512), lds, s, a); break;
-    case 3: hipLaunchKernelGGL((q4_product_kernel<GROUP, 4, 2, 8>), grid, dim3(512), lds, s, a); break;
+    case 0:
+        if (one)
+            hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 1, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a);
+        else
+            hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 1, 8, 4, ALIGNED>), grid, dim3(512), lds, s, a);
+        break;
+    case 1:
+        if (one)
+            hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 2, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a);
+        else
+            hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 2, 8, 3, ALIGNED>), grid, dim3(512), lds, s, a);
+        break;
+    case 2: hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 4, 8, 2, ALIGNED>), grid, dim3(512), lds, s, a); break;
+    case 3: hipLaunchKernelGGL((q4_product_kernel<GROUP, 2, 2, 8, 2, ALIGNED>), grid, dim3(512), lds, s, a); break;
+    case 4: hipLaunchKernelGGL((q4_product_kernel<GROUP, 4, 2, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
+}
+
+template <int GROUP>
+static hipError_t launch_aligned(int config, const Q4Args &a, dim3 grid, unsigned lds, hipStream_t s)
+{
+    return (uintptr_t)a.A % 4 == 0 && a.K % 2 == 0 ? launch_group<GROUP, true>(config, a, grid, lds, s)
+                                                   : launch_group<GROUP, false>(config, a, grid, lds, s);
 }
 
 hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s)
@@ -348,9 +404,9 @@ hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s)
         b.C += m * a.N;
         b.M = (int)std::min<int64_t>(a.M - m, step);
         const dim3 grid((unsigned)a.tiles_n, (unsigned)std::min<int64_t>(a.tiles_m - m / step * 65535, 65535));
-        const hipError_t e = group == 32   ? launch_group<32>(config, b, grid, lds, s)
-                             : group == 64 ? launch_group<64>(config, b, grid, lds, s)
-                                           : launch_group<128>(config, b, grid, lds, s);
+        const hipError_t e = group == 32   ? launch_aligned<32>(config, b, grid, lds, s)
+                             : group == 64 ? launch_aligned<64>(config, b, grid, lds, s)
+                                           : launch_aligned<128>(config, b, grid, lds, s);
         if (e != hipSuccess)
             return e;
     }
