@@ -191,9 +191,13 @@ bool rows_fit(int64_t stride, int64_t heads, int head_dim) { return stride >= he
 bool rows_aligned(const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
 int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0; }
 
-// Parts of the sequences: as many as give every CU two workgroups (the
-// registers hold two to three), while each wave of a part keeps at least two
-// blocks of tokens.
+// Parts of the sequences: none where every CU has two workgroups without
+// (64 x 1000 tokens x 8 heads: 17.8 us whole, 25.6 in two parts); else as many
+// as make two for each CU, or four where sequences may differ in length and
+// the next workgroup evens that out (32 x 4096 x 8 heads: 28.1 us in four parts, 30.6
+// in two, 41.6 whole; one sequence of 131000: 32.9 us in 64 parts, 36.0 in 128), while
+// each wave of a part keeps a block of tokens (one sequence of 2000: 7.8 us in
+// 16 parts, 8.4 in 8).
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {
@@ -206,8 +210,9 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
     const int64_t tiles = (q_heads / heads + 15) / 16, units = batch * heads * tiles;
     if (splits == GEMM_F16_SPLITS_AUTO) {
         const int64_t blocks = (max_length + kQ4AttentionTokens - 1) / kQ4AttentionTokens;
-        const int64_t fill = units > 0 ? (2 * 256 + units - 1) / units : 1;
-        const int64_t most = blocks / (2 * kQ4AttentionWaves);
+        const int64_t here = head_dim == 256 && group < 128 ? 256 : 2 * 256;   // workgroups that the registers admit
+        const int64_t fill = units <= 0 || units >= here ? 1 : (batch > 1 && head_dim < 256 ? 2 * here : here) / units;
+        const int64_t most = blocks / kQ4AttentionWaves;
         splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
     }
     memset(p, 0, sizeof(*p));

@@ -41,9 +41,20 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr float kTop = 15.0f, kLift = 12.0f;   // P' stays below 2^kTop and starts below 2^kLift
 
-// Waves of a SIMD the registers are shared out to (measured for head_dim 128:
-// one wave with all of them lost to two, 50 against 43 us at 32 x 4096).
-constexpr int attention_waves(int head_dim, int group) { return head_dim == 256 && group < 128 ? 1 : 2; }
+// Waves of a SIMD the registers are shared out to.  At 32 x 4096 tokens,
+// head_dim 128: group 64 30.1 us with 2 (and a block's loads ahead), 28.1 with 3
+// (without); group 128 25.9 with 2, 27.0 with 3, and 32.9 against 37.3 for one
+// sequence of 131000.
+constexpr int attention_waves(int head_dim, int group)
+{
+    return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim / group == 1 ? 2 : 3;
+}
+
+// Blocks of a part: whole turns of the workgroup's waves.
+__device__ __forceinline__ int part_blocks(int blocks, int splits)
+{
+    return ((blocks + splits - 1) / splits + WAVES - 1) / WAVES * WAVES;
+}
 
 // Two values rounded towards zero to binary16, packed.  Only for splitting a
 // value into two parts: the second takes up what the first leaves.
@@ -118,7 +129,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
 
     const int length = __builtin_amdgcn_readfirstlane(
         (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.c.max_pages * a.c.page_size));
-    const int blocks = (length + STEP - 1) / STEP, per = (blocks + a.splits - 1) / a.splits;
+    const int blocks = (length + STEP - 1) / STEP, per = part_blocks(blocks, a.splits);
     const int first = split * per, last = min(blocks, first + per);
     if (first >= last && (a.splits > 1 || length > 0))
         return;                                                  // an empty part; the join does not read it
@@ -204,6 +215,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     half8 q[D / 32];
     const float scale = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);   // 0 would undo -infinity
     float q_sum[GROUPS];
+    float4v start[GROUPS];         // takes the 64 off again
     const auto load_queries = [&]() {
         const half_t *row = a.Q + b * a.q_stride + (q_head + min(col, rows - 1)) * D + 8 * g;
 #pragma unroll
@@ -220,6 +232,8 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
                 for (int i = 0; i < 8; ++i)
                     t += (float)q[j][i];
             q_sum[n] = column_sum(t);
+            const float off = -64.0f * q_sum[n];
+            start[n] = float4v{off, off, off, off};
         }
     };
     const q4_bits bits;
@@ -238,8 +252,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int n = 0; n < GROUPS; ++n) {
-                const float start = -64.0f * q_sum[n];
-                float4v s = {start, start, start, start};
+                float4v s = start[n];
 #pragma unroll
                 for (int j = n * JG; j < (n + 1) * JG; ++j)
                     s = __builtin_amdgcn_mfma_f32_16x16x32_f16(q4_codes_64(y.k[u][j], bits), q[j], s, 0, 0, 0);
@@ -270,6 +283,16 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
                     word[n][i] = there ? word[n][i] : 0u;
             }
         }
+        // (the empty asm keeps one conversion of each scale for both uses;
+        // the compiler would make a second one for the absolute value)
+        float s[GROUPS][8];
+#pragma unroll
+        for (int n = 0; n < GROUPS; ++n)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                s[n][i] = q4_scale(word[n][i]);
+                asm("" : "+v"(s[n][i]));
+            }
         float most = x[0], top = 0.0f;
 #pragma unroll
         for (int i = 1; i < 8; ++i)
@@ -278,7 +301,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
         for (int n = 0; n < GROUPS; ++n)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                top = __builtin_fmaxf(top, __builtin_fabsf(q4_scale(word[n][i])));
+                top = __builtin_fmaxf(top, __builtin_fabsf(s[n][i]));
         most = column_max(most);
         top = column_max(top);
         // the place of the largest P', 0 for -infinity times 0 (no token, or scale 0)
@@ -305,7 +328,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
             half8 hi, lo;
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
-                const float p0 = x[i] * q4_scale(w[i]), p1 = x[i + 1] * q4_scale(w[i + 1]);
+                const float p0 = x[i] * s[n][i], p1 = x[i + 1] * s[n][i + 1];
                 const q4_half2 v = pack_rtz(p0, p1), rest = pack_rtz(p0 - (float)v[0], p1 - (float)v[1]);
                 hi[i] = v[0];
                 hi[i + 1] = v[1];
@@ -326,7 +349,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     int block = first + wave, pk = 0, pg = 0;
     if (block < last) {
         next_pages(block, pk, pg);
-        if constexpr (Block::REGISTERS <= 48) {
+        if constexpr (Block::REGISTERS <= 32) {
             // A block's loads go out before the one ahead of it is attended
             // to, its pages one block earlier still (and before that block's
             // loads: waiting for the pages must not wait for those).
@@ -406,49 +429,62 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     }
 }
 
-// Join the parts of one head: D / 4 lanes hold its elements, and as many
-// teams of them as 256 threads make take the parts in turn; the teams' sums
-// are added in order.
-template <int D>
+// Join the parts of the heads: D / 4 lanes hold a head's elements, and TEAMS
+// teams of them take its parts in turn; the teams' sums are added in order.
+// With one team a workgroup joins several heads.
+template <int D, int TEAMS>
 __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs a)
 {
-    constexpr int LANES = D / 4, TEAMS = 256 / LANES;
-    __shared__ float4v sums[TEAMS][LANES];
-    __shared__ float totals[TEAMS];
-    const int64_t head = blockIdx.x;
-    const int d = threadIdx.x % LANES, team = threadIdx.x / LANES, b = (int)(head / a.q_heads);
-    const int length = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.c.max_pages * a.c.page_size);
-    const int blocks = (length + STEP - 1) / STEP, per = (blocks + a.splits - 1) / a.splits;
-    const int used = per > 0 ? (blocks + per - 1) / per : 0;     // parts that hold tokens
-    const float *ml = a.parts + (int64_t)a.c.batch * a.q_heads * a.splits * D + head * a.splits * 2;
-    const float *part = a.parts + head * a.splits * D + 4 * d;
-    float top = -INFINITY;
-    for (int s = threadIdx.x & 63; s < used; s += 64)
-        top = __builtin_fmaxf(top, ml[2 * s]);
-#pragma unroll
-    for (int m = 1; m < 64; m *= 2)
-        top = __builtin_fmaxf(top, __shfl_xor(top, m));
-    const float base = top == -INFINITY ? 0.0f : top;
+    constexpr int LANES = D / 4, HEADS = 256 / LANES / TEAMS;
+    static_assert(TEAMS == 1 || HEADS == 1, "several heads, or several teams");
+    __shared__ float4v sums[TEAMS][HEADS * LANES];
+    __shared__ float totals[TEAMS][HEADS];
+    const int d = threadIdx.x % LANES, team = threadIdx.x / LANES % TEAMS, mine = threadIdx.x / (LANES * TEAMS);
+    const int64_t heads = (int64_t)a.c.batch * a.q_heads, head = (int64_t)blockIdx.x * HEADS + mine;
     float total = 0.0f;
     float4v v = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int s = team; s < used; s += TEAMS) {
-        const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
-        total += f * ml[2 * s + 1];
-        v += f * *reinterpret_cast<const float4v *>(part + (int64_t)s * D);
-    }
-    sums[team][d] = v;
-    if (d == 0)
-        totals[team] = total;
-    __syncthreads();
-    if (team > 0)
-        return;
+    if (head < heads) {
+        const int b = (int)(head / a.q_heads);
+        const int length = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.c.max_pages * a.c.page_size);
+        const int blocks = (length + STEP - 1) / STEP, per = part_blocks(blocks, a.splits);
+        const int used = per > 0 ? (blocks + per - 1) / per : 0;     // parts that hold tokens
+        const float *ml = a.parts + heads * a.splits * D + head * a.splits * 2;
+        const float *part = a.parts + head * a.splits * D + 4 * d;
+        float top = -INFINITY;
+        if constexpr (TEAMS > 1) {   // one head: every wave looks at all parts
+            for (int s = threadIdx.x & 63; s < used; s += 64)
+                top = __builtin_fmaxf(top, ml[2 * s]);
 #pragma unroll
-    for (int t = 1; t < TEAMS; ++t) {
-        v += sums[t][d];
-        total += totals[t];
+            for (int m = 1; m < 64; m *= 2)
+                top = __builtin_fmaxf(top, __shfl_xor(top, m));
+        } else {
+#pragma unroll 4
+            for (int s = 0; s < used; ++s)
+                top = __builtin_fmaxf(top, ml[2 * s]);
+        }
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+        for (int s = team; s < used; s += TEAMS) {
+            const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
+            total += f * ml[2 * s + 1];
+            v += f * *reinterpret_cast<const float4v *>(part + (int64_t)s * D);
+        }
     }
-    store_quotient(a.out + head * D + 4 * d, v, total);
+    if constexpr (TEAMS > 1) {
+        sums[team][mine * LANES + d] = v;
+        if (d == 0)
+            totals[team][mine] = total;
+        __syncthreads();
+        if (team > 0)
+            return;
+#pragma unroll
+        for (int t = 1; t < TEAMS; ++t) {
+            v += sums[t][mine * LANES + d];
+            total += totals[t][mine];
+        }
+    }
+    if (head < heads)
+        store_quotient(a.out + head * D + 4 * d, v, total);
 }
 
 int64_t q4_attention_lds_bytes(int head_dim) { return 4 * WAVES * (16 * (head_dim + 4) + 32); }
@@ -465,7 +501,13 @@ static hipError_t launch_attention(const Q4AttentionArgs &a, int64_t grid, hipSt
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1)
         return e;
-    hipLaunchKernelGGL((q4_attention_join_kernel<D>), dim3((unsigned)(a.c.batch * a.q_heads)), dim3(256), 0, s, a);
+    // few parts: a team for each head; many: all of a workgroup's teams
+    const int64_t heads = (int64_t)a.c.batch * a.q_heads;
+    constexpr int TEAMS = 1024 / D;
+    if (a.splits <= 8)
+        hipLaunchKernelGGL((q4_attention_join_kernel<D, 1>), dim3((unsigned)((heads + TEAMS - 1) / TEAMS)), dim3(256), 0, s, a);
+    else
+        hipLaunchKernelGGL((q4_attention_join_kernel<D, TEAMS>), dim3((unsigned)heads), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
