@@ -128,7 +128,7 @@ def test_every_config(config, group, m, n, k):
     check(m, n, k, group, config=config, seed=m + n + k)
 
 
-@pytest.mark.parametrize("config", [c for c in range(g.q4_num_configs()) if g.plan_q4(64, 64, 128, config=c)["direct_lds"]])
+@pytest.mark.parametrize("config", range(g.q4_num_configs()))
 @pytest.mark.parametrize("m,n,k,splits", [(1, 16, 384, 3), (70, 140, 1030, 2), (64, 128, 4100, 7), (130, 300, 2048, 64),
                                           (129, 257, 132, 2), (300, 520, 514, None)])
 def test_splits(config, m, n, k, splits):

@@ -65,21 +65,17 @@ def test_product_refusals():
         assert call(**bad) == MISALIGNED, bad
     for bad in (dict(m=1 << 31), dict(n=(1 << 22) + 1), dict(k=(1 << 22) + 1)):
         assert call(**bad) == SIZE, bad
-    # the tile configurations: A's rows 4-byte aligned, and a workspace for a split
-    tile = [c for c in range(g.q4_num_configs()) if g.plan_q4(64, 32, 4096, 64, config=c)["direct_lds"]]
-    assert tile
+    # the tile configuration needs A's rows 4-byte aligned; a split a workspace
+    assert [g.plan_q4(64, 32, 4096, 64, config=c)["direct_lds"] for c in range(g.q4_num_configs())] == [0] * (g.q4_num_configs() - 1) + [1]
+    assert call(config=g.q4_num_configs() - 1, a=at(0) + 2) == INVALID and call(config=g.q4_num_configs() - 1, k=255) == INVALID
     for c in range(g.q4_num_configs()):
-        if c in tile:
-            assert call(config=c, a=at(0) + 2) == INVALID and call(config=c, k=255) == INVALID
-            need = g.plan_q4(4, 32, 4096, 64, config=c, splits=3)["workspace_bytes"]
-            assert need == 3 * 4 * 32 * 4
-            assert call(config=c, k=4096, splits=3) == 7
-            assert call(config=c, k=4096, splits=3, ws=at(4), size=need - 1) == 7
-            assert call(config=c, k=4096, splits=3, ws=at(4) + 8, size=need) == MISALIGNED
-            for p in (at(0), at(1), at(2), at(3)):
-                assert call(config=c, k=4096, splits=3, ws=p, size=need) == INVALID
-        else:
-            assert call(config=c, splits=2, k=4096, ws=at(4), size=1 << 20) == INVALID
+        need = g.plan_q4(4, 32, 4096, 64, config=c, splits=3)["workspace_bytes"]
+        assert need == 3 * 4 * 32 * 4
+        assert call(config=c, k=4096, splits=3) == 7
+        assert call(config=c, k=4096, splits=3, ws=at(4), size=need - 1) == 7
+        assert call(config=c, k=4096, splits=3, ws=at(4) + 8, size=need) == MISALIGNED
+        for p in (at(0), at(1), at(2), at(3)):
+            assert call(config=c, k=4096, splits=3, ws=p, size=need) == INVALID
     assert call(splits=-1) == INVALID and call(splits=65) == INVALID and call(ws=None, size=8) == INVALID
     assert call(m=0, a=None, c=None) == 0 and call(n=0, codes=None, words=None, c=None) == 0
     if not torch.cuda.is_available():

@@ -14,19 +14,18 @@
 namespace gemm_f16_impl {
 
 const Q4Config kQ4Configs[kNumQ4Configs] = {
-    {"q4_16x16_w8", 1, 1, 8, 0},
-    {"q4_16x32_w8", 1, 2, 8, 0},
-    {"q4_16x64_w8", 1, 4, 8, 0},
-    {"q4_32x32_w8", 2, 2, 8, 0},
-    {"q4_64x32_w8", 4, 2, 8, 0},
-    {"q4_64x128_s4", 4, 8, 8, 4},
+    {"q4_16x16", 1, 1, 8, 0},
+    {"q4_16x32", 1, 2, 8, 0},
+    {"q4_16x64", 1, 4, 8, 0},
+    {"q4_32x64", 2, 4, 8, 0},
+    {"q4_32x128", 2, 8, 8, 0},
     {"q4_128x256_s3", 8, 16, 4, 3},
 };
 
 int64_t q4_lds_bytes(const Q4Config &c, int group)
 {
     if (c.stages == 0)
-        return (int64_t)c.waves * c.m_blocks * c.n_blocks * 1024;
+        return (int64_t)c.waves * c.m_blocks * q4_sum_chunk(c.m_blocks, c.n_blocks) * 1024;
     const int64_t word_loads = (c.n_blocks * (128 / group) / 4 + c.waves - 1) / c.waves;
     return std::max<int64_t>(c.stages * (c.m_blocks * 4096 + c.n_blocks * 1024 + c.waves * word_loads * 256),
                              16 * c.m_blocks * (16 * c.n_blocks + 8) * 2);
@@ -61,22 +60,37 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     if ((config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumQ4Configs)) || splits < 0 ||
         splits > GEMM_F16_MAX_SPLITS)
         return GEMM_F16_ERROR_INVALID_VALUE;
+    // Wider workgroups read A and W less often, but leave CUs idle when they
+    // are few: the widest one that makes 150 workgroups.  us at (M, N x K) for
+    // 16x16 / 16x32 / 16x64 / 32x64 / 32x128, * the choice: (1, 4096 x 4096) *4.4 / 5.6 / 7.5;
+    // (1, 8192 x 8192) 11.1 / *10.6 / 14.6; (1, 28672 x 8192) 35.4 / 28.3 / *26.2; (16, 28672 x
+    // 8192) 57.4 / 41.1 / *33.1; (16, 5000 x 4100) 9.1 / *7.5 / 8.7; (48, 5000 x 4100) 14.8 / 11.5 /
+    // 10.2 / *11.9 / 14.8; (64, 8192 x 8192) 63.3 / 37.5 / 26.2 / *21.7 / 28.3; (128, 8192 x 8192) - /
+    // - / 45.4 / 38.9 / *28.5.
+    // With 64 blocks of K or more, splitting K beats narrower workgroups:
+    // (24, 2048 x 16384) 18.1 / 13.5 / 12.0 / *11.9 / 13.9; (24, 8192 x 8192) 29.2 / 19.1 /
+    // 15.8 / *14.4 / 16.7.
+    // The 128x256 tile takes over where it makes 64 workgroups for more than
+    // 64 rows (us with it against the best of the others): (100, 28672 x 8192)
+    // 71 / 104, (200, 8192 x 8192) 43 / 52, (2048, 8192 x 8192) 238 / 392; fewer:
+    // (200, 4096 x 4096) 27 / 16, (128, 8192 x 8192) 32 / 28; fewer rows: (48, 28672 x 8192) 67 / 55.
+    const int64_t n_blocks = (N + 15) / 16, blocks = (K + 127) / 128;
+    const int tile = kNumQ4Configs - 1, most_m = M > 16 ? 2 : 1;
+    const auto count = [&](int i) {
+        const int64_t m = 16 * kQ4Configs[i].m_blocks, n = kQ4Configs[i].n_blocks;
+        return (M + m - 1) / m * ((n_blocks + n - 1) / n);
+    };
     int c = config;
     if (c == GEMM_F16_CONFIG_AUTO) {
-        // Up to 16 rows: wider workgroups read A less often but leave CUs
-        // idle when they are fewer than those.  us at (M, N x K), 16 / 32 /
-        // 64 columns: (1, 4096 x 4096) 4.2 / 5.3 / 6.8, (1, 8192 x 8192) 10.6 / 9.1
-        // / 13.5, (1, 28672 x 8192) 33.9 / 27.6 / 29.9, (16, 28672 x 8192) 59.3 / 41.9 / 35.2.
-        // Above, the tiles: 64 rows against 128 take 21.1 / 28.4 at (64,
-        // 8192 x 8192), 31.5 / 34.0 at 128 rows, 98.8 / 77.2 at 512; the kernels for
-        // few rows (for A's rows that are only 2-byte aligned) 22 and more at 32 rows.
-        const int64_t n_blocks = (N + 15) / 16;
-        if (M <= 16)
-            c = M > 8 && n_blocks > 4 * 256 ? 2 : n_blocks > 256 ? 1 : 0;
-        else if (!aligned)
-            c = M <= 32 ? 3 : 4;
-        else
-            c = M <= 128 ? 5 : 6;
+        if (aligned && M > 64 && count(tile) >= 64) {
+            c = tile;
+        } else {
+            for (c = tile - 1; c > 0; --c)
+                if (kQ4Configs[c].m_blocks <= most_m && count(c) >= 150)
+                    break;
+            if (M > 8 && blocks >= 64)
+                c = std::max(c, M > 16 ? 3 : 2);
+        }
     }
     const Q4Config &d = kQ4Configs[c];
     if (d.stages > 0 && !aligned)
@@ -94,14 +108,13 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     p->vec_c = 8;
     p->tiles_m = (M + p->block_m - 1) / p->block_m;
     p->tiles_n = (N + p->block_n - 1) / p->block_n;
-    const int64_t blocks = (K + 127) / 128, tiles = p->tiles_m * p->tiles_n;
+    const int64_t tiles = p->tiles_m * p->tiles_n;
     if (splits == GEMM_F16_SPLITS_AUTO) {
         splits = 1;
-        if (d.stages > 0 && tiles > 0 && tiles < 256)   // a split keeps at least 8 blocks, as long as CUs are left
-            splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / 8), GEMM_F16_MAX_SPLITS));
+        if (M > 8 && tiles > 0 && tiles < 150)   // a part keeps 8 blocks, two for each wave of the kernel for few rows
+            splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / (d.stages > 0 ? 8 : 16)),
+                                                                 GEMM_F16_MAX_SPLITS));
     }
-    if (splits > 1 && d.stages == 0)
-        return GEMM_F16_ERROR_INVALID_VALUE;
     const int64_t per = blocks > 0 ? (blocks + splits - 1) / splits : 0;
     p->splits = per > 0 ? (int)((blocks + per - 1) / per) : 1;   // none empty
     p->grid = tiles * p->splits;
@@ -351,19 +364,22 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     a.words = (const uint32_t *)words;
     a.C = (_Float16 *)C;
     a.M = (int)M;
+    a.rows = (int)M;
+    a.row0 = 0;
     a.N = (int)N;
     a.K = (int)K;
     a.n_blocks = (int)((N + 15) / 16);
     a.k_blocks = (int)((K + 127) / 128);
     a.tiles_m = (int)plan.tiles_m;
     a.tiles_n = (int)plan.tiles_n;
+    a.splits = plan.splits;
     a.split_blocks = (int)plan.k_tiles;
     a.W = plan.splits > 1 ? (float *)workspace : nullptr;
     a.alpha = K == 0 ? 1.0f : alpha;   // the empty sum is +0 whatever alpha
     a.relu = epilogue == GEMM_F16_EPILOGUE_RELU ? 1 : 0;
-    if (kQ4Configs[plan.config].stages == 0)
-        return status_of(launch_q4(plan.config, group, a, (hipStream_t)stream));
-    const hipError_t e = launch_q4_tile(plan.config, group, a, plan.grid, (hipStream_t)stream);
+    const hipError_t e = kQ4Configs[plan.config].stages == 0
+                             ? launch_q4(plan.config, group, a, (hipStream_t)stream)
+                             : launch_q4_tile(group, a, plan.grid, (hipStream_t)stream);
     if (e != hipSuccess || plan.splits == 1)
         return status_of(e);
     return status_of(launch_reduce(a.W, a.C, M, N, plan.splits, a.alpha, a.relu, N % 4 == 0 && (uintptr_t)C % 8 == 0,

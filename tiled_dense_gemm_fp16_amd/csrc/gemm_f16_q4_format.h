@@ -18,8 +18,9 @@ struct Q4Args {
     int M, N, K;
     int n_blocks, k_blocks;  // tiles of 16 rows of W, of 128 k
     int tiles_m, tiles_n;    // workgroups
-    int split_blocks;        // tile kernels: k blocks of a split
-    float *W;                // a split's partial sums, splits x M x N; null: unsplit
+    int splits, split_blocks;   // parts of K, k blocks of one
+    float *W;                // a split's partial sums, splits x rows x N; null: unsplit
+    int rows, row0;          // rows of the call, and the first of this launch
     float alpha;
     int relu;
 };
@@ -29,16 +30,19 @@ struct Q4Config {
     int m_blocks;            // rows of A of a workgroup, in 16s
     int n_blocks;            // rows of W of a workgroup, in 16s
     int waves;
-    int stages;              // LDS stages of a tile kernel, each of 128 k; 0: the kernel for few rows
+    int stages;              // LDS stages of the tile kernel, each of 128 k; 0: the kernel for few rows
 };
-constexpr int kNumQ4Configs = 7;
+constexpr int kNumQ4Configs = 6;
 extern const Q4Config kQ4Configs[kNumQ4Configs];
 
+// The kernel for few rows adds its waves' sums this many 16-column blocks at
+// a time: 64 KiB of LDS at most.
+constexpr int q4_sum_chunk(int m_blocks, int n_blocks) { return m_blocks * n_blocks <= 8 ? n_blocks : 8 / m_blocks; }
 int64_t q4_lds_bytes(const Q4Config &c, int group);
-// The kernel for few rows: tiles_n x tiles_m workgroups.
+// The kernel for few rows: tiles_n x tiles_m x splits workgroups.
 hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s);
-// Tile kernels: tiles_m x tiles_n x splits workgroups; A's rows 4-byte aligned.
-hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s);
+// The tile kernel: tiles_m x tiles_n x splits workgroups; A's rows 4-byte aligned.
+hipError_t launch_q4_tile(int group, const Q4Args &a, int64_t grid, hipStream_t s);
 hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *words, int64_t N, int64_t K, int group,
                               bool symmetric, hipStream_t s);
 hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float16 *W, int64_t N, int64_t K, int group,

@@ -1,12 +1,12 @@
 // gemm_f16_q4_tile.hip -- the product with 4-bit weights, C = epi(alpha A W^T),
-// for more rows of A than one matrix instruction takes: LDS-staged tiles.
+// for many rows of A: LDS-staged tiles, bound by the matrix cores.
 //
 // A workgroup of 4 waves owns 16 MB rows of A and 64 NW rows of W.  A stage
 // holds 128 k: A's rows (256 bytes each), the waves' tiles of codes (1 KiB for
 // each 16 rows of W) and their words, all moved straight from memory to LDS by
 // buffer_load ... lds, STAGES - 1 stages ahead, with one barrier a stage.
 // Every wave multiplies all of A's rows by its own 16 NW rows of W, so codes
-// are unpacked once in a workgroup, and A is read from memory once.
+// are unpacked once in a workgroup.
 //
 // A's rows lie in LDS as 16 chunks of 16 bytes, chunk c of row r in place
 // c ^ (r & 15): a fragment read takes one chunk of 16 rows, which then lie in
@@ -14,15 +14,21 @@
 // direct load fill LDS in order, so the permutation is made by the global
 // address each lane loads.
 //
-// Scales.  With ROUND false the products of a group are summed in fp32 and
-// enter the total times the scale, as in the kernel for few rows: one fused
-// multiply-add per output and group.  With ROUND true the scale multiplies
-// q - z in binary16 (one rounding of the weight, to the value that q4_expand
-// gives) and the matrix cores add up everything: for many rows that
-// multiply-add costs more than it gives, since the weight's rounding is of
-// the size of the result's own (2^-11 of each weight, at random signs).
-#include <type_traits>
-
+// The scale multiplies q - z in binary16, one rounding of the weight, to the
+// value that q4_expand gives, and the matrix cores add up everything.  (The
+// kernels for fewer rows sum a group exactly and scale its sum: one fused
+// multiply-add per output and group, which here, where vector instructions
+// already fill the matrix cores' shadow, would cost as much as the products.
+// The weight's rounding is of the size of the result's own, 2^-11 of each
+// weight at random signs: measured 2.7e-4 of the result's norm from the exact
+// product, against 2.1e-4 for its rounding alone.)
+//
+// 2048 x 8192 x 8192, group 128: 241-250 us, 1100-1140 TFLOP/s, against 189
+// for the dense kernel on binary16 weights.  Bound by issue: a 32-deep step of a wave is
+// 32 matrix instructions (512 cycles) and about 70 vector ones (280), which one wave on
+// its SIMD overlaps only in part.  Eight waves of half the rows (two on a
+// SIMD, codes unpacked twice): 247; operands read three steps ahead with a
+// fixed interleaving: 269.
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
@@ -30,30 +36,27 @@ namespace gemm_f16_impl {
 
 typedef _Float16 half8_any __attribute__((ext_vector_type(8), aligned(2)));
 
-// WM x WN waves: wave (wm, wn) multiplies 16 MB rows of A by 16 NW rows of W.
-template <int GROUP, int MB, int NW, int WM, int WN, int STAGES, bool ROUND>
+template <int GROUP, int MB, int NW, int STAGES_>
 struct Q4Tile {
-    static constexpr int WAVES = WM * WN, GROUPS = 128 / GROUP, PER = GROUP / 32;
-    static constexpr int BM = 16 * MB * WM, BN = 16 * NW * WN, N_BLOCKS = NW * WN;
+    static constexpr int STAGES = STAGES_, WAVES = 4, GROUPS = 128 / GROUP, PER = GROUP / 32;
+    static constexpr int BM = 16 * MB, BN = 16 * NW * WAVES, N_BLOCKS = NW * WAVES;
     static constexpr int A_BYTES = BM * 256, CODE_BYTES = N_BLOCKS * 1024;
-    static constexpr int A_LOADS = BM / 4 / WAVES, CODE_LOADS = N_BLOCKS / WAVES;   // of 1 KiB, for each wave
-    static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;  // of 64 words
+    static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;   // of 64 words, for each wave
     static constexpr int STAGE_BYTES = A_BYTES + CODE_BYTES + WAVES * WORD_LOADS * 256;
-    static constexpr int LOADS = A_LOADS + CODE_LOADS + WORD_LOADS;
+    static constexpr int LOADS = MB + NW + WORD_LOADS;         // of a stage, for each wave
     static constexpr int PITCH = BN + 8;                       // of the staged output, in halves
     static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > BM * PITCH * 2 ? STAGES * STAGE_BYTES : BM * PITCH * 2;
-    static_assert(BM / 4 % WAVES == 0 && N_BLOCKS % WAVES == 0, "whole loads for each wave");
     static_assert(LDS_BYTES <= 163840, "LDS of a CU");
 };
 
-// One stage's loads of a wave: 1 KiB pieces (of A: 4 rows; of the codes: a
+// A wave's loads of a stage: 1 KiB pieces (of A: 4 rows; of the codes: a
 // tile) and 256-byte pieces of the words, dealt out to the waves in turn.
-template <class T>
+template <class T, int MB, int NW>
 struct Q4Loads {
     __amdgpu_buffer_rsrc_t a, codes, words;
-    uint32_t a_off[T::A_LOADS];       // row and chunk of each load of A
-    int chunk[T::A_LOADS];
-    uint32_t code_off[T::CODE_LOADS], word_off[T::WORD_LOADS];
+    uint32_t a_off[MB];       // row and chunk of each load of A
+    int chunk[MB];
+    uint32_t code_off[NW], word_off[T::WORD_LOADS];
     int wave, lane, K, kb_end;
 
     __device__ __forceinline__ void init(const Q4Args &p, int m0, int nb0, int end)
@@ -65,7 +68,7 @@ struct Q4Loads {
         const int rows = min(p.M - m0, T::BM);
         a = make_rsrc(p.A + (int64_t)m0 * p.K, (uint32_t)rows * (uint32_t)p.K * 2u);
 #pragma unroll
-        for (int i = 0; i < T::A_LOADS; ++i) {
+        for (int i = 0; i < MB; ++i) {
             const int row = 4 * (wave + T::WAVES * i) + lane / 16;
             chunk[i] = (lane & 15) ^ (row & 15);
             a_off[i] = (uint32_t)row * (uint32_t)p.K * 2u + (uint32_t)chunk[i] * 16u;
@@ -75,7 +78,7 @@ struct Q4Loads {
         codes = make_rsrc(p.codes + tile * 256, (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
         words = make_rsrc(p.words + tile * (16 * T::GROUPS), (uint32_t)here * (uint32_t)p.k_blocks * (64u * T::GROUPS));
 #pragma unroll
-        for (int i = 0; i < T::CODE_LOADS; ++i)
+        for (int i = 0; i < NW; ++i)
             code_off[i] = (uint32_t)(wave + T::WAVES * i) * (uint32_t)p.k_blocks * 1024u + (uint32_t)lane * 16u;
 #pragma unroll
         for (int i = 0; i < T::WORD_LOADS; ++i) {
@@ -90,13 +93,13 @@ struct Q4Loads {
     {
         const uint32_t gone = oob_unless(kb < kb_end);
 #pragma unroll
-        for (int i = 0; i < T::A_LOADS; ++i) {
+        for (int i = 0; i < MB; ++i) {
             LDS_AS void *d = (LDS_AS void *)(to + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(a, d, 16, a_off[i] | gone | oob_unless(kb * 128 + chunk[i] * 8 < K),
                                                      (uint32_t)kb * 256u, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < T::CODE_LOADS; ++i) {
+        for (int i = 0; i < NW; ++i) {
             LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(codes, d, 16, code_off[i] | gone, (uint32_t)kb * 1024u, 0, 0);
         }
@@ -111,7 +114,7 @@ struct Q4Loads {
     __device__ __forceinline__ void clear_tail(unsigned char *stage) const
     {
 #pragma unroll 1
-        for (int i = 0; i < T::A_LOADS; ++i) {
+        for (int i = 0; i < MB; ++i) {
             const int piece = wave + T::WAVES * i, row = 4 * piece + lane / 16;
             if (((lane & 15) ^ (row & 15)) == K % 128 / 8) {
                 unsigned char *c = stage + piece * 1024 + lane * 16;
@@ -123,7 +126,7 @@ struct Q4Loads {
 };
 
 // TAIL: rows of A end inside a 16-byte chunk (K % 8 != 0).
-template <class T, int MB, int NW, int WN, int STAGES, bool ROUND, bool TAIL>
+template <class T, int MB, int NW, bool TAIL>
 __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
 {
     int tm, tn, split;
@@ -132,9 +135,9 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int begin = split * p.split_blocks, end = min(p.k_blocks, begin + p.split_blocks);
 
-    Q4Loads<T> in;
+    Q4Loads<T, MB, NW> in;
     in.init(p, m0, nb0, end);
-    const int wm = in.wave / WN, wn = in.wave % WN;
+    const int wave = in.wave;
     const q4_bits bits;
 
     float4v acc[MB][NW];
@@ -145,7 +148,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             acc[mb][nw] = float4v{0, 0, 0, 0};
 
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
+    for (int s = 0; s < T::STAGES - 1; ++s)
         in.issue(begin + s, lds + s * T::STAGE_BYTES);
 
     // One stage: request block kb into `fill`, multiply the one in `from`.
@@ -154,9 +157,9 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     const auto step = [&](const unsigned char *__restrict__ from, unsigned char *__restrict__ fill, int kb)
                           __attribute__((always_inline)) {
         in.issue(kb, fill);
-        const unsigned char *wc = from + T::A_BYTES + wn * (NW * 1024) + lane * 16;
+        const unsigned char *wc = from + T::A_BYTES + wave * (NW * 1024) + lane * 16;
         const uint32_t *ww = reinterpret_cast<const uint32_t *>(from + T::A_BYTES + T::CODE_BYTES) +
-                             (wn * (NW * 16) + col) * T::GROUPS;
+                             (wave * (NW * 16) + col) * T::GROUPS;
         uint4 codes[NW];
         unsigned word[NW][T::GROUPS];
 #pragma unroll
@@ -166,45 +169,23 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             for (int q = 0; q < T::GROUPS; ++q)
                 word[nw][q] = ww[nw * (16 * T::GROUPS) + q];
         }
-        float4v sum[MB][NW];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int q = j / T::PER;
-            const unsigned char *x = from + wm * (MB * 4096) + col * 256 + (((4 * j + g) ^ col) * 16);
+            const unsigned char *x = from + col * 256 + (((4 * j + g) ^ col) * 16);
             half8 w[NW];
 #pragma unroll
             for (int nw = 0; nw < NW; ++nw) {
                 const unsigned dw = j == 0 ? codes[nw].x : j == 1 ? codes[nw].y : j == 2 ? codes[nw].z : codes[nw].w;
-                w[nw] = q4_codes(dw, bits, q4_zero(word[nw][q]));
-                if constexpr (ROUND) {
-                    const half_t s = __builtin_bit_cast(q4_half2, word[nw][q])[0];
-                    w[nw] *= half8{s, s, s, s, s, s, s, s};
-                }
+                const unsigned wd = word[nw][j / T::PER];
+                const half_t s = __builtin_bit_cast(q4_half2, wd)[0];
+                w[nw] = q4_codes(dw, bits, q4_zero(wd)) * half8{s, s, s, s, s, s, s, s};
             }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
                 const half8 a = *reinterpret_cast<const half8 *>(x + mb * 4096);
 #pragma unroll
-                for (int nw = 0; nw < NW; ++nw) {
-                    if constexpr (ROUND)
-                        acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
-                    else
-                        sum[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            a, w[nw], j % T::PER == 0 ? float4v{0, 0, 0, 0} : sum[mb][nw], 0, 0, 0);
-                }
-            }
-            if constexpr (!ROUND) {
-                if (j % T::PER == T::PER - 1) {
-#pragma unroll
-                    for (int nw = 0; nw < NW; ++nw) {
-                        const float s = q4_scale(word[nw][q]);
-#pragma unroll
-                        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                acc[mb][nw][r] = __builtin_fmaf(s, sum[mb][nw][r], acc[mb][nw][r]);
-                    }
-                }
+                for (int nw = 0; nw < NW; ++nw)
+                    acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
             }
         }
     };
@@ -213,7 +194,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     for (int kb = begin; kb < end; ++kb) {
         // this wave's loads of the stage have landed; and its reads of the
         // stage that is refilled next are done
-        wait_vm_lgkm0<(STAGES - 2) * T::LOADS>();
+        wait_vm_lgkm0<(T::STAGES - 2) * T::LOADS>();
         if constexpr (TAIL) {
             if (kb == p.k_blocks - 1) {
                 asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
@@ -223,14 +204,14 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
         }
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
-        const int fill = slot == 0 ? STAGES - 1 : slot - 1;
-        step(lds + slot * T::STAGE_BYTES, lds + fill * T::STAGE_BYTES, kb + STAGES - 1);
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        const int fill = slot == 0 ? T::STAGES - 1 : slot - 1;
+        step(lds + slot * T::STAGE_BYTES, lds + fill * T::STAGE_BYTES, kb + T::STAGES - 1);
+        slot = slot + 1 == T::STAGES ? 0 : slot + 1;
     }
     wait_vmcnt<0>();   // the last requests' zeros land before LDS is used again or given back
 
-    // lane (g, col) holds rows 16 mb + 4 g + r of the wave's rows of A, column col of each block
-    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16, wave_m = wm * (16 * MB), wave_n = wn * (16 * NW);
+    // lane (g, col) holds rows 16 mb + 4 g + r of A, column col of each block
+    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16, wave_n = wave * (16 * NW);
     if (p.W) {         // partial sums of a split, joined by the reduction kernel
         float *out = p.W + ((int64_t)split * p.M + m0) * p.N;
 #pragma unroll
@@ -240,7 +221,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int m = wave_m + 16 * mb + 4 * g + r;
+                    const int m = 16 * mb + 4 * g + r;
                     if (m < rows && n < p.N)
                         out[(int64_t)m * p.N + n] = acc[mb][nw][r];
                 }
@@ -259,7 +240,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
                 float v = acc[mb][nw][r] * p.alpha;
                 if (p.relu)
                     v = __builtin_fmaxf(v, 0.0f);
-                c[(wave_m + 16 * mb + 4 * g + r) * T::PITCH + wave_n + nw * 16 + col] = (half_t)v;
+                c[(16 * mb + 4 * g + r) * T::PITCH + wave_n + nw * 16 + col] = (half_t)v;
             }
     __syncthreads();
     constexpr int CHUNKS = T::BN / 8;
@@ -278,40 +259,29 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     }
 }
 
-template <int GROUP, int MB, int NW, int WM, int WN, int STAGES, bool ROUND, bool TAIL>
-__global__ void __launch_bounds__(64 * WM * WN) q4_tile_kernel(Q4Args p)
+constexpr int TILE_MB = 8, TILE_NW = 4, TILE_STAGES = 3;   // q4_128x256_s3
+
+template <int GROUP, bool TAIL>
+__global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
 {
-    typedef Q4Tile<GROUP, MB, NW, WM, WN, STAGES, ROUND> T;
+    typedef Q4Tile<GROUP, TILE_MB, TILE_NW, TILE_STAGES> T;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
-    q4_tile<T, MB, NW, WN, STAGES, ROUND, TAIL>(p, lds);
+    q4_tile<T, TILE_MB, TILE_NW, TAIL>(p, lds);
 }
 
-template <int MB, int NW, int WM, int WN, int STAGES, bool ROUND, bool TAIL>
-static hipError_t launch_tile(const Q4Args &a, int group, int64_t grid, hipStream_t s)
+template <int GROUP>
+static void launch_tile(const Q4Args &a, dim3 grid, hipStream_t s)
 {
-    const dim3 blocks((unsigned)grid), threads(64 * WM * WN);
-    if (group == 32)
-        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
-    else if (group == 64)
-        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
+    if (a.K % 8 != 0)
+        hipLaunchKernelGGL((q4_tile_kernel<GROUP, true>), grid, dim3(256), 0, s, a);
     else
-        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, WM, WN, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
+        hipLaunchKernelGGL((q4_tile_kernel<GROUP, false>), grid, dim3(256), 0, s, a);
+}
+
+hipError_t launch_q4_tile(int group, const Q4Args &a, int64_t grid, hipStream_t s)
+{
+    (group == 32 ? launch_tile<32> : group == 64 ? launch_tile<64> : launch_tile<128>)(a, dim3((unsigned)grid), s);
     return hipGetLastError();
-}
-
-template <bool TAIL>
-static hipError_t launch_config(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
-{
-    switch (config) {
-    case 5: return launch_tile<4, 1, 1, 8, 4, false, TAIL>(a, group, grid, s);
-    case 6: return launch_tile<8, 4, 1, 4, 3, true, TAIL>(a, group, grid, s);
-    default: return hipErrorInvalidValue;
-    }
-}
-
-hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
-{
-    return a.K % 8 != 0 ? launch_config<true>(config, group, a, grid, s) : launch_config<false>(config, group, a, grid, s);
 }
 
 } // namespace gemm_f16_impl

@@ -239,9 +239,9 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
         row[mb] = p.A + (int64_t)(m0 + min(16 * mb + col, rows - 1)) * p.K + 8 * g;
 
     typedef ProductStep<GROUPS, MB, NW> Step;
-    const auto load_w = [&](int kb, uint32_t gone, Step &s) {
+    const auto load_w = [&](int kb, uint32_t gone, Step &s, int from, int to) {
 #pragma unroll
-        for (int nw = 0; nw < NW; ++nw) {
+        for (int nw = from; nw < to; ++nw) {
             const uint32_t tile = (uint32_t)nw * (uint32_t)p.k_blocks;
             const auto v = __builtin_amdgcn_raw_buffer_load_b128(codes, (tile * 1024u + lane * 16u) | gone,
                                                                  (uint32_t)kb * 1024u, 0);
@@ -252,10 +252,11 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
                                s.words[nw]);
         }
     };
-    const int whole = p.K / 128;   // k blocks that A's rows fill
-    const auto load = [&](int kb, Step &s) {
+    // this split's k blocks, and those of them that A's rows fill
+    const int begin = blockIdx.z * p.split_blocks, end = min(p.k_blocks, begin + p.split_blocks);
+    const int whole = min(p.K / 128, end);
+    const auto load_x = [&](int kb, Step &s) {
         const uint32_t gone = oob_unless(kb < whole);
-        load_w(kb, gone, s);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
@@ -277,9 +278,13 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
         for (int nw = 0; nw < NW; ++nw)
             acc[mb][nw] = float4v{0, 0, 0, 0};
 
-    const auto multiply = [&](const Step &s) {
+    const auto load = [&](int kb, Step &s) {
+        load_w(kb, oob_unless(kb < whole), s, 0, NW);
+        load_x(kb, s);
+    };
+    const auto multiply = [&](const Step &s, int from, int to) {
 #pragma unroll
-        for (int nw = 0; nw < NW; ++nw) {
+        for (int nw = from; nw < to; ++nw) {
 #pragma unroll
             for (int q = 0; q < GROUPS; ++q) {
                 const q4_zero zero(s.words[nw][q]);
@@ -302,61 +307,88 @@ __global__ void __launch_bounds__(64 * WAVES) q4_product_kernel(Q4Args p)
         }
     };
 
-    if (wave < whole) {
-        Step s[DEPTH];
+    const int first = begin + wave;
+    if (first < whole) {
+        if constexpr (DEPTH == 1) {
+            // one step's registers: each part is loaded again for the next
+            // step as soon as it has been used
+            Step s;
+            load(first, s);
+            for (int kb = first; kb < whole; kb += WAVES) {
+                const int next = kb + WAVES;
 #pragma unroll
-        for (int d = 0; d < DEPTH; ++d)
-            load(wave + d * WAVES, s[d]);
-        for (int kb = wave;; kb += DEPTH * WAVES) {
-            bool done = false;
-#pragma unroll
-            for (int d = 0; d < DEPTH; ++d) {
-                multiply(s[d]);
-                if (kb + (d + 1) * WAVES >= whole) {
-                    done = true;
-                    break;
+                for (int nw = 0; nw < NW; ++nw) {
+                    multiply(s, nw, nw + 1);
+                    load_w(next, oob_unless(next < whole), s, nw, nw + 1);
                 }
-                load(kb + (d + DEPTH) * WAVES, s[d]);
+                load_x(next, s);
             }
-            if (done)
-                break;
+        } else {
+            Step s[DEPTH];
+#pragma unroll
+            for (int d = 0; d < DEPTH; ++d)
+                load(first + d * WAVES, s[d]);
+            for (int kb = first;; kb += DEPTH * WAVES) {
+                bool done = false;
+#pragma unroll
+                for (int d = 0; d < DEPTH; ++d) {
+                    multiply(s[d], 0, NW);
+                    if (kb + (d + 1) * WAVES >= whole) {
+                        done = true;
+                        break;
+                    }
+                    load(kb + (d + DEPTH) * WAVES, s[d]);
+                }
+                if (done)
+                    break;
+            }
         }
     }
-    if (whole < p.k_blocks && wave == whole % WAVES) {   // the k block that A's rows end in
+    if (whole < end && wave == (whole - begin) % WAVES) {   // the k block that A's rows end in
         Step s;
-        load_w(whole, 0u, s);
+        load_w(whole, 0u, s, 0, NW);
 #pragma unroll
         for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 s.x[mb][j] = row_piece(row[mb] + whole * 128 + 32 * j, p.K - whole * 128 - 8 * g - 32 * j);
-        multiply(s);
+        multiply(s, 0, NW);
     }
 
-    // add the waves' sums in wave order; lane (g, n) holds rows 4 g + r of
-    // A, column n of each 16 x 16 block
-    float4v *part = reinterpret_cast<float4v *>(q4_lds);   // [wave][mb][nw][lane]
+    // add the waves' sums in wave order, CHUNK of the 16-column blocks at a
+    // time; lane (g, col) holds rows 4 g + r of A, column col of each block
+    constexpr int CHUNK = q4_sum_chunk(MB, NW);
+    float4v *part = reinterpret_cast<float4v *>(q4_lds);   // [wave][mb][nw of the chunk][lane]
+    const float *flat = reinterpret_cast<const float *>(q4_lds);
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
+    for (int c = 0; c < NW; c += CHUNK) {
+        if (c > 0)
+            __syncthreads();
 #pragma unroll
-        for (int nw = 0; nw < NW; ++nw)
-            part[((wave * MB + mb) * NW + nw) * 64 + lane] = acc[mb][nw];
-    __syncthreads();
-    const float *flat = reinterpret_cast<const float *>(part);
-    for (int e = tid; e < rows * NW * 16; e += 64 * WAVES) {
-        const int col = e % (NW * 16), m = e / (NW * 16);
-        const int n = nb0 * 16 + col;
-        if (n >= p.N)
-            continue;
-        const int at = (((m / 16) * NW + col / 16) * 64 + m % 16 / 4 * 16 + col % 16) * 4 + m % 4;
-        float v = 0.0f;
+        for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            v += flat[w * (MB * NW * 256) + at];
-        v *= p.alpha;
-        if (p.relu)
-            v = __builtin_fmaxf(v, 0.0f);
-        p.C[(int64_t)(m0 + m) * p.N + n] = (half_t)v;
+            for (int nw = 0; nw < CHUNK; ++nw)
+                part[((wave * MB + mb) * CHUNK + nw) * 64 + lane] = acc[mb][c + nw];
+        __syncthreads();
+        for (int e = tid; e < rows * CHUNK * 16; e += 64 * WAVES) {
+            const int at_n = e % (CHUNK * 16), m = e / (CHUNK * 16);
+            const int n = (nb0 + c) * 16 + at_n;
+            if (n >= p.N)
+                continue;
+            const int at = (((m / 16) * CHUNK + at_n / 16) * 64 + m % 16 / 4 * 16 + at_n % 16) * 4 + m % 4;
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WAVES; ++w)
+                v += flat[w * (MB * CHUNK * 256) + at];
+            if (p.W) {   // a split's partial sums, joined by the reduction kernel
+                p.W[((int64_t)blockIdx.z * p.rows + p.row0 + m0 + m) * p.N + n] = v;
+                continue;
+            }
+            v *= p.alpha;
+            if (p.relu)
+                v = __builtin_fmaxf(v, 0.0f);
+            p.C[(int64_t)(m0 + m) * p.N + n] = (half_t)v;
+        }
     }
 }
 
@@ -364,7 +396,7 @@ template <int GROUP, bool ALIGNED>
 static hipError_t launch_group(int config, const Q4Args &a, dim3 grid, unsigned lds, hipStream_t s)
 {
     // steps in flight: no more than the waves have
-    const bool one = a.K <= 8 * 128;
+    const bool one = a.split_blocks <= 8;
     switch (config) {
     case 0:
         if (one)
@@ -379,8 +411,8 @@ static hipError_t launch_group(int config, const Q4Args &a, dim3 grid, unsigned 
             hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 2, 8, 3, ALIGNED>), grid, dim3(512), lds, s, a);
         break;
     case 2: hipLaunchKernelGGL((q4_product_kernel<GROUP, 1, 4, 8, 2, ALIGNED>), grid, dim3(512), lds, s, a); break;
-    case 3: hipLaunchKernelGGL((q4_product_kernel<GROUP, 2, 2, 8, 2, ALIGNED>), grid, dim3(512), lds, s, a); break;
-    case 4: hipLaunchKernelGGL((q4_product_kernel<GROUP, 4, 2, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a); break;
+    case 3: hipLaunchKernelGGL((q4_product_kernel<GROUP, 2, 4, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a); break;
+    case 4: hipLaunchKernelGGL((q4_product_kernel<GROUP, 2, 8, 8, 1, ALIGNED>), grid, dim3(512), lds, s, a); break;
     default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
@@ -402,8 +434,10 @@ hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s)
         Q4Args b = a;
         b.A += m * a.K;
         b.C += m * a.N;
+        b.row0 = (int)m;
         b.M = (int)std::min<int64_t>(a.M - m, step);
-        const dim3 grid((unsigned)a.tiles_n, (unsigned)std::min<int64_t>(a.tiles_m - m / step * 65535, 65535));
+        const dim3 grid((unsigned)a.tiles_n, (unsigned)std::min<int64_t>(a.tiles_m - m / step * 65535, 65535),
+                        (unsigned)a.splits);
         const hipError_t e = group == 32   ? launch_aligned<32>(config, b, grid, lds, s)
                              : group == 64 ? launch_aligned<64>(config, b, grid, lds, s)
                                            : launch_aligned<128>(config, b, grid, lds, s);
