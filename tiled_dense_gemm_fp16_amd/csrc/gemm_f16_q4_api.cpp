@@ -19,6 +19,7 @@ const Q4Config kQ4Configs[kNumQ4Configs] = {
     {"q4_16x64", 1, 4, 8, 0},
     {"q4_32x64", 2, 4, 8, 0},
     {"q4_32x128", 2, 8, 8, 0},
+    {"q4_64x128_s4", 4, 8, 8, 4},
     {"q4_128x256_s3", 8, 16, 4, 3},
 };
 
@@ -60,32 +61,34 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     if ((config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumQ4Configs)) || splits < 0 ||
         splits > GEMM_F16_MAX_SPLITS)
         return GEMM_F16_ERROR_INVALID_VALUE;
-    // Wider workgroups read A and W less often, but leave CUs idle when they
-    // are few: the widest one that makes 150 workgroups.  us at (M, N x K) for
-    // 16x16 / 16x32 / 16x64 / 32x64 / 32x128, * the choice: (1, 4096 x 4096) *4.4 / 5.6 / 7.5;
-    // (1, 8192 x 8192) 11.1 / *10.6 / 14.6; (1, 28672 x 8192) 35.4 / 28.3 / *26.2; (16, 28672 x
-    // 8192) 57.4 / 41.1 / *33.1; (16, 5000 x 4100) 9.1 / *7.5 / 8.7; (48, 5000 x 4100) 14.8 / 11.5 /
-    // 10.2 / *11.9 / 14.8; (64, 8192 x 8192) 63.3 / 37.5 / 26.2 / *21.7 / 28.3; (128, 8192 x 8192) - /
-    // - / 45.4 / 38.9 / *28.5.
+    // Few rows.  Wider workgroups read A and W less often, but leave CUs idle
+    // when they are few: the widest one that makes 150 workgroups.  us at (M, N x
+    // K) for 16x16 / 16x32 / 16x64 / 32x64 / 32x128, * the choice: (1, 4096 x 4096) *4.4 /
+    // 5.6 / 7.5; (1, 8192 x 8192) 11.1 / *10.6 / 14.6; (1, 28672 x 8192) 35.4 / 28.3 / *26.2;
+    // (16, 28672 x 8192) 57.4 / 41.1 / *33.1; (16, 5000 x 4100) 9.1 / *7.5 / 8.7; (48, 5000 x 4100)
+    // 14.8 / 11.5 / 10.2 / *11.9 / 14.8; (64, 4096 x 4096) - / - / *9.0 / 10.7 / 13.3.
     // With 64 blocks of K or more, splitting K beats narrower workgroups:
     // (24, 2048 x 16384) 18.1 / 13.5 / 12.0 / *11.9 / 13.9; (24, 8192 x 8192) 29.2 / 19.1 /
-    // 15.8 / *14.4 / 16.7.
+    // 15.8 / *14.4 / 16.7; and from 33 rows the 64x128 tile does (us, best of the
+    // others): (48, 8192 x 8192) 19.2, 21.3; (64, 28672 x 8192) 49.9, 62.2; (128, 4096 x 14336)
+    // 27.7, 29.2; but (32, 8192 x 8192) 18.1, 16.4 and (64, 5000 x 4100) 12.9, 12.6.
     // The 128x256 tile takes over where it makes 64 workgroups for more than
-    // 64 rows (us with it against the best of the others): (100, 28672 x 8192)
-    // 71 / 104, (200, 8192 x 8192) 43 / 52, (2048, 8192 x 8192) 238 / 392; fewer:
-    // (200, 4096 x 4096) 27 / 16, (128, 8192 x 8192) 32 / 28; fewer rows: (48, 28672 x 8192) 67 / 55.
+    // 64 rows: (100, 28672 x 8192) 72, 93; (200, 8192 x 8192) 43, 52; (2048, 8192 x 8192) 240, 350;
+    // but (200, 4096 x 4096) 27, 16, (128, 8192 x 8192) 32, 29 and (64, 28672 x 8192) 69, 50.
     const int64_t n_blocks = (N + 15) / 16, blocks = (K + 127) / 128;
-    const int tile = kNumQ4Configs - 1, most_m = M > 16 ? 2 : 1;
+    const int large = kNumQ4Configs - 1, most_m = M > 16 ? 2 : 1;
     const auto count = [&](int i) {
         const int64_t m = 16 * kQ4Configs[i].m_blocks, n = kQ4Configs[i].n_blocks;
         return (M + m - 1) / m * ((n_blocks + n - 1) / n);
     };
     int c = config;
     if (c == GEMM_F16_CONFIG_AUTO) {
-        if (aligned && M > 64 && count(tile) >= 64) {
-            c = tile;
+        if (aligned && M > 64 && count(large) >= 64) {
+            c = large;
+        } else if (aligned && M > 32 && blocks >= 64) {
+            c = large - 1;
         } else {
-            for (c = tile - 1; c > 0; --c)
+            for (c = large - 2; c > 0; --c)
                 if (kQ4Configs[c].m_blocks <= most_m && count(c) >= 150)
                     break;
             if (M > 8 && blocks >= 64)
@@ -111,7 +114,7 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     const int64_t tiles = p->tiles_m * p->tiles_n;
     if (splits == GEMM_F16_SPLITS_AUTO) {
         splits = 1;
-        if (M > 8 && tiles > 0 && tiles < 150)   // a part keeps 8 blocks, two for each wave of the kernel for few rows
+        if (M > 8 && tiles > 0 && tiles < (d.stages > 0 ? 256 : 150))   // a part keeps 8 blocks, two for each wave of the kernel for few rows
             splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / (d.stages > 0 ? 8 : 16)),
                                                                  GEMM_F16_MAX_SPLITS));
     }
@@ -379,7 +382,7 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     a.relu = epilogue == GEMM_F16_EPILOGUE_RELU ? 1 : 0;
     const hipError_t e = kQ4Configs[plan.config].stages == 0
                              ? launch_q4(plan.config, group, a, (hipStream_t)stream)
-                             : launch_q4_tile(group, a, plan.grid, (hipStream_t)stream);
+                             : launch_q4_tile(plan.config, group, a, plan.grid, (hipStream_t)stream);
     if (e != hipSuccess || plan.splits == 1)
         return status_of(e);
     return status_of(launch_reduce(a.W, a.C, M, N, plan.splits, a.alpha, a.relu, N % 4 == 0 && (uintptr_t)C % 8 == 0,

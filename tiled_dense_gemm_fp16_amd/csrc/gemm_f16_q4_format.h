@@ -32,7 +32,7 @@ struct Q4Config {
     int waves;
     int stages;              // LDS stages of the tile kernel, each of 128 k; 0: the kernel for few rows
 };
-constexpr int kNumQ4Configs = 6;
+constexpr int kNumQ4Configs = 7;
 extern const Q4Config kQ4Configs[kNumQ4Configs];
 
 // The kernel for few rows adds its waves' sums this many 16-column blocks at
@@ -42,7 +42,7 @@ int64_t q4_lds_bytes(const Q4Config &c, int group);
 // The kernel for few rows: tiles_n x tiles_m x splits workgroups.
 hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s);
 // The tile kernel: tiles_m x tiles_n x splits workgroups; A's rows 4-byte aligned.
-hipError_t launch_q4_tile(int group, const Q4Args &a, int64_t grid, hipStream_t s);
+hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s);
 hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *words, int64_t N, int64_t K, int group,
                               bool symmetric, hipStream_t s);
 hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float16 *W, int64_t N, int64_t K, int group,

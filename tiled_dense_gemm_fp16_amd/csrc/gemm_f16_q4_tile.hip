@@ -1,12 +1,13 @@
 // gemm_f16_q4_tile.hip -- the product with 4-bit weights, C = epi(alpha A W^T),
-// for many rows of A: LDS-staged tiles, bound by the matrix cores.
+// LDS-staged tiles: for many rows of A, bound by the matrix cores, and for the
+// few dozen rows where K is split.
 //
-// A workgroup of 4 waves owns 16 MB rows of A and 64 NW rows of W.  A stage
+// A workgroup owns 16 MB rows of A and 16 NW rows of W for each of its waves.  A stage
 // holds 128 k: A's rows (256 bytes each), the waves' tiles of codes (1 KiB for
 // each 16 rows of W) and their words, all moved straight from memory to LDS by
 // buffer_load ... lds, STAGES - 1 stages ahead, with one barrier a stage.
-// Every wave multiplies all of A's rows by its own 16 NW rows of W, so codes
-// are unpacked once in a workgroup.
+// Every wave multiplies all of A's rows by its own rows of W, so codes are
+// unpacked once in a workgroup.
 //
 // A's rows lie in LDS as 16 chunks of 16 bytes, chunk c of row r in place
 // c ^ (r & 15): a fragment read takes one chunk of 16 rows, which then lie in
@@ -14,21 +15,28 @@
 // direct load fill LDS in order, so the permutation is made by the global
 // address each lane loads.
 //
-// The scale multiplies q - z in binary16, one rounding of the weight, to the
-// value that q4_expand gives, and the matrix cores add up everything.  (The
-// kernels for fewer rows sum a group exactly and scale its sum: one fused
-// multiply-add per output and group, which here, where vector instructions
-// already fill the matrix cores' shadow, would cost as much as the products.
-// The weight's rounding is of the size of the result's own, 2^-11 of each
-// weight at random signs: measured 2.7e-4 of the result's norm from the exact
-// product, against 2.1e-4 for its rounding alone.)
+// Scales.  With ROUND false the products of a group are summed in fp32 and
+// enter the total times the scale, as in the kernel for few rows: one fused
+// multiply-add per output and group.  With ROUND true the scale multiplies
+// q - z in binary16, one rounding of the weight, to the value that q4_expand
+// gives, and the matrix cores add up everything: for many rows vector
+// instructions already fill the matrix cores' shadow, and that multiply-add
+// would cost as much as the products.  The weight's rounding is of the size of
+// the result's own, 2^-11 of each weight at random signs: measured 2.7e-4 of
+// the result's norm from the exact product, against 2.1e-4 for its rounding alone.
 //
-// 2048 x 8192 x 8192, group 128: 241-250 us, 1100-1140 TFLOP/s, against 189
-// for the dense kernel on binary16 weights.  Bound by issue: a 32-deep step of a wave is
-// 32 matrix instructions (512 cycles) and about 70 vector ones (280), which one wave on
-// its SIMD overlaps only in part.  Eight waves of half the rows (two on a
-// SIMD, codes unpacked twice): 247; operands read three steps ahead with a
-// fixed interleaving: 269.
+// q4_128x256_s3 (4 waves, ROUND): 2048 x 8192 x 8192, group 128, 238-250 us,
+// 1100-1150 TFLOP/s, against 189 us for the dense kernel on binary16 weights.
+// Bound by issue: a 32-deep step of a wave is 32 matrix instructions (512
+// cycles) and about 70 vector ones (280), which one wave on its SIMD overlaps
+// only in part.  Eight waves of half the rows (two on a SIMD, codes unpacked
+// twice): 247; operands read three steps ahead with a fixed interleaving: 269.
+//
+// q4_64x128_s4 (8 waves): 64 x 8192 x 8192, group 64, in four parts of K, 14-16 us
+// and 4 for their sum.  Bound by what a CU takes from the L2: 256 KiB of A
+// and 128 of codes for each workgroup, at 27-32 KB a us.  Unsplit workgroups of
+// the kernel for few rows read 750 KiB: 22-25 us.  4 waves of 32 rows of W:
+// 24; 2 x 4 waves: 22; codes 8 stages ahead by waves of their own: 22.
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
@@ -36,27 +44,29 @@ namespace gemm_f16_impl {
 
 typedef _Float16 half8_any __attribute__((ext_vector_type(8), aligned(2)));
 
-template <int GROUP, int MB, int NW, int STAGES_>
+template <int GROUP, int MB, int NW, int WAVES_, int STAGES_, bool ROUND>
 struct Q4Tile {
-    static constexpr int STAGES = STAGES_, WAVES = 4, GROUPS = 128 / GROUP, PER = GROUP / 32;
+    static constexpr int WAVES = WAVES_, STAGES = STAGES_, GROUPS = 128 / GROUP, PER = GROUP / 32;
     static constexpr int BM = 16 * MB, BN = 16 * NW * WAVES, N_BLOCKS = NW * WAVES;
     static constexpr int A_BYTES = BM * 256, CODE_BYTES = N_BLOCKS * 1024;
-    static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;   // of 64 words, for each wave
+    static constexpr int A_LOADS = BM / 4 / WAVES, CODE_LOADS = N_BLOCKS / WAVES;   // of 1 KiB, for each wave
+    static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;  // of 64 words
     static constexpr int STAGE_BYTES = A_BYTES + CODE_BYTES + WAVES * WORD_LOADS * 256;
-    static constexpr int LOADS = MB + NW + WORD_LOADS;         // of a stage, for each wave
+    static constexpr int LOADS = A_LOADS + CODE_LOADS + WORD_LOADS;
     static constexpr int PITCH = BN + 8;                       // of the staged output, in halves
     static constexpr int LDS_BYTES = STAGES * STAGE_BYTES > BM * PITCH * 2 ? STAGES * STAGE_BYTES : BM * PITCH * 2;
+    static_assert(BM / 4 % WAVES == 0 && N_BLOCKS % WAVES == 0, "whole loads for each wave");
     static_assert(LDS_BYTES <= 163840, "LDS of a CU");
 };
 
-// A wave's loads of a stage: 1 KiB pieces (of A: 4 rows; of the codes: a
+// One stage's loads of a wave: 1 KiB pieces (of A: 4 rows; of the codes: a
 // tile) and 256-byte pieces of the words, dealt out to the waves in turn.
-template <class T, int MB, int NW>
+template <class T>
 struct Q4Loads {
     __amdgpu_buffer_rsrc_t a, codes, words;
-    uint32_t a_off[MB];       // row and chunk of each load of A
-    int chunk[MB];
-    uint32_t code_off[NW], word_off[T::WORD_LOADS];
+    uint32_t a_off[T::A_LOADS];       // row and chunk of each load of A
+    int chunk[T::A_LOADS];
+    uint32_t code_off[T::CODE_LOADS], word_off[T::WORD_LOADS];
     int wave, lane, K, kb_end;
 
     __device__ __forceinline__ void init(const Q4Args &p, int m0, int nb0, int end)
@@ -68,7 +78,7 @@ struct Q4Loads {
         const int rows = min(p.M - m0, T::BM);
         a = make_rsrc(p.A + (int64_t)m0 * p.K, (uint32_t)rows * (uint32_t)p.K * 2u);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < T::A_LOADS; ++i) {
             const int row = 4 * (wave + T::WAVES * i) + lane / 16;
             chunk[i] = (lane & 15) ^ (row & 15);
             a_off[i] = (uint32_t)row * (uint32_t)p.K * 2u + (uint32_t)chunk[i] * 16u;
@@ -78,7 +88,7 @@ struct Q4Loads {
         codes = make_rsrc(p.codes + tile * 256, (uint32_t)here * (uint32_t)p.k_blocks * 1024u);
         words = make_rsrc(p.words + tile * (16 * T::GROUPS), (uint32_t)here * (uint32_t)p.k_blocks * (64u * T::GROUPS));
 #pragma unroll
-        for (int i = 0; i < NW; ++i)
+        for (int i = 0; i < T::CODE_LOADS; ++i)
             code_off[i] = (uint32_t)(wave + T::WAVES * i) * (uint32_t)p.k_blocks * 1024u + (uint32_t)lane * 16u;
 #pragma unroll
         for (int i = 0; i < T::WORD_LOADS; ++i) {
@@ -93,13 +103,13 @@ struct Q4Loads {
     {
         const uint32_t gone = oob_unless(kb < kb_end);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < T::A_LOADS; ++i) {
             LDS_AS void *d = (LDS_AS void *)(to + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(a, d, 16, a_off[i] | gone | oob_unless(kb * 128 + chunk[i] * 8 < K),
                                                      (uint32_t)kb * 256u, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < NW; ++i) {
+        for (int i = 0; i < T::CODE_LOADS; ++i) {
             LDS_AS void *d = (LDS_AS void *)(to + T::A_BYTES + (wave + T::WAVES * i) * 1024);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(codes, d, 16, code_off[i] | gone, (uint32_t)kb * 1024u, 0, 0);
         }
@@ -114,7 +124,7 @@ struct Q4Loads {
     __device__ __forceinline__ void clear_tail(unsigned char *stage) const
     {
 #pragma unroll 1
-        for (int i = 0; i < MB; ++i) {
+        for (int i = 0; i < T::A_LOADS; ++i) {
             const int piece = wave + T::WAVES * i, row = 4 * piece + lane / 16;
             if (((lane & 15) ^ (row & 15)) == K % 128 / 8) {
                 unsigned char *c = stage + piece * 1024 + lane * 16;
@@ -126,7 +136,7 @@ struct Q4Loads {
 };
 
 // TAIL: rows of A end inside a 16-byte chunk (K % 8 != 0).
-template <class T, int MB, int NW, bool TAIL>
+template <class T, int MB, int NW, bool ROUND, bool TAIL>
 __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
 {
     int tm, tn, split;
@@ -135,7 +145,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int begin = split * p.split_blocks, end = min(p.k_blocks, begin + p.split_blocks);
 
-    Q4Loads<T, MB, NW> in;
+    Q4Loads<T> in;
     in.init(p, m0, nb0, end);
     const int wave = in.wave;
     const q4_bits bits;
@@ -169,23 +179,45 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             for (int q = 0; q < T::GROUPS; ++q)
                 word[nw][q] = ww[nw * (16 * T::GROUPS) + q];
         }
+        float4v sum[MB][NW];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+            const int q = j / T::PER;
             const unsigned char *x = from + col * 256 + (((4 * j + g) ^ col) * 16);
             half8 w[NW];
 #pragma unroll
             for (int nw = 0; nw < NW; ++nw) {
                 const unsigned dw = j == 0 ? codes[nw].x : j == 1 ? codes[nw].y : j == 2 ? codes[nw].z : codes[nw].w;
-                const unsigned wd = word[nw][j / T::PER];
-                const half_t s = __builtin_bit_cast(q4_half2, wd)[0];
-                w[nw] = q4_codes(dw, bits, q4_zero(wd)) * half8{s, s, s, s, s, s, s, s};
+                w[nw] = q4_codes(dw, bits, q4_zero(word[nw][q]));
+                if constexpr (ROUND) {
+                    const half_t s = __builtin_bit_cast(q4_half2, word[nw][q])[0];
+                    w[nw] *= half8{s, s, s, s, s, s, s, s};
+                }
             }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
                 const half8 a = *reinterpret_cast<const half8 *>(x + mb * 4096);
 #pragma unroll
-                for (int nw = 0; nw < NW; ++nw)
-                    acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
+                for (int nw = 0; nw < NW; ++nw) {
+                    if constexpr (ROUND)
+                        acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
+                    else
+                        sum[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                            a, w[nw], j % T::PER == 0 ? float4v{0, 0, 0, 0} : sum[mb][nw], 0, 0, 0);
+                }
+            }
+            if constexpr (!ROUND) {
+                if (j % T::PER == T::PER - 1) {
+#pragma unroll
+                    for (int nw = 0; nw < NW; ++nw) {
+                        const float s = q4_scale(word[nw][q]);
+#pragma unroll
+                        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                acc[mb][nw][r] = __builtin_fmaf(s, sum[mb][nw][r], acc[mb][nw][r]);
+                    }
+                }
             }
         }
     };
@@ -259,29 +291,40 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     }
 }
 
-constexpr int TILE_MB = 8, TILE_NW = 4, TILE_STAGES = 3;   // q4_128x256_s3
-
-template <int GROUP, bool TAIL>
-__global__ void __launch_bounds__(256) q4_tile_kernel(Q4Args p)
+template <int GROUP, int MB, int NW, int WAVES, int STAGES, bool ROUND, bool TAIL>
+__global__ void __launch_bounds__(64 * WAVES) q4_tile_kernel(Q4Args p)
 {
-    typedef Q4Tile<GROUP, TILE_MB, TILE_NW, TILE_STAGES> T;
+    typedef Q4Tile<GROUP, MB, NW, WAVES, STAGES, ROUND> T;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
-    q4_tile<T, TILE_MB, TILE_NW, TAIL>(p, lds);
+    q4_tile<T, MB, NW, ROUND, TAIL>(p, lds);
 }
 
-template <int GROUP>
-static void launch_tile(const Q4Args &a, dim3 grid, hipStream_t s)
+template <int MB, int NW, int WAVES, int STAGES, bool ROUND, bool TAIL>
+static hipError_t launch_tile(const Q4Args &a, int group, int64_t grid, hipStream_t s)
 {
-    if (a.K % 8 != 0)
-        hipLaunchKernelGGL((q4_tile_kernel<GROUP, true>), grid, dim3(256), 0, s, a);
+    const dim3 blocks((unsigned)grid), threads(64 * WAVES);
+    if (group == 32)
+        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
+    else if (group == 64)
+        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
     else
-        hipLaunchKernelGGL((q4_tile_kernel<GROUP, false>), grid, dim3(256), 0, s, a);
+        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
+    return hipGetLastError();
 }
 
-hipError_t launch_q4_tile(int group, const Q4Args &a, int64_t grid, hipStream_t s)
+template <bool TAIL>
+static hipError_t launch_config(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
 {
-    (group == 32 ? launch_tile<32> : group == 64 ? launch_tile<64> : launch_tile<128>)(a, dim3((unsigned)grid), s);
-    return hipGetLastError();
+    switch (config) {
+    case 5: return launch_tile<4, 1, 8, 4, false, TAIL>(a, group, grid, s);
+    case 6: return launch_tile<8, 4, 4, 3, true, TAIL>(a, group, grid, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
+{
+    return a.K % 8 != 0 ? launch_config<true>(config, group, a, grid, s) : launch_config<false>(config, group, a, grid, s);
 }
 
 } // namespace gemm_f16_impl
