@@ -110,12 +110,13 @@ typedef struct gemm_f16_q4_cache {
     int32_t heads, page_size, head_dim, group;
 } gemm_f16_q4_cache_t;
 
-/* Limits: heads and q_heads, batch, max_pages, page_size, pages. */
+/* Limits (beyond them, and where a launch would have 2^32 work items or more:
+ * GEMM_F16_ERROR_UNSUPPORTED_SIZE). */
 #define GEMM_F16_Q4_MAX_HEADS 4096
 #define GEMM_F16_Q4_MAX_BATCH ((int64_t)1 << 20)
 #define GEMM_F16_Q4_MAX_PAGE ((int64_t)1 << 16)
 #define GEMM_F16_Q4_MAX_LENGTH ((int64_t)1 << 30)   /* max_pages * page_size */
-#define GEMM_F16_Q4_MAX_TOKENS ((int64_t)1 << 30)   /* of one append or read */
+#define GEMM_F16_Q4_MAX_TOKENS ((int64_t)1 << 26)   /* of one append or read */
 #define GEMM_F16_Q4_MAX_PAGES ((int64_t)1 << 30)
 
 /*
@@ -174,6 +175,7 @@ gemm_f16_status_t gemm_f16_q4_cache_read(const gemm_f16_q4_cache_t *cache, int64
  *   splits  : parts the sequences are divided into, computed by separate
  *             workgroups and joined in order by a second kernel:
  *             GEMM_F16_SPLITS_AUTO or 1 .. GEMM_F16_Q4_MAX_SPLITS.
+ *   scale   : finite.
  *   max_length : what no length exceeds, for the choice of splits only (0:
  *             max_pages * page_size); any value gives right results.
  *   workspace : caller-owned, 16-byte aligned, of at least the plan's

@@ -178,9 +178,9 @@ def read(cache=None, batch=3, tokens=6, max_pages=2, table=at(2), first=at(3), s
 
 
 def attention(cache=None, batch=3, heads=4, max_pages=2, q=at(0), qs=512, table=at(1), lengths=at(2), out=at(3), splits=1,
-              max_length=0, ws=None, size=0):
+              max_length=0, ws=None, size=0, scale=0.1):
     c = cache_struct() if cache is None else cache
-    return g.lib().gemm_f16_q4_attention(ctypes.byref(c), batch, heads, max_pages, q, qs, table, lengths, 0.1, out, splits,
+    return g.lib().gemm_f16_q4_attention(ctypes.byref(c), batch, heads, max_pages, q, qs, table, lengths, scale, out, splits,
                                          max_length, ws, size, None)
 
 
@@ -209,7 +209,7 @@ def test_append_refusals():
         assert append(**bad) == INVALID, bad
     for bad in (dict(k=at(0) + 1), dict(q=at(5) + 1), dict(lengths=at(3) + 2), dict(starts=at(4) + 1), dict(cos=at(7) + 2)):
         assert append(**bad) == MISALIGNED, bad
-    assert append(tokens=(1 << 30) + 1) == SIZE and append(heads=4097, qs=4097 * 128) == SIZE
+    assert append(tokens=(1 << 26) + 1) == SIZE and append(heads=4097, qs=4097 * 128) == SIZE
     assert append(tokens=0) == 0 and append(batch=0) == 0
     if not torch.cuda.is_available():
         assert append(out=at(5)) == NO_DEVICE and append(batch=6, starts=None) == NO_DEVICE
@@ -222,7 +222,7 @@ def test_read_refusals():
         assert read(**bad) == INVALID, bad
     for bad in (dict(k=at(0) + 8), dict(v=at(1) + 2), dict(first=at(3) + 1), dict(starts=at(4) + 2)):
         assert read(**bad) == MISALIGNED, bad
-    assert read(tokens=(1 << 30) + 1) == SIZE and read(tokens=0) == 0
+    assert read(tokens=(1 << 26) + 1) == SIZE and read(tokens=0) == 0
     if not torch.cuda.is_available():
         assert read(first=None) == NO_DEVICE
 
@@ -230,7 +230,8 @@ def test_read_refusals():
 def test_attention_refusals():
     for bad in (dict(heads=0), dict(heads=3), dict(heads=-2), dict(q=None), dict(out=None), dict(lengths=None), dict(qs=511),
                 dict(splits=-1), dict(splits=257), dict(max_length=-1), dict(size=-1), dict(ws=None, size=4), dict(out=at(0)),
-                dict(out=at(11)), dict(out=at(1)), dict(out=at(2)), dict(cache=cache_struct(pages=0))):
+                dict(out=at(11)), dict(out=at(1)), dict(out=at(2)), dict(cache=cache_struct(pages=0)),
+                dict(scale=float("nan")), dict(scale=float("inf"))):
         assert attention(**bad) == INVALID, bad
     for bad in (dict(q=at(0) + 8), dict(qs=516), dict(out=at(3) + 8), dict(lengths=at(2) + 1)):
         assert attention(**bad) == MISALIGNED, bad
@@ -250,8 +251,11 @@ def test_attention_plans():
         assert p["workspace_bytes"] == (batch * heads * p["splits"] * 130 * 4 if p["splits"] > 1 else 0)
     assert g.plan_attention_q4(1, 8, 8, 128, 64, 131000)["splits"] > 1
     assert g.plan_attention_q4(1, 8, 8, 128, 64, 100)["splits"] == 1
+    for bad in ((1, 5, 2, 128, 64, 100), (1 << 20, 4096, 4096, 128, 64, 100), (1 << 20, 4096, 1, 128, 64, 100)):
+        with pytest.raises(g.GemmError):       # heads that do not divide; launches of 2^32 work items
+            g.plan_attention_q4(*bad)
     with pytest.raises(g.GemmError):
-        g.plan_attention_q4(1, 5, 2, 128, 64, 100)
+        g.plan_q4((1 << 31) - 1, 1 << 22, 128, config=g.q4_num_configs() - 1)
 
 
 def test_cache_binding_refusals():

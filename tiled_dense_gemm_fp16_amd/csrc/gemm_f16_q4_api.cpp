@@ -6,6 +6,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "gemm_f16_internal.h"
 #include "gemm_f16_q4.h"
@@ -35,6 +36,9 @@ int64_t q4_lds_bytes(const Q4Config &c, int group)
 namespace {
 
 bool known_group(int group) { return group == 32 || group == 64 || group == 128; }
+
+// Work items of a launch's grid are counted in 32 bits.
+bool launchable(int64_t workgroups, int64_t threads) { return workgroups <= 0xffffffff / threads; }
 
 gemm_f16_status_t status_of(hipError_t e) { return e == hipSuccess ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_LAUNCH_FAILED; }
 
@@ -129,7 +133,7 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
                    2.0 * (double)M * ((double)N + (double)K);
     p->trans_b = 1;
     p->workspace_bytes = p->splits > 1 ? (int64_t)p->splits * M * N * 4 : 0;
-    return p->grid > 0x7fffffff ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
+    return d.stages > 0 && !launchable(p->grid, p->threads) ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
 }
 
 // The cache's description and the page table's shape.
@@ -247,7 +251,7 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
     p->min_bytes = (double)batch * ((double)max_length * heads * (head_dim + 8.0 * head_dim / group) + 4.0 * q_heads * head_dim);
     p->splits = splits;
     p->workspace_bytes = splits > 1 ? batch * q_heads * splits * (head_dim + 2) * 4 : 0;
-    return p->grid > 0x7fffffff ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
+    return launchable(p->grid, p->threads) && launchable(batch * q_heads, 256) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
 }
 
 } // namespace
@@ -524,7 +528,7 @@ gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_
     gemm_f16_status_t st = validate_cache(cache, batch, max_pages);
     if (st != GEMM_F16_SUCCESS)
         return st;
-    if (workspace_bytes < 0 || (!workspace && workspace_bytes != 0) || max_length < 0)
+    if (workspace_bytes < 0 || (!workspace && workspace_bytes != 0) || max_length < 0 || !std::isfinite(scale))
         return GEMM_F16_ERROR_INVALID_VALUE;
     const int64_t room = max_pages * cache->page_size;
     gemm_f16_plan_t plan;
@@ -566,7 +570,7 @@ gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_
     a.q_stride = q_stride;
     a.lengths = lengths;
     a.out = (_Float16 *)out;
-    a.parts = (float *)workspace;
+    a.parts = plan.splits > 1 ? (float *)workspace : nullptr;
     a.scale = scale;
     a.q_heads = q_heads;
     a.ratio = q_heads / cache->heads;
