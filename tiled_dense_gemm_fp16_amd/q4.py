@@ -47,10 +47,21 @@ def _buffer(t, name, dtype, shape, index):
     raise ValueError(f"{name} must be a contiguous tensor on cuda:{index}")
 
 
-def _output(out, shape, index):
+def _empty(shape, dtype, index, stream):
+    """A new tensor that belongs to the call's stream: memory that another
+    stream may still be using is not written to."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=index)
+    if stream.device.index != index:
+        raise ValueError(f"stream must be a stream of cuda:{index}")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=index)
+
+
+def _output(out, shape, index, stream):
     """(tensor, address) of a caller's float16 output, or of a new one."""
     if out is None:
-        out = torch.empty(shape, dtype=torch.float16, device=index)
+        out = _empty(shape, torch.float16, index, stream)
         return out, out.data_ptr() or None
     return out, _buffer(out, "out", torch.float16, shape, index)
 
@@ -65,17 +76,18 @@ def _workspace(workspace, need, index, stream):
         return (workspace.data_ptr() if size else None), size, workspace
     if not need:
         return None, 0, None
-    if stream is None:
-        t = torch.empty(need // 4, dtype=torch.float32, device=index)
-    else:
-        with torch.cuda.device(index), torch.cuda.stream(stream):
-            t = torch.empty(need // 4, dtype=torch.float32, device=index)
+    t = _empty(need // 4, torch.float32, index, stream)
     return t.data_ptr(), need, t
 
 
 def _call(index, stream, what, fn, *args):
     """Call a C entry point on GPU `index` and `stream` (its last argument)."""
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index == index:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError(f"stream must be a stream of cuda:{index}")
     if torch.cuda.current_device() == index:
         st = fn(*args, raw)
     else:
@@ -124,8 +136,7 @@ def q4_compress(w, group: int = 128, symmetric: bool = False, stream=None) -> Q4
     at = _buffer(w, "w", torch.float16, w.shape, index)
     n, k = w.shape
     codes, words = _buffer_shapes(n, k, group)
-    codes = torch.empty(codes, dtype=torch.int32, device=index)
-    words = torch.empty(words, dtype=torch.int32, device=index)
+    codes, words = (_empty(shape, torch.int32, index, stream) for shape in (codes, words))
     _call(index, stream, "gemm_f16_q4_compress", lib().gemm_f16_q4_compress, n, k, group, 1 if symmetric else 0, at,
           codes.data_ptr() or None, words.data_ptr() or None)
     return Q4Matrix(codes, words, n, k, group)
@@ -134,7 +145,7 @@ def q4_compress(w, group: int = 128, symmetric: bool = False, stream=None) -> Q4
 def q4_expand(w: Q4Matrix, out=None, stream=None):
     """The n x k float16 matrix that ``w`` stands for, each value rounded once."""
     index, codes, words = _matrix(w)
-    out, to = _output(out, (w.n, w.k), index)
+    out, to = _output(out, (w.n, w.k), index, stream)
     _call(index, stream, "gemm_f16_q4_expand", lib().gemm_f16_q4_expand, w.n, w.k, w.group, codes, words, to)
     return out
 
@@ -173,7 +184,7 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
     n = w.n
     if k != w.k:
         raise ValueError(f"inner dimensions differ: a is {tuple(a.shape)}, w is {n} x {w.k}")
-    out, to = _output(out, (m, n), index)
+    out, to = _output(out, (m, n), index, stream)
     request = SPLITS_AUTO if splits is None else int(splits)
     need = 0
     if workspace is None and m and n:
@@ -325,7 +336,7 @@ def q4_cache_append(cache: Q4Cache, k, v, table, lengths, starts=None, q=None, c
             raise ValueError("q must be a tensor of tokens x q_heads x head_dim")
         q_heads = q.shape[1]
         q_p, _, q_stride = _rows(q, "q", q_heads, d, index, tokens)
-        out, out_p = _output(out, (tokens, q_heads, d), index)
+        out, out_p = _output(out, (tokens, q_heads, d), index, stream)
     elif out is not None:
         raise ValueError("out is for the rotated queries: give q")
     _call(index, stream, "gemm_f16_q4_cache_append", lib().gemm_f16_q4_cache_append, ctypes.byref(s), batch, tokens, max_pages,
@@ -346,8 +357,7 @@ def q4_cache_read(cache: Q4Cache, table, starts, total: int, first=None, stream=
     if total < 0:
         raise ValueError("total must not be negative")
     shape = (total, s.heads, s.head_dim)
-    k = torch.empty(shape, dtype=torch.float16, device=index)
-    v = torch.empty(shape, dtype=torch.float16, device=index)
+    k, v = (_empty(shape, torch.float16, index, stream) for _ in range(2))
     _call(index, stream, "gemm_f16_q4_cache_read", lib().gemm_f16_q4_cache_read, ctypes.byref(s), batch, total, max_pages,
           table_p, first_p, starts_p, k.data_ptr() or None, v.data_ptr() or None)
     return k, v
@@ -386,7 +396,7 @@ def attention_q4(q, cache: Q4Cache, table, lengths, scale: float | None = None, 
     q_p, batch, q_stride = _rows(q, "q", q_heads, d, index)
     table_p, _, max_pages = _table(table, index, batch)
     lengths_p = _buffer(lengths, "lengths", torch.int32, (batch,), index)
-    out, out_p = _output(out, (batch, q_heads, d), index)
+    out, out_p = _output(out, (batch, q_heads, d), index, stream)
     if max_length is not None and max_length < 0:
         raise ValueError("max_length must not be negative")
     room = max_pages * s.page_size
