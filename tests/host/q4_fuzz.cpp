@@ -112,6 +112,7 @@ hipError_t launch_q4_attention(const Q4AttentionArgs &a, int64_t grid, hipStream
     check_pages(a.c);
     CHECK(a.Q && a.out && a.lengths && a.ratio * a.c.heads == a.q_heads && a.row_tiles * 16 >= a.ratio);
     CHECK(grid == (int64_t)a.c.batch * a.c.heads * a.row_tiles * a.splits && grid * 256 <= 0xffffffff);
+    CHECK(a.step == 32 || (a.step == 64 && a.ratio <= 8) || (a.step == 128 && a.ratio <= 4 && a.c.head_dim < 256));
     CHECK((a.splits > 1) == (a.parts != nullptr) && (a.c.pages > 0 || a.c.max_pages == 0));
     return hipSuccess;
 }

@@ -249,6 +249,61 @@ def test_attention_pages_and_splits(page, splits):
     check_attention(128, 64, page, [0, 1, 31, 32, 33, 200, 257], 4, 1, pages=110, splits=splits)
 
 
+def steps(dim, group, lengths, q_heads, heads, room, splits=None):
+    """Tokens of a wave's step: several blocks where few heads share the columns and the table has room for many tokens."""
+    return g.plan_attention_q4(len(lengths), q_heads, heads, dim, group, room, splits)["block_n"]
+
+
+@pytest.mark.parametrize("dim,group", KINDS)
+@pytest.mark.parametrize("ratio", [1, 2, 3, 4, 5, 7, 8])
+def test_attention_blocks_side_by_side(dim, group, ratio):
+    lengths, width = [1, 0, 7, 33, 64, 100, 129, 300, 31, 128], 1024
+    want = 64 if ratio > 4 or dim == 256 else 128
+    assert steps(dim, group, lengths, 2 * ratio, 2, 16 * width) == want
+    check_attention(dim, group, 16, lengths, 2 * ratio, 2, width=width, pages=80, splits=1)
+    check_attention(dim, group, 16, lengths, 2 * ratio, 2, width=width, pages=80, splits=2, seed=1)
+
+
+@pytest.mark.parametrize("page", [8, 24, 32, 40, 256])
+@pytest.mark.parametrize("splits", [None, 3, 9])
+@pytest.mark.parametrize("ratio", [3, 6])
+def test_attention_blocks_side_by_side_pages(page, splits, ratio):
+    lengths, width = [0, 1, 95, 96, 97, 127, 160, 257, 700, 33], 16384 // page
+    assert steps(128, 64, lengths, 2 * ratio, 2, page * width) == (128 if ratio == 3 else 64)
+    check_attention(128, 64, page, lengths, 2 * ratio, 2, pages=210, splits=splits, width=width)
+
+
+def test_attention_blocks_side_by_side_pages_left_out():
+    for page, bad in ((16, [(0, 0, -1), (0, 3, 64), (1, 7, -2), (2, 1, 2 ** 31 - 1)]), (64, [(0, 1, -1), (1, 0, 64), (2, 0, -9)])):
+        for ratio in (2, 8):
+            for splits in (1, 2):
+                lengths = [200, 140, 30] + [5] * 9
+                assert steps(128, 64, lengths, 2 * ratio, 2, 16384) == (128 if ratio == 2 else 64)
+                check_attention(128, 64, page, lengths, 2 * ratio, 2, bad=bad, splits=splits, width=16384 // page)
+
+
+def test_attention_blocks_side_by_side_ignores_what_lies_behind():
+    # infinite and NaN scales behind the length, in the same blocks and in pages of nobody
+    for ratio in (4, 8):
+        cache = noise_cache(8, 2, 16, 64, 32, 1)
+        tab = torch.full((64, 1024), -1, dtype=torch.int32)
+        tab[0, :3], tab[1, 0] = torch.tensor([3, 5, 1], dtype=torch.int32), 0
+        tab[0, 3], tab[1, 1] = 2, 4                   # pages behind the last token
+        lengths = i32([37, 9] + [0] * 62)
+        assert steps(64, 32, lengths, 2 * ratio, 2, 16384) == 512 // ratio
+        q = torch.randn(64, 2 * ratio, 64, generator=gen(1)).to(torch.float16).to(DEV)
+        want = g.attention_q4(q, cache, tab.to(DEV), lengths).clone()
+        junk = clone(cache)
+        for words in (junk.k_words, junk.v_words):
+            for page, slot in ((1, 5), (0, 9)):
+                words[page, ..., slot:] = torch.tensor([0x7FFF7C00, 0xFFFF7E00 - 2 ** 32], dtype=torch.int32, device=DEV).repeat(
+                    8)[:16 - slot]
+            for page in (2, 4, 6, 7):
+                words[page] = -1
+        assert torch.equal(g.attention_q4(q, junk, tab.to(DEV), lengths), want)
+        assert bool((want[2:] == 0).all()) and bool(want[:2].isfinite().all())
+
+
 def test_attention_long():
     check_attention(128, 128, 64, [3000, 20], 4, 2, pages=70)
     check_attention(64, 64, 16, [6000], 1, 1, pages=400, splits=256)

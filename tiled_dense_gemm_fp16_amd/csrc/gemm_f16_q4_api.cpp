@@ -211,13 +211,20 @@ bool rows_fit(int64_t stride, int64_t heads, int head_dim) { return stride >= he
 bool rows_aligned(const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
 int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0; }
 
+// Blocks of 32 tokens that a wave takes at once.  The 16 columns of its products
+// are query heads; where 4 or 8 heads share a cache head, the softmax of 4 or 2
+// blocks goes through the columns together (32 x 4096 tokens x 8 heads, 4 query
+// heads each: 26.2 us with 4 blocks, 28.1 with 2, 28.6 with 1), while that leaves
+// steps for a wave on every SIMD (8 heads of one sequence of 2000: 7.5 us with 1
+// block, 8.0 with 2, 9.7 with 4).  head_dim 256 has registers for 2.
+//
 // Parts of the sequences: none where every CU has two workgroups without
-// (64 x 1000 tokens x 8 heads: 17.8 us whole, 25.6 in two parts); else as many
-// as make two for each CU, or four where sequences may differ in length and
-// the next workgroup evens that out (32 x 4096 x 8 heads: 28.1 us in four parts, 30.6
-// in two, 41.6 whole; one sequence of 131000: 32.9 us in 64 parts, 36.0 in 128), while
-// each wave of a part keeps a block of tokens (one sequence of 2000: 7.8 us in
-// 16 parts, 8.4 in 8).
+// (64 x 1000 tokens x 8 heads: 15.9 us whole, 21.6 in two parts); else as many
+// as make four for each CU (32 x 4096 x 8 heads: 26.2 us in four parts, 28.3 in
+// two, 29.1 whole; one sequence of 131000: 32.1 us in 128 parts, 33.4 in 64), for
+// head_dim 256 what its registers admit at once (4 x 8000 x 4 heads: 16.2 us in 16
+// parts, 19.4 in 32, 21.6 in 8), while each wave of a part keeps a block of tokens
+// (one sequence of 2000: 7.5 us in 15 parts, 8.2 in 8).
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {
@@ -227,17 +234,20 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (batch > GEMM_F16_Q4_MAX_BATCH || q_heads > GEMM_F16_Q4_MAX_HEADS || max_length > GEMM_F16_Q4_MAX_LENGTH)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
-    const int64_t tiles = (q_heads / heads + 15) / 16, units = batch * heads * tiles;
+    const int64_t ratio = q_heads / heads, tiles = (ratio + 15) / 16, units = batch * heads * tiles;
+    const int64_t blocks = (max_length + kQ4AttentionTokens - 1) / kQ4AttentionTokens;
+    int sub = ratio <= 4 && head_dim < 256 ? 4 : ratio <= 8 ? 2 : 1;
+    while (sub > 1 && units * blocks / sub < 4 * 256)
+        sub /= 2;
     if (splits == GEMM_F16_SPLITS_AUTO) {
-        const int64_t blocks = (max_length + kQ4AttentionTokens - 1) / kQ4AttentionTokens;
-        const int64_t here = head_dim == 256 && group < 128 ? 256 : 2 * 256;   // workgroups that the registers admit
-        const int64_t fill = units <= 0 || units >= here ? 1 : (batch > 1 && head_dim < 256 ? 2 * here : here) / units;
+        const int64_t here = head_dim < 256 ? 4 * 256 : group < 128 ? 256 : 2 * 256;
+        const int64_t fill = units <= 0 || units >= 2 * 256 ? 1 : std::max<int64_t>(here / units, 1);
         const int64_t most = blocks / kQ4AttentionWaves;
         splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
     }
     memset(p, 0, sizeof(*p));
     p->block_m = 16;
-    p->block_n = kQ4AttentionTokens;
+    p->block_n = sub * kQ4AttentionTokens;
     p->block_k = head_dim;
     p->stages = 1;
     p->threads = 64 * kQ4AttentionWaves;
@@ -576,6 +586,7 @@ gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_
     a.ratio = q_heads / cache->heads;
     a.row_tiles = (a.ratio + 15) / 16;
     a.splits = plan.splits;
+    a.step = plan.block_n;
     return status_of(launch_q4_attention(a, plan.grid, (hipStream_t)stream));
 }
 

@@ -3,8 +3,8 @@
 //
 // out[h] = sum_t softmax_t(scale q[h] . k[t]) v[t].  A workgroup owns up to 16
 // query heads that share a cache head, and one part of a sequence's tokens;
-// each of its waves takes every 4th block of 32 tokens, keeps the running
-// maximum m and sum l of the softmax and the unnormalised output in
+// each of its waves takes every 4th step of SUB blocks of 32 tokens, keeps the
+// running maximum m and sum l of the softmax and the unnormalised output in
 // registers, and the waves' results are joined through LDS at the end.
 //
 // Scores: S^T = K Q^T with v_mfma_f32_16x16x32_f16, 16 tokens by 16 heads.
@@ -25,35 +25,51 @@
 // enters as two binary16 parts (22 bits), so that the output carries no error
 // beyond fp32's and its own rounding.
 //
+// Few heads (SUB 2 or 4): the 16 columns hold 16 / SUB heads SUB times, and the
+// columns' copies take one block of the step each, so that scales, softmax
+// and P', which a lane computes for its column, are computed once and not for
+// columns that nobody asked for.  Scores of a block are kept by its own columns;
+// P' of the others is zero in its second product, whose sums thus stay apart:
+// every column is a softmax of its own until the join.  The values' zero
+// points, which a lane has for its own block, go to the row's other lanes by
+// broadcast.  Of about 400 vector instructions for 32 tokens (head_dim 128,
+// groups of 64) 240 remain with SUB 4.
+//
 // p = exp2(x - base), where base is chosen so that P' stays inside binary16:
 // when a block's largest score plus log2 of its largest scale passes base by
 // more than 15, base moves to 12 below it and the sums are rescaled; between,
 // nothing is (3 bits of slack make that rare).  So P' is below 2^15 and exact
 // to 2^-24, 2^-36 of the largest.  The sums of p and of P' v carry the same
 // factor, which the quotient drops.
+#include <type_traits>
+
+#include "gemm_f16_q4.h"
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
 namespace gemm_f16_impl {
 
-constexpr int WAVES = kQ4AttentionWaves, STEP = kQ4AttentionTokens;
+constexpr int WAVES = kQ4AttentionWaves, BLOCK = kQ4AttentionTokens;
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr float kTop = 15.0f, kLift = 12.0f;   // P' stays below 2^kTop and starts below 2^kLift
 
-// Waves of a SIMD the registers are shared out to.  At 32 x 4096 tokens,
-// head_dim 128: group 64 30.1 us with 2 (and a block's loads ahead), 28.1 with 3
-// (without); group 128 25.9 with 2, 27.0 with 3, and 32.9 against 37.3 for one
-// sequence of 131000.
+// Waves of a SIMD the registers are shared out to: as many as leave the sums,
+// a step's codes and words and the products' operands in registers.  Waves
+// that take turns serve better than a wave that loads ahead: with the next
+// step's keys on their way during the softmax and its values during the next
+// scores, in the same registers but for the addresses', 32 x 4096 tokens of
+// groups of 64 take 29 us, not 26.2, and of 128 27.2, not 24.3; only one sequence
+// of 131000 is a little faster so (31.3 us, not 32.1).
 constexpr int attention_waves(int head_dim, int group)
 {
-    return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim / group == 1 ? 2 : 3;
+    return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim == 128 && group == 32 ? 2 : 3;
 }
 
-// Blocks of a part: whole turns of the workgroup's waves.
-__device__ __forceinline__ int part_blocks(int blocks, int splits)
+// Steps of a part: whole turns of the workgroup's waves.
+__device__ __forceinline__ int part_steps(int steps, int splits)
 {
-    return ((blocks + splits - 1) / splits + WAVES - 1) / WAVES * WAVES;
+    return ((steps + splits - 1) / splits + WAVES - 1) / WAVES * WAVES;
 }
 
 // Two values rounded towards zero to binary16, packed.  Only for splitting a
@@ -92,137 +108,177 @@ __device__ __forceinline__ float column_sum(float x)
     return x + __shfl_xor(x, 32);
 }
 
-// What a wave needs of 32 tokens, in the layout of its products.
-template <int D, int GROUP>
-struct AttentionBlock {
-    static constexpr int GROUPS = D / GROUP, REGISTERS = D / 8 + 16 * GROUPS;
-    unsigned k[2][D / 32];          // codes of token 8 (col / 4) + 4 u + col % 4
+// The value of lane LANE of each row of 16 lanes, in all of them.
+template <int LANE>
+__device__ __forceinline__ unsigned row_lane(unsigned x)
+{
+    return (unsigned)__builtin_amdgcn_mov_dpp((int)x, 0x150 + LANE, 0xF, 0xF, true);   // row_newbcast
+}
+
+// What a wave needs of SUB blocks of 32 tokens, in the layout of its products;
+// the words are those of the lane's own block.
+template <int D, int GROUP, int SUB>
+struct AttentionStep {
+    static constexpr int GROUPS = D / GROUP;
+    unsigned k[SUB][2][D / 32];     // codes of token 8 (col / 4) + 4 u + col % 4
     uint4 k_words[2][GROUPS];       // of tokens 8 g + 4 u .. + 3
     uint4 v_words[2][GROUPS];
-    unsigned v[D / 16];             // d = 16 i + col of tokens 8 g .. + 7
-    bool mine;                      // the page of tokens 8 g .. exists
-    int whole;                      // all 32 tokens do
+    unsigned v[SUB][D / 16];        // d = 16 i + col of tokens 8 g .. + 7
+};
+
+// Where they lie: pages of the blocks (of this lane's granules of 8 tokens,
+// for a row of K and for the values, without ONE) and of the lane's words.
+template <int SUB>
+struct AttentionPages {
+    int k[SUB], v[SUB], own;
 };
 
 // ONE: every block of 32 tokens lies in one page (page sizes that are
 // multiples of 32): the page is the wave's and addresses are scalar, but for
 // each lane's place in the block.  Else pages are looked up for every granule
 // of 8 tokens.
-template <int D, int GROUP, bool ONE>
+template <int D, int GROUP, int SUB, bool ONE>
 __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_attention_kernel(Q4AttentionArgs a)
 {
-    constexpr int GROUPS = D / GROUP, JG = GROUP / 32, BLOCKS = D / 16, PITCH = D + 4;
+    constexpr int GROUPS = D / GROUP, JG = GROUP / 32, TILES = D / 16, PITCH = D + 4;
+    constexpr int HEADS = 16 / SUB, STEP = BLOCK * SUB;
     extern __shared__ __attribute__((aligned(16))) unsigned char q4_attention_lds[];
-    float *sums = reinterpret_cast<float *>(q4_attention_lds);   // [wave][16 heads][PITCH]
-    float *stats = sums + WAVES * 16 * PITCH;                    // [wave][base, l][16 heads]
+    float *sums = reinterpret_cast<float *>(q4_attention_lds);   // [wave][16 columns][PITCH]
+    float *stats = sums + WAVES * 16 * PITCH;                    // [wave][base, l][16 columns]
 
-    const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4;
+    const int tid = threadIdx.x, lane = tid & 63, col = lane & 15, g = lane >> 4, own = col / HEADS;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int id = blockIdx.x;
-    const int split = id % a.splits;
-    id /= a.splits;
+    // heads first, so that the XCDs (workgroups in turn) get equal work; parts
+    // last, so that the sequences' first ones, which are whole, start first
+    unsigned id = blockIdx.x;
+    const int h = id % a.c.heads;
+    id /= a.c.heads;
     const int tile = id % a.row_tiles;
     id /= a.row_tiles;
-    const int h = id % a.c.heads, b = id / a.c.heads;
-    const int rows = min(a.ratio - 16 * tile, 16);               // query heads of this workgroup
-    const int64_t q_head = (int64_t)h * a.ratio + 16 * tile;
+    const int b = id % a.c.batch, split = id / a.c.batch;
+    const int rows = min(a.ratio - HEADS * tile, HEADS);         // query heads of this workgroup
+    const int64_t q_head = (int64_t)h * a.ratio + HEADS * tile;
+
+    // this lane's head of Q, elements 32 j + 8 g .. + 7
+    half8 q[D / 32];
+    const half_t *query = a.Q + b * a.q_stride + (q_head + min(col % HEADS, rows - 1)) * D + 8 * g;
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j)
+        q[j] = *reinterpret_cast<const half8 *>(query + 32 * j);
 
     const int length = __builtin_amdgcn_readfirstlane(
         (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.c.max_pages * a.c.page_size));
-    const int blocks = (length + STEP - 1) / STEP, per = part_blocks(blocks, a.splits);
-    const int first = split * per, last = min(blocks, first + per);
+    const int steps = (length + STEP - 1) / STEP, per = part_steps(steps, a.splits);
+    const int first = split * per, last = min(steps, first + per);
     if (first >= last && (a.splits > 1 || length > 0))
         return;                                                  // an empty part; the join does not read it
 
-    // Pages of the lane's two granules of 8 tokens of a block, as a row of K
-    // (col / 4) and as the holder of scores and values (g); -1: none.  Reads
-    // stay inside the sequence's row of the table whatever the block.
+    // Reads stay inside the sequence's row of the table whatever the step.
     const int32_t *table = a.c.table + (int64_t)b * a.c.max_pages;
-    const auto next_pages = [&](int block, int &pk, int &pg) {
-        if constexpr (ONE) {
-            pk = table[min(q4_page_of(a.c, block * STEP), a.c.max_pages - 1)];
-        } else {
-            pk = table[min(q4_page_of(a.c, block * STEP + 8 * (col / 4)), a.c.max_pages - 1)];
-            pg = table[min(q4_page_of(a.c, block * STEP + 8 * g), a.c.max_pages - 1)];
-        }
-    };
-    typedef AttentionBlock<D, GROUP> Block;
+    const auto page_at = [&](int token) { return table[min(q4_page_of(a.c, token), a.c.max_pages - 1)]; };
     // This lane's place in a block: as a row of K, and as holder of 8 tokens
     const int k_token = 8 * (col / 4) + (col & 3), g_token = 8 * g;
-    const auto load = [&](int block, int pk, int pg, Block &x) {
-        const int t0 = block * STEP;
-        const uint32_t *kc, *kw, *vw, *vc;
-        if constexpr (ONE) {
-            const int page = __builtin_amdgcn_readfirstlane(pk);
-            const bool there = page >= 0 && page < a.c.pages;
-            const int64_t hp = (int64_t)(there ? page : 0) * a.c.heads + h;
-            const int slot = t0 - q4_page_of(a.c, t0) * a.c.page_size;
-            kc = a.c.k_codes + (hp * a.c.page_size + slot) * (D / 8) + k_token * (D / 8);
-            kw = a.c.k_words + hp * GROUPS * a.c.page_size + slot + g_token;
-            vw = a.c.v_words + hp * GROUPS * a.c.page_size + slot + g_token;
-            vc = a.c.v_codes + (hp * (a.c.page_size / 8) + slot / 8) * D + (g * 16 + col) * BLOCKS;
-            x.mine = there;
-            x.whole = there && t0 + STEP <= length;
-        } else {
-            const int tk = t0 + 8 * (col / 4), tg = t0 + g_token;
-            const bool there_k = tk < length && pk >= 0 && pk < a.c.pages;
-            const bool there_g = tg < length && pg >= 0 && pg < a.c.pages;
-            const int sk = tk - q4_page_of(a.c, tk) * a.c.page_size, sg = tg - q4_page_of(a.c, tg) * a.c.page_size;
-            const int64_t hk = (int64_t)(there_k ? pk : 0) * a.c.heads + h, hg = (int64_t)(there_g ? pg : 0) * a.c.heads + h;
-            kc = a.c.k_codes + (hk * a.c.page_size + sk + (col & 3)) * (D / 8);
-            kw = a.c.k_words + hg * GROUPS * a.c.page_size + sg;
-            vw = a.c.v_words + hg * GROUPS * a.c.page_size + sg;
-            vc = a.c.v_codes + (hg * (a.c.page_size / 8) + sg / 8) * D + col * BLOCKS;
-            x.mine = there_g;
-            x.whole = __builtin_amdgcn_readfirstlane(__all(there_g && tg + 8 <= length));
-        }
+    typedef AttentionPages<SUB> Pages;
+    const auto next_pages = [&](int step, Pages &p) {
+        const int t0 = step * STEP;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if constexpr (D == 64) {
-                const uint2 v = *reinterpret_cast<const uint2 *>(kc + u * (4 * D / 8) + 2 * g);
-                x.k[u][0] = v.x;
-                x.k[u][1] = v.y;
+        for (int i = 0; i < SUB; ++i) {
+            if constexpr (ONE) {
+                p.k[i] = page_at(t0 + BLOCK * i);
             } else {
-#pragma unroll
-                for (int n = 0; n < D / 128; ++n) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(kc + u * (4 * D / 8) + 16 * n + 4 * g);
-                    x.k[u][4 * n] = v.x;
-                    x.k[u][4 * n + 1] = v.y;
-                    x.k[u][4 * n + 2] = v.z;
-                    x.k[u][4 * n + 3] = v.w;
-                }
+                p.k[i] = page_at(t0 + BLOCK * i + 8 * (col / 4));
+                p.v[i] = page_at(t0 + BLOCK * i + g_token);
             }
         }
+        if constexpr (SUB > 1)
+            p.own = page_at(t0 + BLOCK * own + g_token);
+        else
+            p.own = ONE ? p.k[0] : p.v[0];
+    };
+    const auto exists = [&](int page) { return page >= 0 && page < a.c.pages; };
+    // A block's codes and words come from page 0 where there is no page.
+    typedef AttentionStep<D, GROUP, SUB> Step;
+    const auto load_words = [&](int step, const Pages &p, const uint32_t *words, uint4 (&w)[2][GROUPS]) {
+        const int t = step * STEP + BLOCK * own + g_token;
+        const int64_t hp = (int64_t)(exists(p.own) ? p.own : 0) * a.c.heads + h;
+        const uint32_t *from = words + hp * GROUPS * a.c.page_size + (t - q4_page_of(a.c, t) * a.c.page_size);
 #pragma unroll
         for (int n = 0; n < GROUPS; ++n)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                x.k_words[u][n] = *reinterpret_cast<const uint4 *>(kw + n * a.c.page_size + 4 * u);
-                x.v_words[u][n] = *reinterpret_cast<const uint4 *>(vw + n * a.c.page_size + 4 * u);
+            for (int u = 0; u < 2; ++u)
+                w[u][n] = *reinterpret_cast<const uint4 *>(from + n * a.c.page_size + 4 * u);
+    };
+    const auto load_k = [&](int step, const Pages &p, Step &x) {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            const uint32_t *kc;
+            if constexpr (ONE) {
+                const int page = __builtin_amdgcn_readfirstlane(p.k[i]), t = step * STEP + BLOCK * i;
+                const int64_t hp = (int64_t)(exists(page) && t < length ? page : 0) * a.c.heads + h;
+                const int slot = t - q4_page_of(a.c, t) * a.c.page_size;
+                kc = a.c.k_codes + (hp * a.c.page_size + slot) * (D / 8) + k_token * (D / 8);
+            } else {
+                const int t = step * STEP + BLOCK * i + 8 * (col / 4);
+                const int64_t hp = (int64_t)(exists(p.k[i]) && t < length ? p.k[i] : 0) * a.c.heads + h;
+                const int slot = t - q4_page_of(a.c, t) * a.c.page_size + (col & 3);
+                kc = a.c.k_codes + (hp * a.c.page_size + slot) * (D / 8);
             }
 #pragma unroll
-        for (int i = 0; i < BLOCKS; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(vc + i);
-            x.v[i] = v.x;
-            x.v[i + 1] = v.y;
-            x.v[i + 2] = v.z;
-            x.v[i + 3] = v.w;
+            for (int u = 0; u < 2; ++u) {
+                if constexpr (D == 64) {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(kc + u * (4 * D / 8) + 2 * g);
+                    x.k[i][u][0] = v.x;
+                    x.k[i][u][1] = v.y;
+                } else {
+#pragma unroll
+                    for (int n = 0; n < D / 128; ++n) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(kc + u * (4 * D / 8) + 16 * n + 4 * g);
+                        x.k[i][u][4 * n] = v.x;
+                        x.k[i][u][4 * n + 1] = v.y;
+                        x.k[i][u][4 * n + 2] = v.z;
+                        x.k[i][u][4 * n + 3] = v.w;
+                    }
+                }
+            }
+        }
+        load_words(step, p, a.c.k_words, x.k_words);
+    };
+    const auto load_v = [&](int step, const Pages &p, Step &x) {
+        load_words(step, p, a.c.v_words, x.v_words);
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            const uint32_t *vc;
+            if constexpr (ONE) {
+                const int page = __builtin_amdgcn_readfirstlane(p.k[i]), t = step * STEP + BLOCK * i;
+                const int64_t hp = (int64_t)(exists(page) && t < length ? page : 0) * a.c.heads + h;
+                const int slot = t - q4_page_of(a.c, t) * a.c.page_size;
+                vc = a.c.v_codes + (hp * (a.c.page_size / 8) + slot / 8) * D + (g * 16 + col) * TILES;
+            } else {
+                const int t = step * STEP + BLOCK * i + g_token;
+                const int64_t hp = (int64_t)(exists(p.v[i]) && t < length ? p.v[i] : 0) * a.c.heads + h;
+                const int slot = t - q4_page_of(a.c, t) * a.c.page_size;
+                vc = a.c.v_codes + (hp * (a.c.page_size / 8) + slot / 8) * D + col * TILES;
+            }
+#pragma unroll
+            for (int e = 0; e < TILES; e += 4) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(vc + e);
+                x.v[i][e] = v.x;
+                x.v[i][e + 1] = v.y;
+                x.v[i][e + 2] = v.z;
+                x.v[i][e + 3] = v.w;
+            }
         }
     };
 
-    // This lane's head of Q, elements 32 j + 8 g .. + 7; the sign of the scale
-    // goes into it (exactly), so that the largest product is the largest score.
-    half8 q[D / 32];
+    // The sign of the scale goes into the queries (exactly), so that the
+    // largest product is the largest score.
     const float scale = __builtin_fmaxf(__builtin_fabsf(a.scale) * kLog2e, 0x1p-126f);   // 0 would undo -infinity
     float q_sum[GROUPS];
     float4v start[GROUPS];         // takes the 64 off again
-    const auto load_queries = [&]() {
-        const half_t *row = a.Q + b * a.q_stride + (q_head + min(col, rows - 1)) * D + 8 * g;
+    const auto sum_queries = [&]() {
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-            q[j] = *reinterpret_cast<const half8 *>(row + 32 * j);
+        for (int j = 0; j < D / 32; ++j)
             q[j] = a.scale < 0.0f ? -q[j] : q[j];
-        }
 #pragma unroll
         for (int n = 0; n < GROUPS; ++n) {
             float t = 0.0f;
@@ -239,23 +295,28 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     const q4_bits bits;
 
     float base = -INFINITY, l = 0.0f;
-    float4v acc[BLOCKS];
+    float4v acc[TILES];
 #pragma unroll
-    for (int i = 0; i < BLOCKS; ++i)
+    for (int i = 0; i < TILES; ++i)
         acc[i] = float4v{0, 0, 0, 0};
 
-    const auto attend = [&](int block, const Block &y) {
-        const int tg = block * STEP + g_token;
-        // score / scale of tokens tg + 4 u + r
-        float x[8];
+    // score / scale of the lane's tokens 8 g + 4 u + r of its own block
+    const auto scores = [&](const Step &y, float (&x)[8]) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int n = 0; n < GROUPS; ++n)
 #pragma unroll
-            for (int n = 0; n < GROUPS; ++n) {
-                float4v s = start[n];
+            for (int u = 0; u < 2; ++u) {
+                float4v s;
 #pragma unroll
-                for (int j = n * JG; j < (n + 1) * JG; ++j)
-                    s = __builtin_amdgcn_mfma_f32_16x16x32_f16(q4_codes_64(y.k[u][j], bits), q[j], s, 0, 0, 0);
+                for (int i = 0; i < SUB; ++i) {
+                    float4v t = start[n];
+#pragma unroll
+                    for (int j = n * JG; j < (n + 1) * JG; ++j)
+                        t = __builtin_amdgcn_mfma_f32_16x16x32_f16(q4_codes_64(y.k[i][u][j], bits), q[j], t, 0, 0, 0);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        s[r] = i == 0 || own == i ? t[r] : s[r];
+                }
                 const uint4 w = y.k_words[u][n];
                 const unsigned word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -264,6 +325,10 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
                     x[4 * u + r] = n == 0 ? q4_scale(word[r]) * t : __builtin_fmaf(q4_scale(word[r]), t, x[4 * u + r]);
                 }
             }
+    };
+    const auto attend = [&](int step, const Pages &p, const Step &y, float (&x)[8]) {
+        const int tg = step * STEP + BLOCK * own + g_token;
+        const bool mine = exists(p.own);
         unsigned word[GROUPS][8];
 #pragma unroll
         for (int n = 0; n < GROUPS; ++n) {
@@ -273,10 +338,10 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
             for (int i = 0; i < 8; ++i)
                 word[n][i] = w[i];
         }
-        if (!y.whole) {   // what lies behind the last token has no weight, whatever it is
+        if (!__all(mine && tg + 8 <= length)) {   // what lies behind the last token has no weight, whatever it is
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool there = y.mine && tg + i < length;
+                const bool there = mine && tg + i < length;
                 x[i] = there ? x[i] : -INFINITY;
 #pragma unroll
                 for (int n = 0; n < GROUPS; ++n)
@@ -313,7 +378,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
             base = to;
             l *= fade;
 #pragma unroll
-            for (int i = 0; i < BLOCKS; ++i)
+            for (int i = 0; i < TILES; ++i)
                 acc[i] *= fade;
         }
         const float from = base == -INFINITY ? 0.0f : -base;
@@ -335,66 +400,62 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
                 lo[i] = rest[0];
                 lo[i + 1] = rest[1];
             }
-            const unsigned z0 = q4_zero(w[0] >> 16, w[1] >> 16).a, z1 = q4_zero(w[2] >> 16, w[3] >> 16).b,
-                           z2 = q4_zero(w[4] >> 16, w[5] >> 16).a, z3 = q4_zero(w[6] >> 16, w[7] >> 16).b;
+            const unsigned z[4] = {q4_zero(w[0] >> 16, w[1] >> 16).a, q4_zero(w[2] >> 16, w[3] >> 16).b,
+                                   q4_zero(w[4] >> 16, w[5] >> 16).a, q4_zero(w[6] >> 16, w[7] >> 16).b};
+            const auto block = [&](auto sub) {
+                constexpr int i = decltype(sub)::value;
+                // the other columns' tokens are not of this block
+                uint4 hb = __builtin_bit_cast(uint4, hi), lb = __builtin_bit_cast(uint4, lo);
+                unsigned zb[4] = {z[0], z[1], z[2], z[3]};
+                if constexpr (SUB > 1) {
+                    const unsigned keep = own == i ? ~0u : 0u;
+                    hb = make_uint4(hb.x & keep, hb.y & keep, hb.z & keep, hb.w & keep);
+                    lb = make_uint4(lb.x & keep, lb.y & keep, lb.z & keep, lb.w & keep);
 #pragma unroll
-            for (int i = n * GROUP / 16; i < (n + 1) * GROUP / 16; ++i) {
-                const half8 v = q4_codes(y.v[i], bits, z0, z1, z2, z3);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, hi, acc[i], 0, 0, 0);
-                acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, lo, acc[i], 0, 0, 0);
+                    for (int k = 0; k < 4; ++k)
+                        zb[k] = row_lane<i * HEADS>(zb[k]);
+                }
+#pragma unroll
+                for (int e = n * GROUP / 16; e < (n + 1) * GROUP / 16; ++e) {
+                    const half8 v = q4_codes(y.v[i][e], bits, zb[0], zb[1], zb[2], zb[3]);
+                    acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, __builtin_bit_cast(half8, hb), acc[e], 0, 0, 0);
+                    acc[e] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, __builtin_bit_cast(half8, lb), acc[e], 0, 0, 0);
+                }
+            };
+            block(std::integral_constant<int, 0>{});
+            if constexpr (SUB > 1)
+                block(std::integral_constant<int, 1>{});
+            if constexpr (SUB > 2) {
+                block(std::integral_constant<int, 2>{});
+                block(std::integral_constant<int, 3>{});
             }
         }
     };
 
-    int block = first + wave, pk = 0, pg = 0;
-    if (block < last) {
-        next_pages(block, pk, pg);
-        if constexpr (Block::REGISTERS <= 32) {
-            // A block's loads go out before the one ahead of it is attended
-            // to, its pages one block earlier still (and before that block's
-            // loads: waiting for the pages must not wait for those).
-            Block x0, x1;
-            int pk1 = 0, pg1 = 0;
-            next_pages(block + WAVES, pk1, pg1);
-            load(block, pk, pg, x0);
-            load_queries();
-            for (;;) {
-                if (block + WAVES >= last) {
-                    attend(block, x0);
-                    break;
-                }
-                next_pages(block + 2 * WAVES, pk, pg);
-                load(block + WAVES, pk1, pg1, x1);
-                attend(block, x0);
-                block += WAVES;
-                if (block + WAVES >= last) {
-                    attend(block, x1);
-                    break;
-                }
-                next_pages(block + 2 * WAVES, pk1, pg1);
-                load(block + WAVES, pk, pg, x0);
-                attend(block, x1);
-                block += WAVES;
-            }
-        } else {
-            // two blocks would not fit the registers; the other waves' work
-            // covers the loads
-            load_queries();
-            for (; block < last; block += WAVES) {
-                Block x;
-                load(block, pk, pg, x);
-                next_pages(block + WAVES, pk, pg);
-                attend(block, x);
-            }
+    int step = first + wave;
+    if (step < last) {
+        // A step's pages are looked up before the loads of the step before it
+        // go out: waiting for the pages must not wait for those.
+        Pages here, next;
+        Step y;
+        float x[8];
+        next_pages(step, here);
+        sum_queries();
+        for (; step < last; step += WAVES) {
+            load_k(step, here, y);
+            load_v(step, here, y);
+            next_pages(step + WAVES, next);
+            scores(y, x);
+            attend(step, here, y, x);
+            here = next;
         }
     }
     l = column_sum(l);
 
-    // join the waves: lane (g, head) holds d = 16 i + 4 g + r of its head
+    // join the waves and their columns: lane (g, col) holds d = 16 i + 4 g + r
 #pragma unroll
-    for (int i = 0; i < BLOCKS; ++i) {
+    for (int i = 0; i < TILES; ++i)
         *reinterpret_cast<float4v *>(sums + (wave * 16 + col) * PITCH + 16 * i + 4 * g) = acc[i];
-    }
     if (g == 0) {
         stats[wave * 32 + col] = base;
         stats[wave * 32 + 16 + col] = l;
@@ -404,15 +465,16 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
         const int row = e / (D / 4), d = e % (D / 4) * 4;
         float top = -INFINITY, total = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w)
-            top = __builtin_fmaxf(top, stats[w * 32 + row]);
+        for (int w = 0; w < WAVES * SUB; ++w)
+            top = __builtin_fmaxf(top, stats[w / SUB * 32 + w % SUB * HEADS + row]);
         const float from = top == -INFINITY ? 0.0f : top;
         float4v v = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) {
-            const float f = __builtin_amdgcn_exp2f(stats[w * 32 + row] - from);
-            total += f * stats[w * 32 + 16 + row];
-            const float4v part = *reinterpret_cast<const float4v *>(sums + (w * 16 + row) * PITCH + d);
+        for (int w = 0; w < WAVES * SUB; ++w) {
+            const int at = w % SUB * HEADS + row;
+            const float f = __builtin_amdgcn_exp2f(stats[w / SUB * 32 + at] - from);
+            total += f * stats[w / SUB * 32 + 16 + at];
+            const float4v part = *reinterpret_cast<const float4v *>(sums + (w / SUB * 16 + at) * PITCH + d);
             v += f * part;
         }
         const int64_t head = (int64_t)b * a.q_heads + q_head + row;
@@ -421,17 +483,19 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
         } else {
             *reinterpret_cast<float4v *>(a.parts + (head * a.splits + split) * D + d) = v;
             if (d == 0) {
-                float *ml = a.parts + (int64_t)a.c.batch * a.q_heads * a.splits * D + (head * a.splits + split) * 2;
-                ml[0] = top;
-                ml[1] = total;
+                float2 *ml = reinterpret_cast<float2 *>(a.parts + (int64_t)a.c.batch * a.q_heads * a.splits * D);
+                ml[head * a.splits + split] = make_float2(top, total);
             }
         }
     }
 }
 
+constexpr int FEW = 8;
+
 // Join the parts of the heads: D / 4 lanes hold a head's elements, and TEAMS
 // teams of them take its parts in turn; the teams' sums are added in order.
-// With one team a workgroup joins several heads.
+// With one team a workgroup joins several heads, of
+// at most FEW parts each.
 template <int D, int TEAMS>
 __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs a)
 {
@@ -444,30 +508,46 @@ __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs 
     float total = 0.0f;
     float4v v = {0, 0, 0, 0};
     if (head < heads) {
-        const int b = (int)(head / a.q_heads);
-        const int length = (int)min((int64_t)max(a.lengths[b], 0), (int64_t)a.c.max_pages * a.c.page_size);
-        const int blocks = (length + STEP - 1) / STEP, per = part_blocks(blocks, a.splits);
-        const int used = per > 0 ? (blocks + per - 1) / per : 0;     // parts that hold tokens
-        const float *ml = a.parts + heads * a.splits * D + head * a.splits * 2;
+        const float2 *ml = reinterpret_cast<const float2 *>(a.parts + heads * a.splits * D) + head * a.splits;
         const float *part = a.parts + head * a.splits * D + 4 * d;
+        const int length = (int)min((int64_t)max(a.lengths[head / a.q_heads], 0), (int64_t)a.c.max_pages * a.c.page_size);
+        const int steps = (length + a.step - 1) / a.step, per = part_steps(steps, a.splits);
+        const int used = per > 0 ? (steps + per - 1) / per : 0;      // parts that hold tokens
+        const auto add = [&](float base, const float2 &w, const float4v &x) {
+            const float f = __builtin_amdgcn_exp2f(w.x - base);
+            total += f * w.y;
+            v += f * x;
+        };
         float top = -INFINITY;
         if constexpr (TEAMS > 1) {   // one head: every wave looks at all parts
             for (int s = threadIdx.x & 63; s < used; s += 64)
-                top = __builtin_fmaxf(top, ml[2 * s]);
+                top = __builtin_fmaxf(top, ml[s].x);
 #pragma unroll
             for (int m = 1; m < 64; m *= 2)
                 top = __builtin_fmaxf(top, __shfl_xor(top, m));
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+            for (int s = team; s < used; s += TEAMS)
+                add(base, ml[s], *reinterpret_cast<const float4v *>(part + s * D));
         } else {
-#pragma unroll 4
-            for (int s = 0; s < used; ++s)
-                top = __builtin_fmaxf(top, ml[2 * s]);
-        }
-        const float base = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-        for (int s = team; s < used; s += TEAMS) {
-            const float f = __builtin_amdgcn_exp2f(ml[2 * s] - base);
-            total += f * ml[2 * s + 1];
-            v += f * *reinterpret_cast<const float4v *>(part + (int64_t)s * D);
+            // all parts are read at once, whether the length says that they
+            // are used or not: 0.5 us less than one read after the other
+            float4v x[FEW];
+            float2 w[FEW];
+#pragma unroll
+            for (int i = 0; i < FEW; ++i) {
+                const int s = min(i, a.splits - 1);
+                x[i] = *reinterpret_cast<const float4v *>(part + s * D);
+                w[i] = ml[s];
+            }
+#pragma unroll
+            for (int i = 0; i < FEW; ++i)
+                top = i < used ? __builtin_fmaxf(top, w[i].x) : top;
+            const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+            for (int i = 0; i < FEW; ++i)
+                if (i < used)
+                    add(base, w[i], x[i]);
         }
     }
     if constexpr (TEAMS > 1) {
@@ -489,22 +569,33 @@ __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs 
 
 int64_t q4_attention_lds_bytes(int head_dim) { return 4 * WAVES * (16 * (head_dim + 4) + 32); }
 
+template <int D, int GROUP, int SUB>
+static void launch_parts(const Q4AttentionArgs &a, int64_t grid, hipStream_t s)
+{
+    if (a.c.page_size % BLOCK == 0)
+        hipLaunchKernelGGL((q4_attention_kernel<D, GROUP, SUB, true>), dim3((unsigned)grid), dim3(64 * WAVES),
+                           (unsigned)q4_attention_lds_bytes(D), s, a);
+    else
+        hipLaunchKernelGGL((q4_attention_kernel<D, GROUP, SUB, false>), dim3((unsigned)grid), dim3(64 * WAVES),
+                           (unsigned)q4_attention_lds_bytes(D), s, a);
+}
+
 template <int D, int GROUP>
 static hipError_t launch_attention(const Q4AttentionArgs &a, int64_t grid, hipStream_t s)
 {
-    if (a.c.page_size % STEP == 0)
-        hipLaunchKernelGGL((q4_attention_kernel<D, GROUP, true>), dim3((unsigned)grid), dim3(64 * WAVES),
-                           (unsigned)q4_attention_lds_bytes(D), s, a);
-    else
-        hipLaunchKernelGGL((q4_attention_kernel<D, GROUP, false>), dim3((unsigned)grid), dim3(64 * WAVES),
-                           (unsigned)q4_attention_lds_bytes(D), s, a);
+    if (a.step == BLOCK)
+        launch_parts<D, GROUP, 1>(a, grid, s);
+    else if (a.step == 2 * BLOCK)
+        launch_parts<D, GROUP, 2>(a, grid, s);
+    else if (D < 256)
+        launch_parts<D, GROUP, D < 256 ? 4 : 1>(a, grid, s);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1)
         return e;
     // few parts: a team for each head; many: all of a workgroup's teams
     const int64_t heads = (int64_t)a.c.batch * a.q_heads;
     constexpr int TEAMS = 1024 / D;
-    if (a.splits <= 8)
+    if (a.splits <= FEW)
         hipLaunchKernelGGL((q4_attention_join_kernel<D, 1>), dim3((unsigned)((heads + TEAMS - 1) / TEAMS)), dim3(256), 0, s, a);
     else
         hipLaunchKernelGGL((q4_attention_join_kernel<D, TEAMS>), dim3((unsigned)heads), dim3(256), 0, s, a);

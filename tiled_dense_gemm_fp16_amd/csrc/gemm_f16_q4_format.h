@@ -90,6 +90,7 @@ struct Q4AttentionArgs {
     float scale;
     int q_heads, ratio;       // query heads; query heads of a cache head
     int row_tiles, splits;
+    int step;                 // tokens of a wave's step: 32, or 64 or 128 where up to 8 or 4 heads share the columns
 };
 constexpr int kQ4AttentionWaves = 4;
 constexpr int kQ4AttentionTokens = 32;   // a wave's step
