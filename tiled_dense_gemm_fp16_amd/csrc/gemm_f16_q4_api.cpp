@@ -220,11 +220,12 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 
 //
 // Parts of the sequences: none where every CU has two workgroups without
 // (64 x 1000 tokens x 8 heads: 15.9 us whole, 21.6 in two parts); else as many
-// as make four for each CU (32 x 4096 x 8 heads: 26.2 us in four parts, 28.3 in
-// two, 29.1 whole; one sequence of 131000: 32.1 us in 128 parts, 33.4 in 64), for
-// head_dim 256 what its registers admit at once (4 x 8000 x 4 heads: 16.2 us in 16
-// parts, 19.4 in 32, 21.6 in 8), while each wave of a part keeps a block of tokens
-// (one sequence of 2000: 7.5 us in 15 parts, 8.2 in 8).
+// as make two for each CU, or four where sequences may differ in length and
+// the next workgroup evens that out (32 x 4096 x 8 heads: 26.2 us in four parts,
+// 28.3 in two, 29.1 whole; one sequence of 131000: 34.2 us in 64 parts, 35.8 in 128),
+// for head_dim 256 what its registers admit at once (4 x 8000 x 4 heads: 16.2 us
+// in 16 parts, 19.4 in 32, 21.6 in 8), while each wave of a part keeps a block of
+// tokens (one sequence of 2000: 7.5 us in 15 parts, 8.2 in 8).
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {
@@ -240,8 +241,8 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
     while (sub > 1 && units * blocks / sub < 4 * 256)
         sub /= 2;
     if (splits == GEMM_F16_SPLITS_AUTO) {
-        const int64_t here = head_dim < 256 ? 4 * 256 : group < 128 ? 256 : 2 * 256;
-        const int64_t fill = units <= 0 || units >= 2 * 256 ? 1 : std::max<int64_t>(here / units, 1);
+        const int64_t here = head_dim == 256 && group < 128 ? 256 : 2 * 256;
+        const int64_t fill = units <= 0 || units >= here ? 1 : (batch > 1 && head_dim < 256 ? 2 * here : here) / units;
         const int64_t most = blocks / kQ4AttentionWaves;
         splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
     }

@@ -55,15 +55,16 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 15.0f, kLift = 12.0f;   // P' stays below 2^kTop and starts below 2^kLift
 
 // Waves of a SIMD the registers are shared out to: as many as leave the sums,
-// a step's codes and words and the products' operands in registers.  Waves
-// that take turns serve better than a wave that loads ahead: with the next
-// step's keys on their way during the softmax and its values during the next
-// scores, in the same registers but for the addresses', 32 x 4096 tokens of
-// groups of 64 take 29 us, not 26.2, and of 128 27.2, not 24.3; only one sequence
-// of 131000 is a little faster so (31.3 us, not 32.1).
+// a step's codes and words and the products' operands in registers (groups of
+// 128 would fit 3 times, and take 33.5 us for one sequence of 131000 then, not 32.7).
+// Waves that take turns serve better than a wave that loads ahead: with the
+// next step's keys on their way during the softmax and its values during the
+// next scores, in the same registers but for the addresses', 32 x 4096 tokens
+// of groups of 64 take 29 us, not 26.2, and of 128 27.2, not 24.4; only one sequence
+// of 131000 is hardly slower so.
 constexpr int attention_waves(int head_dim, int group)
 {
-    return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim == 128 && group == 32 ? 2 : 3;
+    return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim == 128 && group != 64 ? 2 : 3;
 }
 
 // Steps of a part: whole turns of the workgroup's waves.
