@@ -69,24 +69,20 @@ __device__ __forceinline__ unsigned round_chunk(float x[8], unsigned &word, bool
         lo = __builtin_fminf(lo, x[i]);
         hi = __builtin_fmaxf(hi, x[i]);
     }
-#pragma unroll
-    for (int m = 1; m < GROUP / 8; m *= 2) {
-        lo = __builtin_fminf(lo, __shfl_xor(lo, m));
-        hi = __builtin_fmaxf(hi, __shfl_xor(hi, m));
-    }
+    q4_row_extremes<GROUP / 8>(lo, hi);
     const q4_rounder r(lo, hi, false);
     word = r.word();
-    unsigned dw = 0;
+    unsigned bits[8];
     if (half) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            dw |= r.code16(x[i]) << q4_shift(i);
+            bits[i] = r.code16(x[i]);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            dw |= r.code(x[i]) << q4_shift(i);
+            bits[i] = r.code(x[i]);
     }
-    return dw;
+    return r.join(bits);
 }
 
 // LDS written by a wave is read by the same wave: its LDS accesses complete in

@@ -176,43 +176,114 @@ __device__ __forceinline__ float q4_scale(unsigned word)
     return (float)__builtin_bit_cast(q4_half2, word)[0];
 }
 
+// x / s, correctly rounded, for an s of at most 11 bits whose reciprocal is r
+// to within an ulp or two: the remainder of x r is exact, and with it the
+// quotient is known to 2^-44 of itself, while a quotient of 24 bits by 11 is at
+// least 2^-36 of itself away from every number half way between two floats
+// (never on one: that number times s would need 25 bits).  Not for infinite
+// x; where the remainder underflows the quotient is nothing next to 1/2.
+__device__ __forceinline__ float q4_divide(float x, float s, float r)
+{
+    const float q = x * r;
+    return __builtin_fmaf(__builtin_fmaf(-s, q, x), r, q);
+}
+
 // Scale word and codes of a group, from its extreme values.  NaN has been
 // replaced by 0 before.
 struct q4_rounder {
+    static constexpr float kLarge = 3e38f;                // for infinite values
+    static constexpr float kInteger = 12582912.0f;        // 1.5 2^23: its neighbours are 1 apart
     float s, z, r;
     __device__ __forceinline__ q4_rounder(float lo, float hi, bool symmetric)
     {
         lo = __builtin_fminf(lo, 0.0f);
         hi = __builtin_fmaxf(hi, 0.0f);
-        const float wide = symmetric ? __builtin_fmaxf(hi, -lo) / 7.0f : (hi - lo) / 15.0f;
+        // infinity becomes NaN here, which the minimum takes for 65504
+        const float wide = symmetric ? q4_divide(__builtin_fmaxf(hi, -lo), 7.0f, 1.0f / 7.0f)
+                                     : q4_divide(hi - lo, 15.0f, 1.0f / 15.0f);
         s = (float)(_Float16)__builtin_fminf(__builtin_fabsf(wide), 65504.0f);   // |.|: never -0
-        z = symmetric ? 8.0f : s > 0.0f ? __builtin_fminf(__builtin_fmaxf(__builtin_rintf(-lo / s), 0.0f), 15.0f) : 0.0f;
-        r = s > 0.0f ? 1.0f / s : 0.0f;
+        r = s > 0.0f ? __builtin_amdgcn_rcpf(s) : 0.0f;
+        z = symmetric ? 8.0f
+                      : __builtin_amdgcn_fmed3f(__builtin_rintf(q4_divide(__builtin_fminf(-lo, kLarge), s, r)), 0.0f, 15.0f);
     }
     __device__ __forceinline__ unsigned word() const
     {
         const _Float16 h = (_Float16)s;
         return (unsigned)__builtin_bit_cast(unsigned short, h) | (unsigned)z << 16;
     }
+
+    // Codes come as the bits of kInteger + n, with n = code - z: the sum rounds
+    // to an integer as rint does (halves to even).
     __device__ __forceinline__ unsigned clamped(float t) const
     {
-        return (unsigned)__builtin_amdgcn_fmed3f(t + z, 0.0f, 15.0f);
+        return __builtin_bit_cast(unsigned, __builtin_amdgcn_fmed3f(t, kInteger - z, kInteger + 15.0f - z));
     }
-    // code of any x
+    // of any x
     __device__ __forceinline__ unsigned code(float x) const
     {
-        return clamped(s > 0.0f ? __builtin_rintf(x / s) : 0.0f);
+        return clamped(q4_divide(__builtin_amdgcn_fmed3f(x, -kLarge, kLarge), s, r) + kInteger);
     }
-    // Code of a binary16 x, the same without the division: for x and s of 11
-    // bits the quotient either is a multiple of 1/2 or at least 2^-13 from one
-    // (where it matters, between codes), and x r is within 2^-18 of it, so
-    // rounding x r to a multiple of 2^-14 (adding 768 and taking it off) puts
-    // it on the multiple or leaves it on its side.
+    // Of a binary16 x, without the remainder: for x and s of 11 bits the
+    // quotient either is a multiple of 1/2 or at least 2^-13 from one (where it
+    // matters, between codes), and x r is within 2^-17 of it, so rounding x r to
+    // a multiple of 2^-14 (adding 768) puts it on the multiple or leaves it on
+    // its side.  Taking the 768 off is exact and part of the second sum.
     __device__ __forceinline__ unsigned code16(float x) const
     {
-        return clamped(__builtin_rintf(__builtin_fmaf(x, r, 768.0f) - 768.0f));
+        return clamped(__builtin_fmaf(x, r, 768.0f) + (kInteger - 768.0f));
+    }
+    // The dword of eight codes: their bits summed at the codes' places, in which
+    // nothing carries once the constant part is taken off.
+    __device__ __forceinline__ unsigned join(const unsigned (&bits)[8]) const
+    {
+        unsigned dw = ((unsigned)z - 0x4B400000u) * 0x11111111u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            dw += bits[i] << (4 * (i / 2 + 4 * (i & 1)));
+        return dw;
     }
 };
+
+// Smallest lo and largest hi of neighbouring lanes, 2, 4, 8 or 16 of a row.
+template <int LANES>
+__device__ __forceinline__ void q4_row_extremes(float &lo, float &hi)
+{
+    const auto with = [&](float l, float h) {
+        lo = __builtin_fminf(lo, l);
+        hi = __builtin_fmaxf(hi, h);
+    };
+#define GEMM_F16_Q4_DPP(x, ctrl) \
+    __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), ctrl, 0xF, 0xF, true))
+    with(GEMM_F16_Q4_DPP(lo, 0xB1), GEMM_F16_Q4_DPP(hi, 0xB1));             // the lane next to it
+    if constexpr (LANES > 2)
+        with(GEMM_F16_Q4_DPP(lo, 0x4E), GEMM_F16_Q4_DPP(hi, 0x4E));         // the other pair of four
+    if constexpr (LANES > 4)
+        with(GEMM_F16_Q4_DPP(lo, 0x141), GEMM_F16_Q4_DPP(hi, 0x141));       // eight mirrored: the other four
+    if constexpr (LANES > 8)
+        with(GEMM_F16_Q4_DPP(lo, 0x140), GEMM_F16_Q4_DPP(hi, 0x140));       // sixteen mirrored: the other eight
+#undef GEMM_F16_Q4_DPP
+}
+
+// ... of the four lanes 16 and 32 apart.  The swaps exchange rows of 16 or
+// halves of 32 lanes between two registers; of two copies of x they leave
+// each pair's values side by side.
+__device__ __forceinline__ void q4_column_extremes(float &lo, float &hi)
+{
+    const auto pair16 = [](float x, auto pick) {
+        const unsigned v = __builtin_bit_cast(unsigned, x);
+        const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return pick(__builtin_bit_cast(float, (unsigned)a[0]), __builtin_bit_cast(float, (unsigned)a[1]));
+    };
+    const auto pair32 = [](float x, auto pick) {
+        const unsigned v = __builtin_bit_cast(unsigned, x);
+        const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return pick(__builtin_bit_cast(float, (unsigned)a[0]), __builtin_bit_cast(float, (unsigned)a[1]));
+    };
+    const auto least = [](float a, float b) { return __builtin_fminf(a, b); };
+    const auto most = [](float a, float b) { return __builtin_fmaxf(a, b); };
+    lo = pair32(pair16(lo, least), least);
+    hi = pair32(pair16(hi, most), most);
+}
 
 // Position of value i of eight in a dword, in bits.
 __device__ __forceinline__ constexpr int q4_shift(int i) { return 4 * (i / 2 + 4 * (i & 1)); }

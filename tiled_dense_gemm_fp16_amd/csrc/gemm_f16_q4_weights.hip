@@ -30,6 +30,12 @@ __device__ __forceinline__ half8 row_piece(const half_t *p, int left)
 // of four dwords that is contiguous over the wave.  A group of 32 is one j of
 // the four lanes g, 64 two of them, 128 all four.
 
+// A tile row's words, loaded and stored at once.
+template <int GROUPS>
+struct alignas(4 * GROUPS) q4_row_words {
+    uint32_t w[GROUPS];
+};
+
 template <int GROUP>
 __global__ void __launch_bounds__(256) q4_compress_kernel(const half_t *__restrict__ W, uint32_t *__restrict__ codes,
                                                           uint32_t *__restrict__ words, int64_t N, int64_t K,
@@ -63,7 +69,7 @@ __global__ void __launch_bounds__(256) q4_compress_kernel(const half_t *__restri
                 for (int i = 0; i < 8; ++i)
                     x[j][i] = x[j][i] == x[j][i] ? x[j][i] : (half_t)0.0f;
         }
-        uint32_t word[GROUPS];
+        q4_row_words<GROUPS> word;
         uint4 out;
         unsigned dw[4];
 #pragma unroll
@@ -80,28 +86,22 @@ __global__ void __launch_bounds__(256) q4_compress_kernel(const half_t *__restri
                 lo = __builtin_fminf(lo, (float)low[i]);
                 hi = __builtin_fmaxf(hi, (float)high[i]);
             }
-#pragma unroll
-            for (int m = 16; m < 64; m *= 2) {
-                lo = __builtin_fminf(lo, __shfl_xor(lo, m));
-                hi = __builtin_fmaxf(hi, __shfl_xor(hi, m));
-            }
+            q4_column_extremes(lo, hi);
             const q4_rounder r(lo, hi, symmetric);
-            word[q] = r.word();
+            word.w[q] = r.word();
 #pragma unroll
             for (int j = q * PER; j < (q + 1) * PER; ++j) {
-                dw[j] = 0;
+                unsigned bits[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dw[j] |= r.code16((float)x[j][i]) << q4_shift(i);
+                    bits[i] = r.code16((float)x[j][i]);
+                dw[j] = r.join(bits);
             }
         }
         out = make_uint4(dw[0], dw[1], dw[2], dw[3]);
         *reinterpret_cast<uint4 *>(codes + (tile * 64 + lane) * 4) = out;
-        if (g == 0) {
-#pragma unroll
-            for (int q = 0; q < GROUPS; ++q)
-                words[(tile * 16 + n) * GROUPS + q] = word[q];
-        }
+        if (g == 0)
+            *reinterpret_cast<q4_row_words<GROUPS> *>(words + (tile * 16 + n) * GROUPS) = word;
     }
 }
 
@@ -118,9 +118,10 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const uint32_t *__restri
         const int64_t row = tile / k_blocks * 16 + n, k0 = tile % k_blocks * 128 + 8 * g;
         const uint4 c = *reinterpret_cast<const uint4 *>(codes + (tile * 64 + lane) * 4);
         const unsigned dw[4] = {c.x, c.y, c.z, c.w};
+        const q4_row_words<GROUPS> row_word = *reinterpret_cast<const q4_row_words<GROUPS> *>(words + (tile * 16 + n) * GROUPS);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t word = words[(tile * 16 + n) * GROUPS + j / PER];
+            const uint32_t word = row_word.w[j / PER];
             const float s = q4_scale(word);
             const half8 q = q4_codes(dw[j], bits, q4_zero(word));
             half8 v;
