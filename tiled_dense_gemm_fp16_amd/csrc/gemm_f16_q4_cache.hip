@@ -85,15 +85,6 @@ __device__ __forceinline__ unsigned round_chunk(float x[8], unsigned &word, bool
     return r.join(bits);
 }
 
-// LDS written by a wave is read by the same wave: its LDS accesses complete in
-// order, the compiler must only keep them so.
-__device__ __forceinline__ void wave_lds_fence()
-{
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
-
 template <int D, int GROUP>
 __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArgs a)
 {
@@ -173,7 +164,7 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArg
     }
     if (!value)
         return;
-    wave_lds_fence();
+    q4_wave_fence();
 #pragma unroll
     for (int s = 0; s < 8; ++s)
         if (s >= gr.slot && s < gr.slot + gr.count && gr.pos + s < covered)
@@ -212,7 +203,7 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_read_kernel(Q4ReadArgs a)
 #pragma unroll
         for (int e = lane; e < D; e += 64)
             codes[wave][e % (D / 16) * 16 + e / (D / 16)] = from[e];
-        wave_lds_fence();
+        q4_wave_fence();
     }
 #pragma unroll
     for (int pass = 0; pass < 8 / TOKENS; ++pass) {

@@ -285,6 +285,15 @@ __device__ __forceinline__ void q4_column_extremes(float &lo, float &hi)
     hi = pair32(pair16(hi, most), most);
 }
 
+// LDS written by a wave is read by the same wave: its LDS accesses complete in
+// order, the compiler must only keep them so.
+__device__ __forceinline__ void q4_wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Position of value i of eight in a dword, in bits.
 __device__ __forceinline__ constexpr int q4_shift(int i) { return 4 * (i / 2 + 4 * (i & 1)); }
 

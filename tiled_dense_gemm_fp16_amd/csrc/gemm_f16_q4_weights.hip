@@ -28,7 +28,13 @@ __device__ __forceinline__ half8 row_piece(const half_t *p, int left)
 // One wave per 16 x 128 tile.  Lane 16 g + n holds the tile's dwords of row n,
 // k = 32 j + 8 g + 0..7: four 16-byte pieces of the row, and one 16-byte store
 // of four dwords that is contiguous over the wave.  A group of 32 is one j of
-// the four lanes g, 64 two of them, 128 all four.
+// the four lanes g, 64 two of them, 128 all four.  Both kernels are bound by the
+// matrix's bytes: at 8192 x 8192 compress takes 30 us (groups of 128; 31 with 32) and
+// expand 32.7 (35.8), 5.6 and 5.2 TB/s, and at 5000 x 4100 with groups of 32, whose
+// rows are only 8-byte aligned, 14.5 and 15.2.  Compress reads the pieces as the
+// tile has them, 64 bytes of a row by four lanes (through LDS, whole rows of
+// 256 bytes at once: 35 us at 8192 x 8192 with groups of 32); expand writes whole rows
+// by way of LDS (64 bytes each: 38.5).
 
 // A tile row's words, loaded and stored at once.
 template <int GROUPS>
@@ -112,10 +118,11 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const uint32_t *__restri
 {
     constexpr int GROUPS = 128 / GROUP, PER = GROUP / 32;
     const q4_bits bits;
+    __shared__ half8 rows[4][16][17];   // [wave][row][piece]: 16 pieces, one more against bank conflicts
     const int lane = threadIdx.x & 63, n = lane & 15, g = lane >> 4;
+    half8(&mine)[16][17] = rows[threadIdx.x >> 6];
     const int64_t stride = (int64_t)gridDim.x * 4;
     for (int64_t tile = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); tile < tiles; tile += stride) {
-        const int64_t row = tile / k_blocks * 16 + n, k0 = tile % k_blocks * 128 + 8 * g;
         const uint4 c = *reinterpret_cast<const uint4 *>(codes + (tile * 64 + lane) * 4);
         const unsigned dw[4] = {c.x, c.y, c.z, c.w};
         const q4_row_words<GROUPS> row_word = *reinterpret_cast<const q4_row_words<GROUPS> *>(words + (tile * 16 + n) * GROUPS);
@@ -128,16 +135,24 @@ __global__ void __launch_bounds__(256) q4_expand_kernel(const uint32_t *__restri
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 v[i] = (half_t)(s * (float)q[i]);
-            const int64_t k = k0 + 32 * j;
+            mine[n][4 * j + g] = v;
+        }
+        // whole rows of 256 bytes at once, as memory holds them
+        q4_wave_fence();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t row = tile / k_blocks * 16 + 4 * i + g, k = tile % k_blocks * 128 + 8 * n;
+            const half8 v = mine[4 * i + g][n];
             if (row < N && k + 8 <= K) {
                 *reinterpret_cast<half8_any *>(W + row * K + k) = v;
             } else if (row < N) {
 #pragma unroll
-                for (int i = 0; i < 7; ++i)
-                    if (k + i < K)
-                        W[row * K + k + i] = v[i];
+                for (int e = 0; e < 7; ++e)
+                    if (k + e < K)
+                        W[row * K + k + e] = v[e];
             }
         }
+        q4_wave_fence();
     }
 }
 
