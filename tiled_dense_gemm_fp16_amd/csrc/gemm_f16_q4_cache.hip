@@ -1,15 +1,26 @@
 // gemm_f16_q4_cache.hip -- the 4-bit paged key/value cache: appending new
 // tokens (rotating keys and queries on the way) and reading tokens back.
+#include <algorithm>
+
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
 namespace gemm_f16_impl {
 
-// A wave handles one granule of up to 8 tokens of one head.  D / 8 lanes hold
+// A wave handles one granule of up to 8 tokens of some heads.  D / 8 lanes hold
 // a token's 8-element chunks, so a pass covers 64 / (D / 8) tokens.  Groups
 // reduce over group / 8 neighbouring lanes.  Keys store one dword a lane;
 // values exchange codes through LDS (bytes, [token][d]) so that each lane then
 // stores dwords of 8 tokens of one d.
+//
+// A granule's sequence, position and page take three reads one after the
+// other, each as long as the reads of its tokens: with few granules every head
+// has a wave of its own, and with many a wave takes several heads of one
+// granule (about 4096 waves; prompts of up to 1021 tokens of 5 sequences, 48 heads of 128,
+// appended and read back: 30.1 us, 31.0 with 8192 waves, 34.6 with a wave for
+// every head, 37.9 with 2048; 256 sequences of one token, 80 heads: 32.4, 30.5, 44.1, 40.3).  That
+// is 75 % of what a copy of the bytes takes for the prompts; 64 single tokens
+// (5.3 us to append, 7 to read) are bound by the chain of reads.
 constexpr int kCacheWaves = 4;
 
 __device__ __forceinline__ half8 load8(const half_t *p, bool vec)
@@ -92,9 +103,6 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArg
     __shared__ unsigned codes[kCacheWaves][8][LANES];   // [slot][chunk]: a dword of 8 codes of the chunk
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, chunk = lane % LANES;
     const int H = a.c.heads, jobs = 2 * H + (a.Q ? a.q_heads : 0);
-    const int job = blockIdx.y * kCacheWaves + wave;
-    if (job >= jobs)
-        return;
     const q4_granule gr = q4_find(blockIdx.x, a.starts, a.lengths, a.tokens, a.c.batch);
     if (gr.count == 0)
         return;
@@ -104,80 +112,83 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_append_kernel(Q4AppendArg
     // position has no page
     const int64_t covered = a.cos ? a.positions : INT64_MAX;
 
-    if (job >= 2 * H) {   // queries
-        const int h = job - 2 * H;
+    for (int job = blockIdx.y * kCacheWaves + wave; job < jobs; job += gridDim.y * kCacheWaves) {
+        if (job >= 2 * H) {   // queries
+            const int h = job - 2 * H;
+#pragma unroll
+            for (int pass = 0; pass < 8 / TOKENS; ++pass) {
+                const int slot = pass * TOKENS + lane / LANES, row = gr.row + slot - gr.slot;
+                if (slot < gr.slot || slot >= gr.slot + gr.count)
+                    continue;
+                float x[8] = {};
+                if (page >= 0 && gr.pos + slot < covered)
+                    load_rotated(a.Q + row * a.q_stride + h * D, chunk, a.vec_q, a, gr.pos + slot, x);
+                half8 v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = (half_t)x[i];
+                half_t *to = a.Q_out + ((int64_t)row * a.q_heads + h) * D + 8 * chunk;
+                if (a.vec_out) {
+                    *reinterpret_cast<half8 *>(to) = v;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        to[i] = v[i];
+                }
+            }
+            continue;
+        }
+        if (page < 0)
+            continue;
+        const bool value = job >= H;
+        const int h = value ? job - H : job;
+        const int64_t head = (int64_t)page * H + h;
+        unsigned keep = 0;   // slots of the granule that are written
 #pragma unroll
         for (int pass = 0; pass < 8 / TOKENS; ++pass) {
             const int slot = pass * TOKENS + lane / LANES, row = gr.row + slot - gr.slot;
-            if (slot < gr.slot || slot >= gr.slot + gr.count)
-                continue;
+            const bool mine = slot >= gr.slot && slot < gr.slot + gr.count && gr.pos + slot < covered;
             float x[8] = {};
-            if (page >= 0 && gr.pos + slot < covered)
-                load_rotated(a.Q + row * a.q_stride + h * D, chunk, a.vec_q, a, gr.pos + slot, x);
-            half8 v;
+            if (mine) {
+                if (value) {
+                    const half8 v = load8(a.V + row * a.v_stride + h * D + 8 * chunk, a.vec_v);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = (half_t)x[i];
-            half_t *to = a.Q_out + ((int64_t)row * a.q_heads + h) * D + 8 * chunk;
-            if (a.vec_out) {
-                *reinterpret_cast<half8 *>(to) = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    to[i] = v[i];
+                    for (int i = 0; i < 8; ++i)
+                        x[i] = (float)v[i];
+                } else {
+                    load_rotated(a.K + row * a.k_stride + h * D, chunk, a.vec_k, a, gr.pos + slot, x);
+                }
             }
-        }
-        return;
-    }
-    if (page < 0)
-        return;
-    const bool value = job >= H;
-    const int h = value ? job - H : job;
-    const int64_t head = (int64_t)page * H + h;
-    unsigned keep = 0;   // slots of the granule that are written
-#pragma unroll
-    for (int pass = 0; pass < 8 / TOKENS; ++pass) {
-        const int slot = pass * TOKENS + lane / LANES, row = gr.row + slot - gr.slot;
-        const bool mine = slot >= gr.slot && slot < gr.slot + gr.count && gr.pos + slot < covered;
-        float x[8] = {};
-        if (mine) {
-            if (value) {
-                const half8 v = load8(a.V + row * a.v_stride + h * D + 8 * chunk, a.vec_v);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    x[i] = (float)v[i];
-            } else {
-                load_rotated(a.K + row * a.k_stride + h * D, chunk, a.vec_k, a, gr.pos + slot, x);
+            unsigned word;
+            const unsigned dw = round_chunk<GROUP>(x, word, value);
+            if (mine) {
+                uint32_t *words = value ? a.c.v_words : a.c.k_words;
+                if (chunk % (GROUP / 8) == 0)
+                    words[(head * (D / GROUP) + chunk / (GROUP / 8)) * a.c.page_size + in_page + slot] = word;
+                if (!value)
+                    a.c.k_codes[(head * a.c.page_size + in_page + slot) * (D / 8) + q4_key_dword<D>(chunk)] = dw;
             }
+            if (value)
+                codes[wave][slot][chunk] = dw;
         }
-        unsigned word;
-        const unsigned dw = round_chunk<GROUP>(x, word, value);
-        if (mine) {
-            uint32_t *words = value ? a.c.v_words : a.c.k_words;
-            if (chunk % (GROUP / 8) == 0)
-                words[(head * (D / GROUP) + chunk / (GROUP / 8)) * a.c.page_size + in_page + slot] = word;
-            if (!value)
-                a.c.k_codes[(head * a.c.page_size + in_page + slot) * (D / 8) + q4_key_dword<D>(chunk)] = dw;
-        }
-        if (value)
-            codes[wave][slot][chunk] = dw;
-    }
-    if (!value)
-        return;
-    q4_wave_fence();
-#pragma unroll
-    for (int s = 0; s < 8; ++s)
-        if (s >= gr.slot && s < gr.slot + gr.count && gr.pos + s < covered)
-            keep |= 15u << q4_shift(s);
-    uint32_t *to = a.c.v_codes + (head * (a.c.page_size / 8) + in_page / 8) * D;
-#pragma unroll
-    for (int e = lane; e < D; e += 64) {   // in the order of the stored dwords: [d % 16][d / 16]
-        const int d = e % (D / 16) * 16 + e / (D / 16);
-        unsigned dw = 0;
+        if (!value)
+            continue;
+        q4_wave_fence();
 #pragma unroll
         for (int s = 0; s < 8; ++s)
-            dw |= (codes[wave][s][d / 8] >> (4 * (d % 8 / 2 + 4 * (d & 1))) & 15u) << q4_shift(s);
-        to[e] = keep == 0xFFFFFFFFu ? dw : (to[e] & ~keep) | (dw & keep);   // other tokens' codes stay
+            if (s >= gr.slot && s < gr.slot + gr.count && gr.pos + s < covered)
+                keep |= 15u << q4_shift(s);
+        uint32_t *to = a.c.v_codes + (head * (a.c.page_size / 8) + in_page / 8) * D;
+#pragma unroll
+        for (int e = lane; e < D; e += 64) {   // in the order of the stored dwords: [d % 16][d / 16]
+            const int d = e % (D / 16) * 16 + e / (D / 16);
+            unsigned dw = 0;
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+                dw |= (codes[wave][s][d / 8] >> (4 * (d % 8 / 2 + 4 * (d & 1))) & 15u) << q4_shift(s);
+            to[e] = keep == 0xFFFFFFFFu ? dw : (to[e] & ~keep) | (dw & keep);   // other tokens' codes stay
+        }
+        q4_wave_fence();   // the next job's codes come after this one's reads
     }
 }
 
@@ -187,46 +198,55 @@ __global__ void __launch_bounds__(64 * kCacheWaves) q4_read_kernel(Q4ReadArgs a)
     constexpr int LANES = D / 8, TOKENS = 64 / LANES;
     __shared__ unsigned codes[kCacheWaves][D];   // a granule's values: dword of d
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, chunk = lane % LANES;
-    const int H = a.c.heads, job = blockIdx.y * kCacheWaves + wave;
-    if (job >= 2 * H)
-        return;
+    const int H = a.c.heads;
     const q4_granule gr = q4_find(blockIdx.x, a.starts, a.first, a.tokens, a.c.batch);
     if (gr.count == 0)
         return;
     const int page = q4_page(a.c, gr.b, gr.pos);
     const int in_page = page >= 0 ? (int)gr.pos - q4_page_of(a.c, (int)gr.pos) * a.c.page_size : 0;
-    const bool value = job >= H;
-    const int h = value ? job - H : job;
-    const int64_t head = (int64_t)page * H + h;
-    if (value && page >= 0) {
-        const uint32_t *from = a.c.v_codes + (head * (a.c.page_size / 8) + in_page / 8) * D;
+    for (int job = blockIdx.y * kCacheWaves + wave; job < 2 * H; job += gridDim.y * kCacheWaves) {
+        const bool value = job >= H;
+        const int h = value ? job - H : job;
+        const int64_t head = (int64_t)page * H + h;
+        if (value && page >= 0) {
+            const uint32_t *from = a.c.v_codes + (head * (a.c.page_size / 8) + in_page / 8) * D;
 #pragma unroll
-        for (int e = lane; e < D; e += 64)
-            codes[wave][e % (D / 16) * 16 + e / (D / 16)] = from[e];
-        q4_wave_fence();
-    }
-#pragma unroll
-    for (int pass = 0; pass < 8 / TOKENS; ++pass) {
-        const int slot = pass * TOKENS + lane / LANES, row = gr.row + slot - gr.slot;
-        if (slot < gr.slot || slot >= gr.slot + gr.count)
-            continue;
-        half8 v = {};
-        if (page >= 0) {
-            const uint32_t *words = value ? a.c.v_words : a.c.k_words;
-            const unsigned word = words[(head * (D / GROUP) + chunk / (GROUP / 8)) * a.c.page_size + in_page + slot];
-            const float s = q4_scale(word), z = (float)(word >> 16);
-            unsigned dw = 0;
-            if (!value)
-                dw = a.c.k_codes[(head * a.c.page_size + in_page + slot) * (D / 8) + q4_key_dword<D>(chunk)];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const unsigned q = value ? codes[wave][8 * chunk + i] >> (4 * (slot / 2 + 4 * (slot & 1))) & 15u
-                                         : dw >> q4_shift(i) & 15u;
-                v[i] = (half_t)(s * ((float)q - z));
-            }
+            for (int e = lane; e < D; e += 64)
+                codes[wave][e % (D / 16) * 16 + e / (D / 16)] = from[e];
+            q4_wave_fence();
         }
-        *reinterpret_cast<half8 *>((value ? a.V : a.K) + ((int64_t)row * H + h) * D + 8 * chunk) = v;
+#pragma unroll
+        for (int pass = 0; pass < 8 / TOKENS; ++pass) {
+            const int slot = pass * TOKENS + lane / LANES, row = gr.row + slot - gr.slot;
+            if (slot < gr.slot || slot >= gr.slot + gr.count)
+                continue;
+            half8 v = {};
+            if (page >= 0) {
+                const uint32_t *words = value ? a.c.v_words : a.c.k_words;
+                const unsigned word = words[(head * (D / GROUP) + chunk / (GROUP / 8)) * a.c.page_size + in_page + slot];
+                const float s = q4_scale(word), z = (float)(word >> 16);
+                unsigned dw = 0;
+                if (!value)
+                    dw = a.c.k_codes[(head * a.c.page_size + in_page + slot) * (D / 8) + q4_key_dword<D>(chunk)];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned q = value ? codes[wave][8 * chunk + i] >> (4 * (slot / 2 + 4 * (slot & 1))) & 15u
+                                             : dw >> q4_shift(i) & 15u;
+                    v[i] = (half_t)(s * ((float)q - z));
+                }
+            }
+            *reinterpret_cast<half8 *>((value ? a.V : a.K) + ((int64_t)row * H + h) * D + 8 * chunk) = v;
+        }
+        q4_wave_fence();   // the next job's codes come after this one's reads
     }
+}
+
+// Workgroups for the heads of a granule.
+static unsigned head_groups(int heads, int64_t granules)
+{
+    constexpr int64_t kWaves = 4096;
+    const int64_t most = (heads + kCacheWaves - 1) / kCacheWaves, enough = (kWaves / kCacheWaves + granules - 1) / granules;
+    return (unsigned)std::max<int64_t>(std::min(most, enough), 1);
 }
 
 template <int D, int GROUP>
@@ -234,7 +254,7 @@ static hipError_t launch_append(const Q4AppendArgs &a, hipStream_t s)
 {
     const int jobs = 2 * a.c.heads + (a.Q ? a.q_heads : 0);
     const int64_t units = a.starts ? a.tokens / 8 + 2 * (int64_t)a.c.batch : a.c.batch;
-    hipLaunchKernelGGL((q4_append_kernel<D, GROUP>), dim3((unsigned)units, (unsigned)((jobs + kCacheWaves - 1) / kCacheWaves)),
+    hipLaunchKernelGGL((q4_append_kernel<D, GROUP>), dim3((unsigned)units, head_groups(jobs, units)),
                        dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }
@@ -244,7 +264,7 @@ static hipError_t launch_read(const Q4ReadArgs &a, hipStream_t s)
 {
     const int64_t units = a.tokens / 8 + 2 * (int64_t)a.c.batch;
     hipLaunchKernelGGL((q4_read_kernel<D, GROUP>),
-                       dim3((unsigned)units, (unsigned)((2 * a.c.heads + kCacheWaves - 1) / kCacheWaves)),
+                       dim3((unsigned)units, head_groups(2 * a.c.heads, units)),
                        dim3(64 * kCacheWaves), 0, s, a);
     return hipGetLastError();
 }
