@@ -309,3 +309,94 @@ def test_offsets_beyond_32_bits(dim, page):
     q = torch.randn(2, 16, dim, generator=gen(3)).to(torch.float16).to(DEV)
     lengths = i32([n, n])
     assert torch.equal(g.attention_q4(q, cache, i32(tab), lengths), g.attention_q4(q, small, near, lengths))
+
+
+def test_refusals():
+    layer = Layer(2, 256, 4, 2, 64, 16, 4, 64, 64)
+    c, table, lengths = layer.cache, layer.table, i32([5, 9])
+    x = torch.zeros(2, 256, dtype=torch.float16, device=DEV)
+    q, kv = torch.zeros(2, 4, 64, dtype=torch.float16, device=DEV), torch.zeros(2, 2, 64, dtype=torch.float16, device=DEV)
+    w = layer.w_in
+    before = copies(c[:4])
+    values = [lambda: g.gemm_q4(x.float(), w), lambda: g.gemm_q4(x[0], w), lambda: g.gemm_q4(x[:, :128].contiguous(), w),
+              lambda: g.gemm_q4(x.t(), w), lambda: g.gemm_q4(x.cpu(), w), lambda: g.gemm_q4(x, w, epilogue="tanh"),
+              lambda: g.gemm_q4(x, w, out=q), lambda: g.gemm_q4(x, w._replace(codes=w.codes[1:])),
+              lambda: g.gemm_q4(x, w._replace(group=32)), lambda: g.gemm_q4(x, w._replace(words=w.words.cpu())),
+              lambda: g.q4_compress(x[:, ::2]), lambda: g.q4_compress(x, 48), lambda: g.q4_expand(w, out=x),
+              lambda: g.attention_q4(q[:, :3], c, table, lengths), lambda: g.attention_q4(q[:1], c, table, lengths),
+              lambda: g.attention_q4(q, c, table, lengths.long()), lambda: g.attention_q4(q, c, table.long(), lengths),
+              lambda: g.attention_q4(q, c, table, lengths, max_length=-1), lambda: g.attention_q4(q, c, table.t(), lengths),
+              lambda: g.attention_q4(q.transpose(1, 2).contiguous().transpose(1, 2), c, table, lengths),
+              lambda: g.attention_q4(q, c._replace(k_words=c.k_words[:1]), table, lengths),
+              lambda: g.attention_q4(q, c._replace(group=32), table, lengths),
+              lambda: g.attention_q4(q, c, table, lengths, out=kv),
+              lambda: g.q4_cache_append(c, kv, kv[:1], table, lengths), lambda: g.q4_cache_append(c, kv[:1], kv[:1], table, lengths),
+              lambda: g.q4_cache_append(c, q, q, table, lengths), lambda: g.q4_cache_append(c, kv, kv, table, lengths, cos=layer.cos),
+              lambda: g.q4_cache_append(c, kv, kv, table, lengths, out=q), lambda: g.q4_cache_append(c, kv, kv, table, lengths[:1]),
+              lambda: g.q4_cache_append(c, kv, kv, table, lengths, cos=layer.cos[:, :4], sin=layer.sin[:, :4]),
+              lambda: g.q4_cache_append(c, kv, kv, table, lengths, cos=layer.cos, sin=layer.sin[:-1]),
+              lambda: g.q4_cache_append(c, kv, kv, table, lengths, starts=lengths),
+              lambda: g.q4_cache_read(c, table, lengths, 2), lambda: g.q4_cache_read(c, table, i32([0, 1, 2]), -1),
+              lambda: g.q4_cache_read(c, table, i32([0, 1, 2]), 2, first=i32([0]))]
+    for i, call in enumerate(values):
+        with pytest.raises(ValueError):
+            call()
+            print(f"[q4] call {i} was not refused", flush=True)
+    statuses = [lambda: g.gemm_q4(x, w, config=99), lambda: g.gemm_q4(x, w, splits=-3), lambda: g.gemm_q4(x, w, splits=65),
+                lambda: g.attention_q4(q, c, table, lengths, scale=float("nan")), lambda: g.attention_q4(q, c, table, lengths, splits=257),
+                lambda: g.attention_q4(q, c, table, lengths, out=q)]
+    for call in statuses:
+        with pytest.raises(g.GemmError):
+            call()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(c[:4], before))
+
+
+def test_nothing_to_do():
+    none = torch.empty(0, 128, dtype=torch.float16, device=DEV)
+    w = g.q4_compress(none, 64)
+    assert g.q4_expand(w).shape == (0, 128)
+    a = torch.ones(3, 128, dtype=torch.float16, device=DEV)
+    assert g.gemm_q4(a, w).shape == (3, 0)
+    assert g.gemm_q4(none, g.q4_compress(a, 64)).shape == (0, 3)
+    assert g.gemm_q4(a[:, :0], g.q4_compress(a[:, :0], 64)).tolist() == [[0.0] * 3] * 3
+    cache = g.q4_cache(0, 2, 16, 64, 32, DEV)
+    table, lengths = torch.empty(2, 0, dtype=torch.int32, device=DEV), i32([7, 0])
+    rows = torch.ones(2, 2, 64, dtype=torch.float16, device=DEV)
+    assert bool((g.attention_q4(rows, cache, table, lengths) == 0).all())
+    q = g.q4_cache_append(cache, rows, rows, table, lengths, q=rows)
+    assert bool((q == 0).all())                      # no page: rotated queries of tokens that are not appended are zeros
+    k, v = g.q4_cache_read(cache, table, i32([0, 1, 2]), 2)
+    assert bool((k == 0).all()) and bool((v == 0).all())
+    some = noise_cache(2, 2, 16, 64, 32, 0)
+    empty = torch.empty(0, 3, dtype=torch.int32, device=DEV)
+    assert g.attention_q4(rows[:0], some, empty, lengths[:0]).shape == (0, 2, 64)
+    assert g.q4_cache_append(some, rows[:0], rows[:0], empty, lengths[:0], q=rows[:0]).shape == (0, 2, 64)
+    assert g.q4_cache_read(some, empty, i32([0]), 0)[0].shape == (0, 2, 64)
+
+
+def test_threads():
+    """Calls from several threads at once, each on a stream of its own."""
+    import threading
+
+    w = g.q4_compress(weights(520, 4096, 1).to(DEV), 64)
+    cache, table, lengths = noise_cache(120, 2, 16, 128, 64, 0), i32(make_table([900, 700], 16, 120, 0)), i32([900, 700])
+    a = [torch.randn(2 + i, 4096, generator=gen(i)).to(torch.float16).to(DEV) for i in range(4)]
+    q = [torch.randn(2, 4, 128, generator=gen(i)).to(torch.float16).to(DEV) for i in range(4)]
+    want = [(g.gemm_q4(x, w, splits=3), g.attention_q4(y, cache, table, lengths, splits=5)) for x, y in zip(a, q)]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(30):
+                got = g.gemm_q4(a[i], w, splits=3), g.attention_q4(q[i], cache, table, lengths, splits=5)
+                if not all(torch.equal(x, y) for x, y in zip(got, want[i])):
+                    failed.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed

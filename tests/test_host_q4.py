@@ -283,3 +283,35 @@ def test_reference_cache_layout():
     c = ref.Cache(codes, words, values, words, 64)
     k, v = c.values("k"), c.values("v")
     assert k[0, 5, 0, 70] == 9 and k.sum() == 9 and v[0, 5, 0, 70] == 11 and v.sum() == 11
+
+
+def test_binding_refuses_any_object():
+    """Every argument of every entry point replaced by something else, one at a time and all at once: an exception, never
+    a crash (all of them lack a GPU tensor)."""
+    cache, i = g.q4_cache(4, 2, 16, 128, device="cpu"), torch.zeros(1, 1, dtype=torch.int32)
+    q = torch.zeros(1, 2, 128, dtype=torch.float16)
+    w = g.Q4Matrix(torch.zeros(1, 1, 4, 16, 4, dtype=torch.int32), torch.zeros(1, 1, 16, 1, dtype=torch.int32), 16, 128, 128)
+    turn, n = torch.zeros(64, 64), torch.zeros(2, dtype=torch.int32)
+    junk = [None, 3, -1, 2 ** 70, 1.5, "x", [], (), {}, object(), torch.zeros(()), torch.zeros(2, 3).to_sparse(),
+            torch.zeros(3, 3, 3, dtype=torch.float16, device="meta"), q.transpose(0, 1), q.to(torch.bfloat16), w, cache,
+            g.Q4Matrix(*"abcde"), g.Q4Matrix(w.codes, w.words, -5, 2 ** 62, 128), g.Q4Matrix(w.codes, w.words, 2 ** 62, 1, 32),
+            g.Q4Cache(*"abcde"), g.Q4Cache(i, i, i, i, 64), tuple.__new__(g.Q4Matrix, (1,)), tuple.__new__(g.Q4Cache, ())]
+    calls = [(g.q4_compress, [q[0]], {"group": 64, "symmetric": False}), (g.q4_expand, [w], {"out": q[0]}),
+             (g.gemm_q4, [q[0], w], {"epilogue": "none", "out": q[0], "config": 0, "splits": 1, "workspace": q, "alpha": 1.0}),
+             (g.q4_cache_append, [cache, q, q, i, i[0]], {"starts": n, "q": q, "cos": turn, "sin": turn, "interleaved": True,
+                                                          "out": q}),
+             (g.q4_cache_read, [cache, i, n, 1], {"first": i[0]}),
+             (g.attention_q4, [q, cache, i, i[0]], {"scale": 1.0, "out": q, "splits": 2, "workspace": q, "max_length": 8})]
+    refused = (ValueError, TypeError, OverflowError, RuntimeError)
+    for fn, args, kw in calls:
+        with pytest.raises(ValueError):
+            fn(*args, **kw)
+        for x in junk:
+            for at in range(len(args)):
+                with pytest.raises(refused):
+                    fn(*args[:at], x, *args[at + 1:], **kw)
+            for name in kw:
+                with pytest.raises(refused):
+                    fn(*args, **{**kw, name: x})
+            with pytest.raises(refused):
+                fn(*[x] * len(args))

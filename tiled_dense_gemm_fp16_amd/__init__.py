@@ -16,6 +16,7 @@ import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgemm_f16.so")
+BINDING_PATH = os.path.join(_HERE, "_q4_binding.so")
 PROBE_LIB_PATH = os.path.join(_HERE, "libgemm_f16_probe.so")
 
 SUCCESS = 0
