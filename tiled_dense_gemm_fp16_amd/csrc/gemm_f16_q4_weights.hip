@@ -207,6 +207,11 @@ hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float
 // rows past M and rows of W past N read nothing (and return zeros) without a
 // branch, which would make the compiler wait for more than it needs.  A whose
 // rows are only 2-byte aligned is read by plain loads instead (ALIGNED false).
+//
+// 1 x 28672 x 8192 with groups of 128 takes 26.2 us, 4.8 TB/s of codes and words,
+// 0.92 of what a copy reaches; 13 x 5000 x 4100 with groups of 32, one round of
+// workgroups of which each wave takes 4 or 5 blocks, 7.6 us: latency.  A wider
+// workgroup of 64 x 128 outputs spills (43 us at 64 x 8192 x 8192, 27 with 4 waves).
 
 template <int GROUPS>
 __device__ __forceinline__ void load_words(__amdgpu_buffer_rsrc_t r, uint32_t off, uint32_t at, unsigned (&w)[GROUPS])
