@@ -273,6 +273,39 @@ def test_attention_blocks_side_by_side_pages(page, splits, ratio):
     check_attention(128, 64, page, lengths, 2 * ratio, 2, pages=210, splits=splits, width=width)
 
 
+@pytest.mark.parametrize("ratio", [2, 8])
+def test_attention_blocks_side_by_side_scores(ratio):
+    # sharp, negative and constant scores; parts that are joined by one team and by several; strided queries
+    kw = dict(q_heads=2 * ratio, heads=2, pages=100, width=1024)
+    lengths = [90, 300, 0, 500]
+    assert steps(128, 64, lengths, 2 * ratio, 2, 16384) == (128 if ratio == 2 else 64)
+    check_attention(128, 64, 16, lengths, spread=20.0, splits=2, **kw)
+    check_attention(128, 64, 16, lengths, scale=-0.3, splits=8, **kw)
+    check_attention(128, 64, 16, lengths, scale=0.0, splits=9, **kw)
+    cache = noise_cache(100, 2, 16, 128, 64, 0)
+    table = i32(make_table(lengths, 16, 100, 0, 1024))
+    wide = torch.randn(4, 4 * ratio, 128, generator=gen(1)).to(torch.float16).to(DEV)
+    part = wide[:, ratio:3 * ratio]
+    assert torch.equal(g.attention_q4(part, cache, table, i32(lengths)), g.attention_q4(part.contiguous(), cache, table, i32(lengths)))
+
+
+def test_attention_infinite_queries_stay_in_their_head():
+    for width, ratio in ((32, 4), (1024, 4), (1024, 8)):
+        cache = noise_cache(100, 2, 16, 128, 64, 0)
+        lengths = [90, 300, 40, 500]
+        table = i32(make_table(lengths, 16, 100, 0, width))
+        q = torch.randn(4, 2 * ratio, 128, generator=gen(1)).to(torch.float16).to(DEV)
+        want = g.attention_q4(q, cache, table, i32(lengths))
+        odd = q.clone()
+        odd[1, 3, 5] = float("inf")
+        odd[2, ratio + 1, 7] = float("nan")
+        got = g.attention_q4(odd, cache, table, i32(lengths))
+        assert not got[1, 3].isfinite().any() and not got[2, ratio + 1].isfinite().any()
+        keep = torch.ones(4, 2 * ratio, dtype=torch.bool, device=DEV)
+        keep[1, 3] = keep[2, ratio + 1] = False
+        assert torch.equal(got[keep], want[keep])
+
+
 def test_attention_blocks_side_by_side_pages_left_out():
     for page, bad in ((16, [(0, 0, -1), (0, 3, 64), (1, 7, -2), (2, 1, 2 ** 31 - 1)]), (64, [(0, 1, -1), (1, 0, 64), (2, 0, -9)])):
         for ratio in (2, 8):
