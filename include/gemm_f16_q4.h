@@ -70,12 +70,15 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
  * A and C need 2-byte alignment, codes and words 16-byte; C overlaps none of
  * them.  K = 0 writes +0.  Limits: M <= GEMM_F16_MAX_DIM, N and K as gemm_f16.
  *   config : GEMM_F16_CONFIG_AUTO or an index below gemm_f16_q4_num_configs().
- *            The last two (plan: direct_lds 1) need A's rows 4-byte aligned (K
- *            even), the others nothing.  The last one also rounds each weight
+ *            The tiles (plan: direct_lds 1) need A's rows 4-byte aligned (K
+ *            even), the others nothing.  The last two also round each weight
  *            to binary16 (the value gemm_f16_q4_expand gives) before the
- *            product; all others use it exactly.  AUTO takes it for many
- *            rows.
- *   splits, workspace, workspace_bytes : as gemm_f16_split.
+ *            product; all others use it exactly.  AUTO takes them for many
+ *            rows.  The last one, q4_expanded, runs gemm_f16_q4_expand into the
+ *            workspace (2 N K bytes) and the dense product of gemm_f16_scaled,
+ *            whose plan its own does not repeat.
+ *   splits, workspace, workspace_bytes : as gemm_f16_split; splits 1 with
+ *            config AUTO never needs a workspace.
  */
 gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, const void *codes,
                               const void *words, void *C, float alpha, int epilogue, int config, int splits,

@@ -49,7 +49,7 @@ static void check_product(const Q4Args &a, int group)
 }
 hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t)
 {
-    CHECK(config >= 0 && config < kNumQ4Configs && kQ4Configs[config].stages == 0);
+    CHECK(config >= 0 && config < kQ4Expanded && kQ4Configs[config].stages == 0);
     CHECK((int64_t)a.tiles_m * 16 * kQ4Configs[config].m_blocks >= a.M);
     CHECK((int64_t)a.tiles_n * kQ4Configs[config].n_blocks >= a.n_blocks);
     check_product(a, group);
@@ -118,6 +118,16 @@ hipError_t launch_q4_attention(const Q4AttentionArgs &a, int64_t grid, hipStream
 }
 } // namespace gemm_f16_impl
 
+extern "C" gemm_f16_status_t gemm_f16_scaled(int64_t M, int64_t N, int64_t K, const void *A, int trans_a, const void *B, int trans_b,
+                                             void *C, float, int epilogue, int config, void *)
+{
+    CHECK(M > 0 && N > 0 && K >= 0 && C && !trans_a && trans_b == 1 && config == GEMM_F16_CONFIG_AUTO);
+    CHECK(K == 0 || (A && B && (uintptr_t)B % 16 == 0));
+    CHECK(epilogue == GEMM_F16_EPILOGUE_NONE || epilogue == GEMM_F16_EPILOGUE_RELU);
+    g_launches += K == 0;   // (with K > 0 the expansion before it is counted)
+    return GEMM_F16_SUCCESS;
+}
+
 static uint64_t g_rng = 0x9E3779B97F4A7C15ull;
 static uint64_t next()
 {
@@ -148,7 +158,7 @@ int main()
         bool nothing = false;
         const int kind = (int)(next() % 5);
         if (kind == 0) {
-            const int64_t M = pick(600), N = pick(5000), K = pick(9000);
+            const int64_t M = next() % 6 ? pick(600) : 2000 + pick(600), N = pick(5000), K = pick(9000);
             const int gr = group(), config = (int)(next() % 10) - 1, splits = next() % 3 ? 0 : (int)(next() % 70) - 1;
             gemm_f16_plan_t plan;
             void *A = at(0), *ws = next() % 2 ? at(4) : nullptr;

@@ -7,7 +7,7 @@ import pytest
 
 import tiled_dense_gemm_fp16_amd as g
 from test_gpu_q4_cache import KINDS, check_append, check_attention
-from test_gpu_q4_weights import check
+from test_gpu_q4_weights import EXPANDED, check
 
 pytestmark = pytest.mark.gpu
 
@@ -25,7 +25,7 @@ def test_products(seed):
     except g.GemmError:
         config = g.CONFIG_AUTO                      # rows that the configuration does not take
     check(m, n, k, group, config=config, epilogue=r.choice(["none", "relu"]), alpha=r.choice([1.0, -0.3, 2.5]), shift=shift,
-          seed=seed, splits=r.choice([None, None, 1, 2, 5]))
+          seed=seed, splits=None if config == EXPANDED else r.choice([None, None, 1, 2, 5]))
 
 
 @pytest.mark.parametrize("seed", range(60))

@@ -10,9 +10,10 @@ group, one per group of its wave's share of K, 8 across the waves, and the
 products with s and alpha: D = 32 + 3 + K / group + 8 + 2 roundings, each of at
 most 2^-23 of the sum of magnitudes (2^-24 for a rounding to nearest, twice
 that in case the matrix unit truncates).  (A split adds fewer than it takes
-off a wave's share.)  The configuration that rounds the weights to binary16
-adds half a step of each: 2^-11 of the sum of magnitudes (no weight here is
-below binary16's normals).
+off a wave's share.)  The configurations that round the weights to binary16
+add half a step of each: 2^-11 of the sum of magnitudes (no weight here is
+below binary16's normals); their sums run through the matrix unit alone, one
+addition for every 32 of K in the place of one for every group.
 """
 import numpy as np
 import pytest
@@ -35,7 +36,7 @@ def weights(n, k, seed):
 
 
 def bound(c, size, k, group, rounded=False):
-    depth = 45 + -(-k // group)
+    depth = 45 + -(-k // (32 if rounded else group))
     return ref.half_steps(c) * (1 + 2.0 ** -10) + (depth * 2.0 ** -23 + (2.0 ** -11 if rounded else 0.0)) * size
 
 
@@ -93,7 +94,8 @@ def test_compress_unaligned_source():
     assert bool((out[:1] == 7).all()) and bool((out[-2:] == 7).all())
 
 
-ROUNDED = g.q4_num_configs() - 1      # the configuration that rounds the weights
+EXPANDED = g.q4_num_configs() - 1              # W expanded, then the dense product: no split of K
+ROUNDED = (EXPANDED - 1, EXPANDED)             # the configurations that round the weights
 
 
 def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shift=0, seed=0, splits=None):
@@ -111,7 +113,7 @@ def check(m, n, k, group, config=g.CONFIG_AUTO, epilogue="none", alpha=1.0, shif
     want, size = ref.product(a.double().numpy(), w, float(np.float32(alpha)), epilogue == "relu")
     err = np.abs(ref.host(got).astype(np.float64) - want)
     chosen = g.plan_q4(m, n, k, group, config, splits, ad.data_ptr())["config"]
-    tol = bound(want, size, k, group, chosen == ROUNDED)
+    tol = bound(want, size, k, group, chosen in ROUNDED)
     assert (err <= tol).all(), (err / tol).max()
     assert bool((room[:64 + shift] == 9).all()) and bool((room[64 + shift + m * n:] == 9).all())
 
@@ -128,7 +130,7 @@ def test_every_config(config, group, m, n, k):
     check(m, n, k, group, config=config, seed=m + n + k)
 
 
-@pytest.mark.parametrize("config", range(g.q4_num_configs()))
+@pytest.mark.parametrize("config", range(EXPANDED))
 @pytest.mark.parametrize("m,n,k,splits", [(1, 16, 384, 3), (70, 140, 1030, 2), (64, 128, 4100, 7), (130, 300, 2048, 64),
                                           (129, 257, 132, 2), (300, 520, 514, None)])
 def test_splits(config, m, n, k, splits):
@@ -146,7 +148,7 @@ def test_last_chunk_keeps_to_its_row(config):
         got = ref.host(g.gemm_q4(a.to(DEV), packed, config=config)).astype(np.float64)
         w = ref.unpack_weights(ref.host(packed.codes), ref.host(packed.words), 48, k, 64)
         want, size = ref.product(a[::2].double().numpy(), w)
-        assert (np.abs(got[::2] - want) <= bound(want, size, k, 64, config == ROUNDED)).all()
+        assert (np.abs(got[::2] - want) <= bound(want, size, k, 64, config in ROUNDED)).all()
         assert not np.isfinite(got[1::2]).any() or (w[:, 0] == 0).any()
 
 
@@ -155,6 +157,24 @@ def test_last_chunk_keeps_to_its_row(config):
 @pytest.mark.parametrize("epilogue,alpha", [("none", 1.0), ("relu", 0.125), ("none", -1.7)])
 def test_automatic_choice(m, n, k, epilogue, alpha):
     check(m, n, k, 64, epilogue=epilogue, alpha=alpha)
+
+
+@pytest.mark.parametrize("n,k,shift", [(520, 1024, 0), (33, 300, 0), (48, 129, 1), (1, 1, 0)])
+def test_many_rows(n, k, shift):
+    """From 2048 rows W is expanded into the workspace; not with splits=1."""
+    chosen = [g.plan_q4(2050, n, k, 64, splits=s, A_ptr=2 * shift)["config"] for s in (None, 1)]
+    assert chosen[0] == EXPANDED and chosen[1] < EXPANDED
+    for splits in (None, 1):
+        check(2050, n, k, 64, epilogue="relu", alpha=0.3, shift=shift, splits=splits)
+    w = g.q4_compress(weights(n, k, 0).to(DEV), 64)
+    a = torch.randn(2050, k, generator=gen(1)).to(torch.float16).to(DEV)
+    dense = g.gemm(a, g.q4_expand(w), trans_b=True, alpha=0.3, splits=1)
+    assert torch.equal(g.gemm_q4(a, w, alpha=0.3), dense)
+    room = torch.full((2 * n * k + 32,), 85, dtype=torch.uint8, device=DEV)
+    assert torch.equal(g.gemm_q4(a, w, alpha=0.3, workspace=room[16:-16]), dense)
+    assert bool((room[:16] == 85).all()) and bool((room[-16:] == 85).all())
+    with pytest.raises(g.GemmError):
+        g.gemm_q4(a, w, workspace=room[16:-17])
 
 
 def test_unaligned_pointers():

@@ -66,10 +66,16 @@ def test_product_refusals():
     for bad in (dict(m=1 << 31), dict(n=(1 << 22) + 1), dict(k=(1 << 22) + 1)):
         assert call(**bad) == SIZE, bad
     # the tile configurations need A's rows 4-byte aligned; a split a workspace
-    assert [g.plan_q4(64, 32, 4096, 64, config=c)["direct_lds"] for c in range(g.q4_num_configs())] == [0] * (g.q4_num_configs() - 2) + [1] * 2
-    for c in range(g.q4_num_configs() - 2, g.q4_num_configs()):
+    last = g.q4_num_configs() - 1            # expands W into the workspace
+    assert [g.plan_q4(64, 32, 4096, 64, config=c)["direct_lds"] for c in range(last + 1)] == [0] * (last - 2) + [1] * 2 + [0]
+    for c in (last - 2, last - 1):
         assert call(config=c, a=at(0) + 2) == INVALID and call(config=c, k=255) == INVALID
-    for c in range(g.q4_num_configs()):
+    assert call(config=last, splits=2) == INVALID and call(config=last) == 7
+    assert call(config=last, ws=at(4), size=2 * 32 * 256 - 1) == 7
+    assert call(config=last, ws=at(4) + 8, size=2 * 32 * 256) == MISALIGNED
+    for p in (at(0), at(1), at(2), at(3)):
+        assert call(config=last, ws=p, size=2 * 32 * 256) == INVALID
+    for c in range(last):
         need = g.plan_q4(4, 32, 4096, 64, config=c, splits=3)["workspace_bytes"]
         assert need == 3 * 4 * 32 * 4
         assert call(config=c, k=4096, splits=3) == 7
@@ -98,14 +104,23 @@ def test_compress_and_expand_refusals():
 
 
 def test_plans():
-    for c in range(g.q4_num_configs()):
+    last = g.q4_num_configs() - 1
+    assert g.q4_config_name(last) == "q4_expanded"
+    for m, n, k in [(1, 16, 128), (2048, 5001, 301), (1, 1, 1 << 22)]:
+        p = g.plan_q4(m, n, k, 64, config=last)
+        assert p["config"] == last and p["splits"] == 1 and p["workspace_bytes"] == 2 * n * k and p["flops"] == 2.0 * m * n * k
+    assert g.plan_q4(2048, 8192, 8192, 64, splits=None)["config"] == last
+    assert g.plan_q4(2048, 8192, 8192, 64, splits=1)["workspace_bytes"] == 0
+    assert g.plan_q4(2047, 8192, 8192, 64, splits=None)["config"] < last
+    assert g.plan_q4(4096, 8192, 0, 64, splits=None)["workspace_bytes"] == 0
+    for c in range(last):
         assert g.q4_config_name(c)
         for m, n, k in [(1, 16, 128), (5, 1000, 4100), (64, 8192, 8192), (2048, 5000, 300), (1, 1, 1 << 22)]:
             p = g.plan_q4(m, n, k, 64, config=c)
             assert p["config"] == c and p["splits"] == 1 and p["workspace_bytes"] == 0 and p["lds_bytes"] <= 163840 and p["threads"] <= 1024
             assert p["tiles_m"] * p["block_m"] >= m and p["tiles_n"] * p["block_n"] >= n
             assert p["flops"] == 2.0 * m * n * k
-    for m in (1, 16, 17, 33, 100, 300, 5000):
+    for m in (1, 16, 17, 33, 100, 300, 2000):
         for n, k in [(16, 128), (1000, 4100), (8192, 8192), (64, 100000)]:
             p = g.plan_q4(m, n, k, 64, splits=None)
             assert p["splits"] * p["k_split"] >= k and (p["splits"] - 1) * p["k_split"] < k
@@ -255,7 +270,7 @@ def test_attention_plans():
         with pytest.raises(g.GemmError):       # heads that do not divide; launches of 2^32 work items
             g.plan_attention_q4(*bad)
     with pytest.raises(g.GemmError):
-        g.plan_q4((1 << 31) - 1, 1 << 22, 128, config=g.q4_num_configs() - 1)
+        g.plan_q4((1 << 31) - 1, 1 << 22, 128, config=g.q4_num_configs() - 2)
 
 
 def test_cache_binding_refusals():

@@ -22,11 +22,12 @@ const Q4Config kQ4Configs[kNumQ4Configs] = {
     {"q4_32x128", 2, 8, 8, 0},
     {"q4_64x128_s4", 4, 8, 8, 4},
     {"q4_128x256_s3", 8, 16, 4, 3},
+    {"q4_expanded", 0, 0, 0, 0},
 };
 
 int64_t q4_lds_bytes(const Q4Config &c, int group)
 {
-    if (c.stages == 0)
+    if (c.stages == 0)   // (no waves, no LDS: the expanded product's is its own)
         return (int64_t)c.waves * c.m_blocks * q4_sum_chunk(c.m_blocks, c.n_blocks) * 1024;
     const int64_t word_loads = (c.n_blocks * (128 / group) / 4 + c.waves - 1) / c.waves;
     return std::max<int64_t>(c.stages * (c.m_blocks * 4096 + c.n_blocks * 1024 + c.waves * word_loads * 256),
@@ -79,15 +80,23 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // The 128x256 tile takes over where it makes 64 workgroups for more than
     // 64 rows: (100, 28672 x 8192) 72, 93; (200, 8192 x 8192) 43, 52; (2048, 8192 x 8192) 240, 350;
     // but (200, 4096 x 4096) 27, 16, (128, 8192 x 8192) 32, 29 and (64, 28672 x 8192) 69, 50.
+    // From 2048 rows, expanding W into a workspace and the dense product take
+    // less: the tile unpacks each code once for 128 rows, in the matrix cores' shadow only
+    // in part.  (us, the tile's and this) (2048, 8192 x 8192) 241, 217; (4096, 8192 x
+    // 8192) 485, 392; (8192, 8192 x 8192) 974, 767; (2048, 5000 x 4100) 159, 130; (8192,
+    // 2048 x 2048) 73, 59; but (2048, 4096 x 4096) 67, 68; (1024, 8192 x 8192) 126, 138 and
+    // (1536, 8192 x 28672) 921, 950.  Not where the caller allows no workspace (1 split).
     const int64_t n_blocks = (N + 15) / 16, blocks = (K + 127) / 128;
-    const int large = kNumQ4Configs - 1, most_m = M > 16 ? 2 : 1;
+    const int large = kQ4Expanded - 1, most_m = M > 16 ? 2 : 1;
     const auto count = [&](int i) {
         const int64_t m = 16 * kQ4Configs[i].m_blocks, n = kQ4Configs[i].n_blocks;
         return (M + m - 1) / m * ((n_blocks + n - 1) / n);
     };
     int c = config;
     if (c == GEMM_F16_CONFIG_AUTO) {
-        if (aligned && M > 64 && count(large) >= 64) {
+        if (M >= 2048 && N > 0 && K > 0 && splits == GEMM_F16_SPLITS_AUTO) {
+            c = kQ4Expanded;
+        } else if (aligned && M > 64 && count(large) >= 64) {
             c = large;
         } else if (aligned && M > 32 && blocks >= 64) {
             c = large - 1;
@@ -100,10 +109,20 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
         }
     }
     const Q4Config &d = kQ4Configs[c];
-    if (d.stages > 0 && !aligned)
+    if ((d.stages > 0 && !aligned) || (c == kQ4Expanded && splits > 1))
         return GEMM_F16_ERROR_INVALID_VALUE;
     memset(p, 0, sizeof(*p));
     p->config = c;
+    p->flops = 2.0 * (double)M * (double)N * (double)K;
+    p->min_bytes = 0.5 * (double)N * (double)K + 4.0 * (double)N * (double)((K + group - 1) / group) +
+                   2.0 * (double)M * ((double)N + (double)K);
+    p->trans_b = 1;
+    if (c == kQ4Expanded) {   // the rest is the dense product's own plan
+        p->splits = 1;
+        p->k_split = K;
+        p->workspace_bytes = M > 0 ? 2 * N * K : 0;
+        return GEMM_F16_SUCCESS;
+    }
     p->block_m = 16 * d.m_blocks;
     p->block_n = 16 * d.n_blocks;
     p->block_k = 128;
@@ -128,10 +147,6 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     p->k_tiles = per;
     p->k_split = p->splits > 1 ? per * 128 : K;
     p->lds_bytes = q4_lds_bytes(d, group);
-    p->flops = 2.0 * (double)M * (double)N * (double)K;
-    p->min_bytes = 0.5 * (double)N * (double)K + 4.0 * (double)N * (double)((K + group - 1) / group) +
-                   2.0 * (double)M * ((double)N + (double)K);
-    p->trans_b = 1;
     p->workspace_bytes = p->splits > 1 ? (int64_t)p->splits * M * N * 4 : 0;
     return d.stages > 0 && !launchable(p->grid, p->threads) ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
 }
@@ -359,7 +374,7 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
         return st;
     if (M == 0 || N == 0)
         return GEMM_F16_SUCCESS;
-    if (plan.splits > 1) {
+    if (plan.workspace_bytes > 0) {
         if (!workspace)
             return GEMM_F16_ERROR_WORKSPACE;
         if ((uintptr_t)workspace % 16)
@@ -376,6 +391,14 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     st = check_device(&dev);
     if (st != GEMM_F16_SUCCESS)
         return st;
+    if (K == 0)
+        alpha = 1.0f;   // the empty sum is +0 whatever alpha
+    if (plan.config == kQ4Expanded) {
+        if (K > 0 && launch_q4_expand((const uint32_t *)codes, (const uint32_t *)words, (_Float16 *)workspace, N, K, group,
+                                      (hipStream_t)stream) != hipSuccess)
+            return GEMM_F16_ERROR_LAUNCH_FAILED;
+        return gemm_f16_scaled(M, N, K, A, 0, workspace, 1, C, alpha, epilogue, GEMM_F16_CONFIG_AUTO, stream);
+    }
     Q4Args a;
     a.A = (const _Float16 *)A;
     a.codes = (const uint32_t *)codes;
@@ -393,7 +416,7 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     a.splits = plan.splits;
     a.split_blocks = (int)plan.k_tiles;
     a.W = plan.splits > 1 ? (float *)workspace : nullptr;
-    a.alpha = K == 0 ? 1.0f : alpha;   // the empty sum is +0 whatever alpha
+    a.alpha = alpha;
     a.relu = epilogue == GEMM_F16_EPILOGUE_RELU ? 1 : 0;
     const hipError_t e = kQ4Configs[plan.config].stages == 0
                              ? launch_q4(plan.config, group, a, (hipStream_t)stream)

@@ -32,7 +32,8 @@ struct Q4Config {
     int waves;
     int stages;              // LDS stages of the tile kernel, each of 128 k; 0: the kernel for few rows
 };
-constexpr int kNumQ4Configs = 7;
+constexpr int kNumQ4Configs = 8;
+constexpr int kQ4Expanded = 7;   // W expanded into the workspace, then the dense product
 extern const Q4Config kQ4Configs[kNumQ4Configs];
 
 // The kernel for few rows adds its waves' sums this many 16-column blocks at

@@ -147,7 +147,7 @@ struct Workspace {
             at = address(*t);
             bytes = (int64_t)t->nbytes();
         } else if (need > 0) {
-            made = empty({need / 4}, at::kFloat, index);
+            made = empty({(need + 3) / 4}, at::kFloat, index);
             at = made.data_ptr();
             bytes = need;
         }
