@@ -33,10 +33,14 @@
 // twice): 247; operands read three steps ahead with a fixed interleaving: 269.
 //
 // q4_64x128_s4 (8 waves): 64 x 8192 x 8192, group 64, in four parts of K, 14-16 us
-// and 4 for their sum.  Bound by what a CU takes from the L2: 256 KiB of A
-// and 128 of codes for each workgroup, at 27-32 KB a us.  Unsplit workgroups of
-// the kernel for few rows read 750 KiB: 22-25 us.  4 waves of 32 rows of W:
-// 24; 2 x 4 waves: 22; codes 8 stages ahead by waves of their own: 22.
+// and 4 for their sum.  Bound by issue again: about 100 vector instructions
+// and 16 matrix instructions of a wave for each stage, two waves on a SIMD,
+// fill three quarters of its cycles.  Neither 3, 5 or 6 stages, nor two
+// workgroups on a CU (3 stages, 8 parts), nor half the reads of LDS (waves in
+// two halves of k, two columns of blocks each), nor workgroups that start at
+// different k change the time by more than 3 %.  Unsplit workgroups of the
+// kernel for few rows take 22-25 us; 4 waves of 32 rows of W 24; 2 x 4 waves 22;
+// codes 8 stages ahead by waves of their own 22; 64 x 256 in 8 parts 23.5.
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"
 
