@@ -96,7 +96,7 @@ def _compile_binding(verbose, incremental):
 
     obj = os.path.join(OBJDIR, os.path.basename(BINDING_SOURCE) + ".o")
     if incremental and os.path.exists(obj):
-        newest = max(os.path.getmtime(p) for p in (BINDING_SOURCE, os.path.join(INCLUDE, "gemm_f16_q4.h")))
+        newest = max(os.path.getmtime(p) for p in (BINDING_SOURCE, *(os.path.join(INCLUDE, f) for f in ("gemm_f16.h", "gemm_f16_q4.h"))))
         if os.path.getmtime(obj) > newest:
             return obj
     rocm = os.path.dirname(os.path.dirname(os.path.realpath(HIPCC)))
