@@ -239,8 +239,11 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 
 // the next workgroup evens that out (32 x 4096 x 8 heads: 26.2 us in four parts,
 // 28.3 in two, 29.1 whole; one sequence of 131000: 34.2 us in 64 parts, 35.8 in 128),
 // for head_dim 256 what its registers admit at once (4 x 8000 x 4 heads: 16.2 us
-// in 16 parts, 19.4 in 32, 21.6 in 8), while each wave of a part keeps a block of
-// tokens (one sequence of 2000: 7.5 us in 15 parts, 8.2 in 8).
+// in 16 parts, 19.4 in 32, 21.6 in 8), down to a block of tokens for each wave of a
+// part (one sequence of 2000: 7.5 us in 16 parts, 8.2 in 8).  The second kernel
+// costs 2 us at least, so short sequences stay whole (16 x 4 heads of 64 / 128 /
+// 256, whole or in parts: 380 tokens 5.0, 6.4, 10.0 or 6.6, 7.2, 8.7 us; 200
+// tokens 4.4, 5.4, 7.9 or 6.5, 7.2, 8.5; 640 tokens 6.4, 8.5, 13.8 or 7.2, 8.4, 10.0).
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {
@@ -258,8 +261,10 @@ gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head
     if (splits == GEMM_F16_SPLITS_AUTO) {
         const int64_t here = head_dim == 256 && group < 128 ? 256 : 2 * 256;
         const int64_t fill = units <= 0 || units >= here ? 1 : (batch > 1 && head_dim < 256 ? 2 * here : here) / units;
-        const int64_t most = blocks / kQ4AttentionWaves;
+        const int64_t most = (blocks + kQ4AttentionWaves - 1) / kQ4AttentionWaves;
         splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(fill, most), GEMM_F16_Q4_MAX_SPLITS));
+        if (blocks <= std::min(20, 1920 / head_dim))
+            splits = 1;
     }
     memset(p, 0, sizeof(*p));
     p->block_m = 16;
