@@ -77,9 +77,16 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // 15.8 / *14.4 / 16.7; and from 33 rows the 64x128 tile does (us, best of the
     // others): (48, 8192 x 8192) 19.2, 21.3; (64, 28672 x 8192) 49.9, 62.2; (128, 4096 x 14336)
     // 27.7, 29.2; but (32, 8192 x 8192) 18.1, 16.4 and (64, 5000 x 4100) 12.9, 12.6.
+    // It also does where the widest workgroup would come in more than one round, as
+    // it starts and ends faster: (64, 28672 x 4096) 28, 39; (128, 14336 x 512) 6.8, 11.8;
+    // (300, 5000 x 1024) 9.7, 15.3; (300, 4096 x 4096) 25, 33; but (128, 8192 x 4096) 21.2, 18.8.
     // The 128x256 tile takes over where it makes 64 workgroups for more than
     // 64 rows: (100, 28672 x 8192) 72, 93; (200, 8192 x 8192) 43, 52; (2048, 8192 x 8192) 240, 350;
-    // but (200, 4096 x 4096) 27, 16, (128, 8192 x 8192) 32, 29 and (64, 28672 x 8192) 69, 50.
+    // but (200, 4096 x 4096) 27, 16, (128, 8192 x 8192) 32, 29 and (64, 28672 x 8192) 69, 50;
+    // and not while the 64x128 tile's workgroups are one round over at most 32
+    // blocks of K, or two over 16 (its time, this one's): (512, 4096 x 4096) 28, 33;
+    // (256, 8192 x 1024) 9.8, 21; (1024, 4096 x 2048) 29, 34; but (1024, 4096 x 4096) 51, 46 and
+    // (512, 14336 x 1024) 32, 21.5.
     // From 2048 rows, expanding W into a workspace and the dense product take
     // less: the tile unpacks each code once for 128 rows, in the matrix cores' shadow only
     // in part.  (us, the tile's and this) (2048, 8192 x 8192) 241, 217; (4096, 8192 x
@@ -96,9 +103,9 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     if (c == GEMM_F16_CONFIG_AUTO) {
         if (M >= 2048 && N > 0 && K > 0 && splits == GEMM_F16_SPLITS_AUTO) {
             c = kQ4Expanded;
-        } else if (aligned && M > 64 && count(large) >= 64) {
+        } else if (aligned && M > 64 && count(large) >= 64 && count(large - 1) > (blocks <= 16 ? 512 : blocks <= 32 ? 256 : 0)) {
             c = large;
-        } else if (aligned && M > 32 && blocks >= 64) {
+        } else if (aligned && M > 32 && (blocks >= 64 || count(large - 2) > 256)) {
             c = large - 1;
         } else {
             for (c = large - 2; c > 0; --c)
