@@ -147,6 +147,13 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
         if (M > 8 && tiles > 0 && tiles < (d.stages > 0 ? 256 : 150))   // a part keeps 8 blocks, two for each wave of the kernel for few rows
             splits = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / (d.stages > 0 ? 8 : 16)),
                                                                  GEMM_F16_MAX_SPLITS));
+        // one row or few, where it saves more than the second launch costs a caller
+        // that does not capture its calls, 3 us.  us whole and split: (1, 1024 x 28672)
+        // 16.0, 8.2; (4, 1024 x 16384) 11.6, 7.5; (1, 256 x 16384) 10.1, 6.1; but (1, 512 x
+        // 8192) 6.2, 5.4, (8, 2048 x 8192) 8.1, 7.4, (1, 512 x 4096) 3.8, 4.9, (4, 4096 x 8192)
+        // 7.3, 9.2, and in 8 parts (1, 1024 x 28672) 8.5 and (4, 1024 x 16384) 8.9.
+        else if (M <= 8 && d.stages == 0 && blocks >= 128 && tiles > 0 && tiles <= 128)
+            splits = (int)std::min<int64_t>(std::min<int64_t>(256 / tiles, blocks / 16), 4);
     }
     const int64_t per = blocks > 0 ? (blocks + splits - 1) / splits : 0;
     p->splits = per > 0 ? (int)((blocks + per - 1) / per) : 1;   // none empty
