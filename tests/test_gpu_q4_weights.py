@@ -153,7 +153,7 @@ def test_last_chunk_keeps_to_its_row(config):
 
 
 @pytest.mark.parametrize("m,n,k", [(1, 1024, 1024), (2, 5000, 4100), (13, 256, 8192), (40, 600, 3000), (300, 300, 300),
-                                   (70, 64, 9000), (520, 700, 1000)])
+                                   (70, 64, 9000), (520, 700, 1000), (3, 70, 16500), (300, 5000, 300), (40, 9000, 520)])
 @pytest.mark.parametrize("epilogue,alpha", [("none", 1.0), ("relu", 0.125), ("none", -1.7)])
 def test_automatic_choice(m, n, k, epilogue, alpha):
     check(m, n, k, 64, epilogue=epilogue, alpha=alpha)
