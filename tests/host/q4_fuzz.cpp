@@ -63,6 +63,13 @@ hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, 
     check_product(a, group);
     return hipSuccess;
 }
+static int g_packs = 0;
+hipError_t launch_q4_pack(const _Float16 *A, _Float16 *to, int64_t M, int64_t K, int64_t pitch, hipStream_t)
+{
+    ++g_packs;
+    CHECK(A && to && (uintptr_t)to % 16 == 0 && M > 0 && K > 0 && pitch >= K && pitch < K + 8 && pitch % 8 == 0);
+    return hipSuccess;
+}
 hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *words, int64_t N, int64_t K, int group, bool,
                               hipStream_t)
 {

@@ -168,13 +168,34 @@ def test_many_rows(n, k, shift):
         check(2050, n, k, 64, epilogue="relu", alpha=0.3, shift=shift, splits=splits)
     w = g.q4_compress(weights(n, k, 0).to(DEV), 64)
     a = torch.randn(2050, k, generator=gen(1)).to(torch.float16).to(DEV)
-    dense = g.gemm(a, g.q4_expand(w), trans_b=True, alpha=0.3, splits=1)
-    assert torch.equal(g.gemm_q4(a, w, alpha=0.3), dense)
-    room = torch.full((2 * n * k + 32,), 85, dtype=torch.uint8, device=DEV)
-    assert torch.equal(g.gemm_q4(a, w, alpha=0.3, workspace=room[16:-16]), dense)
+    want = g.gemm_q4(a, w, alpha=0.3)
+    if k % 2 == 0:
+        assert torch.equal(want, g.gemm(a, g.q4_expand(w), trans_b=True, alpha=0.3, splits=1))
+    need = g.plan_q4(2050, n, k, 64, splits=None)["workspace_bytes"]
+    room = torch.full((need + 32,), 85, dtype=torch.uint8, device=DEV)
+    assert torch.equal(g.gemm_q4(a, w, alpha=0.3, workspace=room[16:-16]), want)
     assert bool((room[:16] == 85).all()) and bool((room[-16:] == 85).all())
     with pytest.raises(g.GemmError):
         g.gemm_q4(a, w, workspace=room[16:-17])
+
+
+@pytest.mark.parametrize("m,n,k,shift", [(16, 40, 129, 0), (17, 264, 1001, 1), (40, 9000, 300, 1), (33, 48, 8193, 0), (300, 520, 2047, 0),
+                                         (70, 300, 8, 1), (130, 16400, 33, 3), (20, 30, 1, 0)])
+def test_rows_of_odd_length(m, n, k, shift):
+    """From 16 rows A is copied to aligned rows; not with splits=1 or a configuration."""
+    for group, splits in ((32, None), (128, None), (64, 1)):
+        check(m, n, k, group, shift=shift, splits=splits, epilogue="relu", alpha=0.7)
+    w = g.q4_compress(weights(n, k, 0).to(DEV), 64)
+    a = torch.randn(m, k, generator=gen(1)).to(torch.float16).to(DEV)
+    if k % 2:
+        need = g.plan_q4(m, n, k, 64, splits=None)["workspace_bytes"]
+        assert need >= 2 * m * k
+        room = torch.full((need + 32,), 255, dtype=torch.uint8, device=DEV)          # NaN: all that is read was written
+        assert torch.equal(g.gemm_q4(a, w, workspace=room[16:-16]), g.gemm_q4(a, w))
+        assert bool((room[:16] == 255).all()) and bool((room[-16:] == 255).all())
+    a[1::2] = float("inf")                            # rows do not reach into each other
+    got, clean = g.gemm_q4(a, w), g.gemm_q4(torch.where(a.isinf(), torch.zeros_like(a), a), w)
+    assert torch.equal(got[::2], clean[::2])
 
 
 def test_unaligned_pointers():

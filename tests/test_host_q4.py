@@ -125,7 +125,14 @@ def test_plans():
             p = g.plan_q4(m, n, k, 64, splits=None)
             assert p["splits"] * p["k_split"] >= k and (p["splits"] - 1) * p["k_split"] < k
             assert p["workspace_bytes"] == (p["splits"] * m * n * 4 if p["splits"] > 1 else 0)
-            assert g.plan_q4(m, n, k, 64, splits=None, A_ptr=2)["direct_lds"] == 0
+            assert g.plan_q4(m, n, k, 64, splits=1, A_ptr=2)["direct_lds"] == 0
+            odd = g.plan_q4(m, n, k, 64, splits=None, A_ptr=2)     # from 16 rows A is copied to aligned rows
+            if m >= 16:
+                wide = g.plan_q4(m, n, -(-k // 8) * 8, 64, splits=None)
+                copy = -(-2 * m * -(-k // 8) * 8 // 256) * 256
+                assert odd["workspace_bytes"] == wide["workspace_bytes"] + copy and odd["config"] == wide["config"]
+            else:
+                assert odd["direct_lds"] == 0
     assert g.q4_config_name(-1) is None and g.q4_config_name(g.q4_num_configs()) is None
     for bad in (dict(m=-1), dict(group=31), dict(k=1 << 23), dict(config=99)):
         with pytest.raises(g.GemmError):

@@ -60,9 +60,28 @@ gemm_f16_status_t validate_weights(int64_t N, int64_t K, int group, const void *
 // Whether the tile kernels' direct loads can read A's rows.
 bool rows_4_aligned(const void *A, int64_t K) { return (uintptr_t)A % 4 == 0 && K % 2 == 0; }
 
+// Rows of A that are not 4-byte aligned (an odd K or pointer) are first copied
+// to aligned rows in the workspace, where one is allowed and there are enough
+// of them: every kernel but the one that loads single elements becomes possible.
+// us at (M, N x K) without and with the copy: (48, 8192 x 8193) 58, 24; (300, 4096 x
+// 4097) 69, 32; (1000, 8192 x 8193) 494, 143; (2100, 8192 x 8193) 833, 385; (16, 4096 x
+// 4097) 15.8, 8.9; but (16, 20000 x 1001) 9.3, 9.6.
+bool packs(int64_t M, int64_t N, int64_t K, bool aligned, int config, int splits)
+{
+    return !aligned && config == GEMM_F16_CONFIG_AUTO && splits == GEMM_F16_SPLITS_AUTO && M >= 16 && N > 0 && K > 0;
+}
+int64_t packed_k(int64_t K) { return (K + 7) / 8 * 8; }   // within the last group: the codes' order is the same
+int64_t packed_bytes(int64_t M, int64_t K) { return (2 * M * packed_k(K) + 255) / 256 * 256; }
+
 gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool aligned, int config, int splits,
                             gemm_f16_plan_t *p)
 {
+    if (packs(M, N, K, aligned, config, splits)) {
+        const gemm_f16_status_t st = make_plan(M, N, packed_k(K), group, true, config, splits, p);
+        p->workspace_bytes += packed_bytes(M, K);
+        p->flops = 2.0 * (double)M * (double)N * (double)K;
+        return st;
+    }
     if ((config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumQ4Configs)) || splits < 0 ||
         splits > GEMM_F16_MAX_SPLITS)
         return GEMM_F16_ERROR_INVALID_VALUE;
@@ -410,6 +429,13 @@ gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const 
     st = check_device(&dev);
     if (st != GEMM_F16_SUCCESS)
         return st;
+    if (packs(M, N, K, rows_4_aligned(A, K), config, splits)) {
+        if (launch_q4_pack((const _Float16 *)A, (_Float16 *)workspace, M, K, packed_k(K), (hipStream_t)stream) != hipSuccess)
+            return GEMM_F16_ERROR_LAUNCH_FAILED;
+        const int64_t used = packed_bytes(M, K), rest = plan.workspace_bytes - used;
+        return gemm_f16_q4(M, N, packed_k(K), group, workspace, codes, words, C, alpha, epilogue, config, splits,
+                           rest > 0 ? (char *)workspace + used : nullptr, rest, stream);
+    }
     if (K == 0)
         alpha = 1.0f;   // the empty sum is +0 whatever alpha
     if (plan.config == kQ4Expanded) {

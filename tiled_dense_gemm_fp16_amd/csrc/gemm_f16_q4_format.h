@@ -44,6 +44,8 @@ int64_t q4_lds_bytes(const Q4Config &c, int group);
 hipError_t launch_q4(int config, int group, const Q4Args &a, hipStream_t s);
 // The tile kernel: tiles_m x tiles_n x splits workgroups; A's rows 4-byte aligned.
 hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s);
+// A's M rows of K copied to rows of `pitch` (a multiple of 8), zeros behind them.
+hipError_t launch_q4_pack(const _Float16 *A, _Float16 *to, int64_t M, int64_t K, int64_t pitch, hipStream_t s);
 hipError_t launch_q4_compress(const _Float16 *W, uint32_t *codes, uint32_t *words, int64_t N, int64_t K, int group,
                               bool symmetric, hipStream_t s);
 hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float16 *W, int64_t N, int64_t K, int group,

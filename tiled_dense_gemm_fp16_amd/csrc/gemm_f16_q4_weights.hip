@@ -24,6 +24,28 @@ __device__ __forceinline__ half8 row_piece(const half_t *p, int left)
     return v;
 }
 
+// ---- rows made aligned ---------------------------------------------------------------
+// 16 bytes a thread; the products over the copy are what this is for (bound by
+// A's bytes, 3 us for 300 rows of 8193 with the launch).
+__global__ void __launch_bounds__(256) q4_pack_kernel(const half_t *__restrict__ A, half_t *__restrict__ to, int64_t K,
+                                                      int64_t chunks, int64_t pitch)
+{
+    const int64_t row = blockIdx.x / chunks;
+    const int64_t k = (blockIdx.x % chunks * 256 + threadIdx.x) * 8;
+    if (k < pitch)
+        *reinterpret_cast<half8 *>(to + row * pitch + k) = row_piece(A + row * K + k, (int)(K - k < 8 ? K - k : 8));
+}
+
+hipError_t launch_q4_pack(const _Float16 *A, _Float16 *to, int64_t M, int64_t K, int64_t pitch, hipStream_t s)
+{
+    // workgroups of 2048 elements of a row; launches stay below 2^31 threads
+    const int64_t chunks = (pitch + 2047) / 2048, rows = std::max<int64_t>(((int64_t)1 << 22) / chunks, 1);
+    for (int64_t m = 0; m < M; m += rows)
+        hipLaunchKernelGGL(q4_pack_kernel, dim3((unsigned)(std::min(rows, M - m) * chunks)), dim3(256), 0, s, A + m * K,
+                           to + m * pitch, K, chunks, pitch);
+    return hipGetLastError();
+}
+
 // ---- compress and expand ---------------------------------------------------------
 // One wave per 16 x 128 tile.  Lane 16 g + n holds the tile's dwords of row n,
 // k = 32 j + 8 g + 0..7: four 16-byte pieces of the row, and one 16-byte store
