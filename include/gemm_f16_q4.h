@@ -77,8 +77,9 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
  *            rows.  The last one, q4_expanded, runs gemm_f16_q4_expand into the
  *            workspace (2 N K bytes) and the dense product of gemm_f16_scaled,
  *            whose plan its own does not repeat.
- *   splits, workspace, workspace_bytes : as gemm_f16_split; splits 1 with
- *            config AUTO never needs a workspace.
+ *   splits, workspace, workspace_bytes : as gemm_f16_split; the plan's
+ *            workspace may also hold a copy of A with aligned rows (K odd).
+ *            splits 1 with config AUTO never needs a workspace.
  */
 gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, const void *codes,
                               const void *words, void *C, float alpha, int epilogue, int config, int splits,

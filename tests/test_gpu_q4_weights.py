@@ -180,9 +180,9 @@ def test_many_rows(n, k, shift):
 
 
 @pytest.mark.parametrize("m,n,k,shift", [(16, 40, 129, 0), (17, 264, 1001, 1), (40, 9000, 300, 1), (33, 48, 8193, 0), (300, 520, 2047, 0),
-                                         (70, 300, 8, 1), (130, 16400, 33, 3), (20, 30, 1, 0)])
+                                         (70, 300, 8, 1), (130, 16400, 33, 3), (20, 30, 1, 0), (9, 40, 4099, 0)])
 def test_rows_of_odd_length(m, n, k, shift):
-    """From 16 rows A is copied to aligned rows; not with splits=1 or a configuration."""
+    """From 16 rows (8 over long K) A is copied to aligned rows; not with splits=1 or a configuration."""
     for group, splits in ((32, None), (128, None), (64, 1)):
         check(m, n, k, group, shift=shift, splits=splits, epilogue="relu", alpha=0.7)
     w = g.q4_compress(weights(n, k, 0).to(DEV), 64)

@@ -65,10 +65,12 @@ bool rows_4_aligned(const void *A, int64_t K) { return (uintptr_t)A % 4 == 0 && 
 // of them: every kernel but the one that loads single elements becomes possible.
 // us at (M, N x K) without and with the copy: (48, 8192 x 8193) 58, 24; (300, 4096 x
 // 4097) 69, 32; (1000, 8192 x 8193) 494, 143; (2100, 8192 x 8193) 833, 385; (16, 4096 x
-// 4097) 15.8, 8.9; but (16, 20000 x 1001) 9.3, 9.6.
+// 4097) 15.8, 8.9; (8, 8192 x 8193) 21.9, 14.5; but (16, 20000 x 1001) 9.3, 9.6, (8, 20000 x
+// 1001) 8.4, 9.1 and (1, 8192 x 8193) 11.6, 14.0.
 bool packs(int64_t M, int64_t N, int64_t K, bool aligned, int config, int splits)
 {
-    return !aligned && config == GEMM_F16_CONFIG_AUTO && splits == GEMM_F16_SPLITS_AUTO && M >= 16 && N > 0 && K > 0;
+    return !aligned && config == GEMM_F16_CONFIG_AUTO && splits == GEMM_F16_SPLITS_AUTO &&
+           (M >= 16 || (M >= 8 && K >= 4096)) && N > 0 && K > 0;
 }
 int64_t packed_k(int64_t K) { return (K + 7) / 8 * 8; }   // within the last group: the codes' order is the same
 int64_t packed_bytes(int64_t M, int64_t K) { return (2 * M * packed_k(K) + 255) / 256 * 256; }

@@ -85,8 +85,9 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
     fp32 and rounded once; one row reads each code once.
 
     ``splits`` and ``workspace`` as in gemm(): None lets the planner split K
-    when that pays and, from 2048 rows, expand w for the dense product (2 n k
-    bytes), with a workspace from torch's caching allocator; 1 does neither."""
+    when that pays, expand w for the dense product from 2048 rows (2 n k bytes)
+    and copy rows of odd length to aligned ones, with a workspace from torch's
+    caching allocator; 1 does none of it."""
     epi = _EPILOGUES.get(epilogue)
     if epi is None:
         raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
