@@ -71,15 +71,17 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
  * them.  K = 0 writes +0.  Limits: M <= GEMM_F16_MAX_DIM, N and K as gemm_f16.
  *   config : GEMM_F16_CONFIG_AUTO or an index below gemm_f16_q4_num_configs().
  *            The tiles (plan: direct_lds 1) need A's rows 4-byte aligned (K
- *            even), the others nothing.  The last two also round each weight
- *            to binary16 (the value gemm_f16_q4_expand gives) before the
- *            product; all others use it exactly.  AUTO takes them for many
- *            rows.  The last one, q4_expanded, runs gemm_f16_q4_expand into the
- *            workspace (2 N K bytes) and the dense product of gemm_f16_scaled,
- *            whose plan its own does not repeat.
+ *            even), the others nothing.  All of them use the weights s (q - z)
+ *            exactly but the last one, q4_expanded: it runs gemm_f16_q4_expand
+ *            into the workspace (2 N K bytes) and the dense product of
+ *            gemm_f16_scaled, whose plan its own does not repeat, and so rounds
+ *            each weight to binary16 (infinite from 65520 on) before the product.
+ *            AUTO takes it from 2048 rows with groups of 32 and 64, where exact
+ *            products take up to twice the time; never with splits 1.
  *   splits, workspace, workspace_bytes : as gemm_f16_split; the plan's
  *            workspace may also hold a copy of A with aligned rows (K odd).
- *            splits 1 with config AUTO never needs a workspace.
+ *            splits 1 with config AUTO never needs a workspace, and uses every
+ *            weight exactly.
  */
 gemm_f16_status_t gemm_f16_q4(int64_t M, int64_t N, int64_t K, int group, const void *A, const void *codes,
                               const void *words, void *C, float alpha, int epilogue, int config, int splits,

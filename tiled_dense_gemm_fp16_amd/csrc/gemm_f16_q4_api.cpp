@@ -21,7 +21,7 @@ const Q4Config kQ4Configs[kNumQ4Configs] = {
     {"q4_32x64", 2, 4, 8, 0},
     {"q4_32x128", 2, 8, 8, 0},
     {"q4_64x128_s4", 4, 8, 8, 4},
-    {"q4_128x256_s3", 8, 16, 4, 3},
+    {"q4_128x256_s3", 8, 16, 8, 3},
     {"q4_expanded", 0, 0, 0, 0},
 };
 
@@ -102,18 +102,21 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // it starts and ends faster: (64, 28672 x 4096) 28, 39; (128, 14336 x 512) 6.8, 11.8;
     // (300, 5000 x 1024) 9.7, 15.3; (300, 4096 x 4096) 25, 33; but (128, 8192 x 4096) 21.2, 18.8.
     // The 128x256 tile takes over where it makes 64 workgroups for more than
-    // 64 rows: (100, 28672 x 8192) 72, 93; (200, 8192 x 8192) 43, 52; (2048, 8192 x 8192) 240, 350;
-    // but (200, 4096 x 4096) 27, 16, (128, 8192 x 8192) 32, 29 and (64, 28672 x 8192) 69, 50;
-    // and not while the 64x128 tile's workgroups are one round over at most 32
-    // blocks of K, or two over 16 (its time, this one's): (512, 4096 x 4096) 28, 33;
-    // (256, 8192 x 1024) 9.8, 21; (1024, 4096 x 2048) 29, 34; but (1024, 4096 x 4096) 51, 46 and
-    // (512, 14336 x 1024) 32, 21.5.
-    // From 2048 rows, expanding W into a workspace and the dense product take
-    // less: the tile unpacks each code once for 128 rows, in the matrix cores' shadow only
-    // in part.  (us, the tile's and this) (2048, 8192 x 8192) 241, 217; (4096, 8192 x
-    // 8192) 485, 392; (8192, 8192 x 8192) 974, 767; (2048, 5000 x 4100) 159, 130; (8192,
-    // 2048 x 2048) 73, 59; but (2048, 4096 x 4096) 67, 68; (1024, 8192 x 8192) 126, 138 and
-    // (1536, 8192 x 28672) 921, 950.  Not where the caller allows no workspace (1 split).
+    // 64 rows (its time, the 64x128 tile's, with groups of 64): (100, 28672 x 8192) 80, 100;
+    // (200, 8192 x 8192) 47, 49; (1500, 5000 x 4100) 72, 111; but (200, 4096 x 4096) 28, 18,
+    // (128, 8192 x 8192) 34, 30 and (64, 28672 x 8192) 74, 53; and not while the 64x128
+    // tile's workgroups are one round over at most 32 blocks of K, or two over 16:
+    // (512, 4096 x 4096) 35, 26; (256, 8192 x 1024) 20, 9; (1024, 4096 x 2048) 35, 28; but
+    // (1024, 4096 x 4096) 50, 51 and (512, 14336 x 1024) 22, 31.
+    // Both tiles use weights exactly.  From 2048 rows, W expanded to binary16 and
+    // the dense product take less time, but each weight is rounded.  That is only
+    // accepted where it saves most: exact products with groups of 128 take a third
+    // longer at most, so they stay exact; with groups of 64 they take up to half
+    // as long again, with 32 twice as long.  (us, the tile's with groups of 128, 64,
+    // 32, and this) (2048, 8192 x 8192) 271, 284, 373, 205; (8192, 8192 x 8192) 974, 1131,
+    // 1482, 745; (8192, 2048 x 2048) 71, 86, 105, 57; (2048, 4096 x 4096) 65, 74, 98, 63; but
+    // fewer rows, (1024, 8192 x 8192) 147, 155, 188, 136, gain less, and (1536, 8192 x 28672) 759, 920,
+    // 1279, 952.  Not where the caller allows no workspace (1 split).
     const int64_t n_blocks = (N + 15) / 16, blocks = (K + 127) / 128;
     const int large = kQ4Expanded - 1, most_m = M > 16 ? 2 : 1;
     const auto count = [&](int i) {
@@ -122,7 +125,7 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     };
     int c = config;
     if (c == GEMM_F16_CONFIG_AUTO) {
-        if (M >= 2048 && N > 0 && K > 0 && splits == GEMM_F16_SPLITS_AUTO) {
+        if (M >= 2048 && group < 128 && N > 0 && K > 0 && splits == GEMM_F16_SPLITS_AUTO) {
             c = kQ4Expanded;
         } else if (aligned && M > 64 && count(large) >= 64 && count(large - 1) > (blocks <= 16 ? 512 : blocks <= 32 ? 256 : 0)) {
             c = large;

@@ -2,12 +2,11 @@
 // LDS-staged tiles: for many rows of A, bound by the matrix cores, and for the
 // few dozen rows where K is split.
 //
-// A workgroup owns 16 MB rows of A and 16 NW rows of W for each of its waves.  A stage
-// holds 128 k: A's rows (256 bytes each), the waves' tiles of codes (1 KiB for
-// each 16 rows of W) and their words, all moved straight from memory to LDS by
-// buffer_load ... lds, STAGES - 1 stages ahead, with one barrier a stage.
-// Every wave multiplies all of A's rows by its own rows of W, so codes are
-// unpacked once in a workgroup.
+// A workgroup's waves stand in WM rows: each owns 16 MB rows of A and 16 NW rows
+// of W.  A stage holds 128 k: A's rows (256 bytes each), the workgroup's tiles of
+// codes (1 KiB for each 16 rows of W) and their words, all moved straight from
+// memory to LDS by buffer_load ... lds, STAGES - 1 stages ahead, with one barrier
+// a stage.
 //
 // A's rows lie in LDS as 16 chunks of 16 bytes, chunk c of row r in place
 // c ^ (r & 15): a fragment read takes one chunk of 16 rows, which then lie in
@@ -15,22 +14,21 @@
 // direct load fill LDS in order, so the permutation is made by the global
 // address each lane loads.
 //
-// Scales.  With ROUND false the products of a group are summed in fp32 and
+// Scales.  The products of a group are summed in fp32 by the matrix cores and
 // enter the total times the scale, as in the kernel for few rows: one fused
-// multiply-add per output and group.  With ROUND true the scale multiplies
-// q - z in binary16, one rounding of the weight, to the value that q4_expand
-// gives, and the matrix cores add up everything: for many rows vector
-// instructions already fill the matrix cores' shadow, and that multiply-add
-// would cost as much as the products.  The weight's rounding is of the size of
-// the result's own, 2^-11 of each weight at random signs: measured 2.7e-4 of
-// the result's norm from the exact product, against 2.1e-4 for its rounding alone.
+// multiply-add per output and group, so weights are used exactly, whatever the
+// number of rows.  (A weight rounded to binary16 would need no sums of its own:
+// 246, 251 and 273 us at 2048 x 8192 x 8192 with groups of 128, 64 and 32 where this
+// takes 275, 284 and 373; but s (q - z) has up to 15 bits, the rounding is as large as the
+// result's own, and from 65520 on it is infinite.)
 //
-// q4_128x256_s3 (4 waves, ROUND): 2048 x 8192 x 8192, group 128, 238-250 us,
-// 1100-1150 TFLOP/s, against 189 us for the dense kernel on binary16 weights.
-// Bound by issue: a 32-deep step of a wave is 32 matrix instructions (512
-// cycles) and about 70 vector ones (280), which one wave on its SIMD overlaps
-// only in part.  Eight waves of half the rows (two on a SIMD, codes unpacked
-// twice): 247; operands read three steps ahead with a fixed interleaving: 269.
+// q4_128x256_s3 (8 waves): a wave of 128 rows by 32 of W unpacks each code once;
+// for groups of 32, whose multiply-adds fill the vector unit, waves of 64 rows by
+// 64 (two rows of waves, codes unpacked twice, half the reads of LDS) are faster
+// (us at 2048 x 8192 x 8192 with groups of 128, 64, 32: 275, 284, 406 and 277, 299,
+// 373).  Two waves on a SIMD, so that one's vector instructions run beside the
+// other's matrix ones: 4 waves of 128 x 64 take 302, 398, 613.  189 us is the dense
+// kernel's time on binary16 weights.
 //
 // q4_64x128_s4 (8 waves): 64 x 8192 x 8192, group 64, in four parts of K, 14-16 us
 // and 4 for their sum.  Bound by issue again: about 100 vector instructions
@@ -48,10 +46,10 @@ namespace gemm_f16_impl {
 
 typedef _Float16 half8_any __attribute__((ext_vector_type(8), aligned(2)));
 
-template <int GROUP, int MB, int NW, int WAVES_, int STAGES_, bool ROUND>
+template <int GROUP, int MB, int NW, int WM, int WAVES_, int STAGES_>
 struct Q4Tile {
     static constexpr int WAVES = WAVES_, STAGES = STAGES_, GROUPS = 128 / GROUP, PER = GROUP / 32;
-    static constexpr int BM = 16 * MB, BN = 16 * NW * WAVES, N_BLOCKS = NW * WAVES;
+    static constexpr int BM = 16 * MB * WM, BN = 16 * NW * WAVES / WM, N_BLOCKS = NW * WAVES / WM;
     static constexpr int A_BYTES = BM * 256, CODE_BYTES = N_BLOCKS * 1024;
     static constexpr int A_LOADS = BM / 4 / WAVES, CODE_LOADS = N_BLOCKS / WAVES;   // of 1 KiB, for each wave
     static constexpr int WORD_LOADS = (N_BLOCKS * GROUPS / 4 + WAVES - 1) / WAVES;  // of 64 words
@@ -140,7 +138,7 @@ struct Q4Loads {
 };
 
 // TAIL: rows of A end inside a 16-byte chunk (K % 8 != 0).
-template <class T, int MB, int NW, bool ROUND, bool TAIL>
+template <class T, int MB, int NW, int WM, bool TAIL>
 __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
 {
     int tm, tn, split;
@@ -151,7 +149,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
 
     Q4Loads<T> in;
     in.init(p, m0, nb0, end);
-    const int wave = in.wave;
+    const int wave = in.wave / WM, wave_m = in.wave % WM;   // place along W's rows and along A's
     const q4_bits bits;
 
     float4v acc[MB][NW];
@@ -183,45 +181,37 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             for (int q = 0; q < T::GROUPS; ++q)
                 word[nw][q] = ww[nw * (16 * T::GROUPS) + q];
         }
-        float4v sum[MB][NW];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int q = j / T::PER;
-            const unsigned char *x = from + col * 256 + (((4 * j + g) ^ col) * 16);
-            half8 w[NW];
+        for (int q = 0; q < T::GROUPS; ++q) {
+            half8 w[NW][T::PER];
+            float s[NW];
 #pragma unroll
             for (int nw = 0; nw < NW; ++nw) {
-                const unsigned dw = j == 0 ? codes[nw].x : j == 1 ? codes[nw].y : j == 2 ? codes[nw].z : codes[nw].w;
-                w[nw] = q4_codes(dw, bits, q4_zero(word[nw][q]));
-                if constexpr (ROUND) {
-                    const half_t s = __builtin_bit_cast(q4_half2, word[nw][q])[0];
-                    w[nw] *= half8{s, s, s, s, s, s, s, s};
-                }
+                const unsigned dw[4] = {codes[nw].x, codes[nw].y, codes[nw].z, codes[nw].w};
+                const q4_zero zero(word[nw][q]);
+#pragma unroll
+                for (int j = 0; j < T::PER; ++j)
+                    w[nw][j] = q4_codes(dw[q * T::PER + j], bits, zero);
+                s[nw] = q4_scale(word[nw][q]);
             }
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
-                const half8 a = *reinterpret_cast<const half8 *>(x + mb * 4096);
+                float4v sum[NW];
 #pragma unroll
-                for (int nw = 0; nw < NW; ++nw) {
-                    if constexpr (ROUND)
-                        acc[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw], acc[mb][nw], 0, 0, 0);
-                    else
-                        sum[mb][nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                            a, w[nw], j % T::PER == 0 ? float4v{0, 0, 0, 0} : sum[mb][nw], 0, 0, 0);
+                for (int j = 0; j < T::PER; ++j) {
+                    const int chunk = 4 * (q * T::PER + j) + g;
+                    const half8 a = *reinterpret_cast<const half8 *>(from + (wave_m * MB + mb) * 4096 + col * 256 +
+                                                                     (chunk ^ col) * 16);
+#pragma unroll
+                    for (int nw = 0; nw < NW; ++nw)
+                        sum[nw] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, w[nw][j], j == 0 ? float4v{0, 0, 0, 0} : sum[nw],
+                                                                         0, 0, 0);
                 }
-            }
-            if constexpr (!ROUND) {
-                if (j % T::PER == T::PER - 1) {
 #pragma unroll
-                    for (int nw = 0; nw < NW; ++nw) {
-                        const float s = q4_scale(word[nw][q]);
+                for (int nw = 0; nw < NW; ++nw)
 #pragma unroll
-                        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                acc[mb][nw][r] = __builtin_fmaf(s, sum[mb][nw][r], acc[mb][nw][r]);
-                    }
-                }
+                    for (int r = 0; r < 4; ++r)
+                        acc[mb][nw][r] = __builtin_fmaf(s[nw], sum[nw][r], acc[mb][nw][r]);
             }
         }
     };
@@ -246,8 +236,8 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     }
     wait_vmcnt<0>();   // the last requests' zeros land before LDS is used again or given back
 
-    // lane (g, col) holds rows 16 mb + 4 g + r of A, column col of each block
-    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16, wave_n = wave * (16 * NW);
+    // lane (g, col) holds rows 16 mb + 4 g + r of the wave's, column col of each block
+    const int rows = min(p.M - m0, T::BM), n0 = nb0 * 16, wave_n = wave * (16 * NW), row0 = wave_m * (16 * MB);
     if (p.W) {         // partial sums of a split, joined by the reduction kernel
         float *out = p.W + ((int64_t)split * p.M + m0) * p.N;
 #pragma unroll
@@ -257,7 +247,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
             for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const int m = 16 * mb + 4 * g + r;
+                    const int m = row0 + 16 * mb + 4 * g + r;
                     if (m < rows && n < p.N)
                         out[(int64_t)m * p.N + n] = acc[mb][nw][r];
                 }
@@ -276,7 +266,7 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
                 float v = acc[mb][nw][r] * p.alpha;
                 if (p.relu)
                     v = __builtin_fmaxf(v, 0.0f);
-                c[(16 * mb + 4 * g + r) * T::PITCH + wave_n + nw * 16 + col] = (half_t)v;
+                c[(row0 + 16 * mb + 4 * g + r) * T::PITCH + wave_n + nw * 16 + col] = (half_t)v;
             }
     __syncthreads();
     constexpr int CHUNKS = T::BN / 8;
@@ -295,40 +285,38 @@ __device__ __forceinline__ void q4_tile(const Q4Args &p, unsigned char *lds)
     }
 }
 
-template <int GROUP, int MB, int NW, int WAVES, int STAGES, bool ROUND, bool TAIL>
+template <int GROUP, int MB, int NW, int WM, int WAVES, int STAGES, bool TAIL>
 __global__ void __launch_bounds__(64 * WAVES) q4_tile_kernel(Q4Args p)
 {
-    typedef Q4Tile<GROUP, MB, NW, WAVES, STAGES, ROUND> T;
+    typedef Q4Tile<GROUP, MB, NW, WM, WAVES, STAGES> T;
     __shared__ __attribute__((aligned(1024))) unsigned char lds[T::LDS_BYTES];
-    q4_tile<T, MB, NW, ROUND, TAIL>(p, lds);
+    q4_tile<T, MB, NW, WM, TAIL>(p, lds);
 }
 
-template <int MB, int NW, int WAVES, int STAGES, bool ROUND, bool TAIL>
-static hipError_t launch_tile(const Q4Args &a, int group, int64_t grid, hipStream_t s)
+template <int GROUP, bool TAIL>
+static hipError_t launch_config(int config, const Q4Args &a, int64_t grid, hipStream_t s)
 {
-    const dim3 blocks((unsigned)grid), threads(64 * WAVES);
-    if (group == 32)
-        hipLaunchKernelGGL((q4_tile_kernel<32, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
-    else if (group == 64)
-        hipLaunchKernelGGL((q4_tile_kernel<64, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
-    else
-        hipLaunchKernelGGL((q4_tile_kernel<128, MB, NW, WAVES, STAGES, ROUND, TAIL>), blocks, threads, 0, s, a);
+    const dim3 blocks((unsigned)grid), threads(512);
+    constexpr int WM = GROUP == 32 ? 2 : 1;
+    switch (config) {
+    case 5: hipLaunchKernelGGL((q4_tile_kernel<GROUP, 4, 1, 1, 8, 4, TAIL>), blocks, threads, 0, s, a); break;
+    case 6: hipLaunchKernelGGL((q4_tile_kernel<GROUP, 8 / WM, 2 * WM, WM, 8, 3, TAIL>), blocks, threads, 0, s, a); break;
+    default: return hipErrorInvalidValue;
+    }
     return hipGetLastError();
 }
 
-template <bool TAIL>
-static hipError_t launch_config(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
+template <int GROUP>
+static hipError_t launch_group(int config, const Q4Args &a, int64_t grid, hipStream_t s)
 {
-    switch (config) {
-    case 5: return launch_tile<4, 1, 8, 4, false, TAIL>(a, group, grid, s);
-    case 6: return launch_tile<8, 4, 4, 3, true, TAIL>(a, group, grid, s);
-    default: return hipErrorInvalidValue;
-    }
+    return a.K % 8 != 0 ? launch_config<GROUP, true>(config, a, grid, s) : launch_config<GROUP, false>(config, a, grid, s);
 }
 
 hipError_t launch_q4_tile(int config, int group, const Q4Args &a, int64_t grid, hipStream_t s)
 {
-    return a.K % 8 != 0 ? launch_config<true>(config, group, a, grid, s) : launch_config<false>(config, group, a, grid, s);
+    return group == 32   ? launch_group<32>(config, a, grid, s)
+           : group == 64 ? launch_group<64>(config, a, grid, s)
+                         : launch_group<128>(config, a, grid, s);
 }
 
 } // namespace gemm_f16_impl

@@ -85,9 +85,11 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
     fp32 and rounded once; one row reads each code once.
 
     ``splits`` and ``workspace`` as in gemm(): None lets the planner split K
-    when that pays, expand w for the dense product from 2048 rows (2 n k bytes)
-    and copy rows of odd length to aligned ones, with a workspace from torch's
-    caching allocator; 1 does none of it."""
+    when that pays, copy rows of odd length to aligned ones and, from 2048 rows
+    with groups of 32 or 64, expand w for the dense product (2 n k bytes), with a
+    workspace from torch's caching allocator.  The expanded weights are rounded
+    to float16 (infinite from 65520 on); in all other products they are exact.  1
+    does none of it: every weight is used exactly, whatever the number of rows."""
     epi = _EPILOGUES.get(epilogue)
     if epi is None:
         raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
