@@ -77,7 +77,8 @@ gemm_f16_status_t gemm_f16_q4_expand(int64_t N, int64_t K, int group, const void
  *            gemm_f16_scaled, whose plan its own does not repeat, and so rounds
  *            each weight to binary16 (infinite from 65520 on) before the product.
  *            AUTO takes it from 2048 rows with groups of 32 and 64, where exact
- *            products take up to twice the time; never with splits 1.
+ *            products take up to twice the time (but not for few outputs over
+ *            K beyond 1024); never with splits 1.
  *   splits, workspace, workspace_bytes : as gemm_f16_split; the plan's
  *            workspace may also hold a copy of A with aligned rows (K odd).
  *            splits 1 with config AUTO never needs a workspace, and uses every

@@ -55,7 +55,7 @@ def test_every_exact_config(config, group):
 
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("m,n,k", [(1, 300, 384), (17, 300, 384), (40, 300, 1024), (130, 16500, 256), (1100, 6000, 384),
-                                   (2050, 2100, 264), (2050, 40, 512)])
+                                   (2050, 2100, 264), (2050, 40, 512), (2050, 64, 2056), (2500, 300, 4096)])
 def test_automatic_choice_is_exact(m, n, k, group):
     a, packed, want, dense, (one, two) = setup(m, n, k, group, m)
     assert np.array_equal(ref.host(g.gemm_q4(a, packed, splits=1)), want)

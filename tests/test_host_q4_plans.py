@@ -18,3 +18,18 @@ def test_weights_are_rounded_only_where_it_is_said(group):
                 p = g.plan_q4(m, n, k, group, splits=None)
                 assert p["config"] < EXPANDED and p["workspace_bytes"] < 2 * n * k + (p["splits"] > 1) * 2 ** 40 + 2 * m * (k + 256)
     assert g.plan_q4(2048, 8192, 8192, group, splits=None)["config"] == (EXPANDED if group < 128 else EXPANDED - 1)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("n", [1, 16, 64, 128, 256, 512])
+@pytest.mark.parametrize("k", [2048, 8192, 16384])
+def test_few_outputs_over_a_long_k_keep_the_split(n, k, group):
+    """At 2048 rows as at 2047: a few columns of tiles fill the card only with K split, which the dense product never does."""
+    below, at = (g.plan_q4(m, n, k, group, splits=None) for m in (2047, 2048))
+    assert at["config"] == below["config"] < EXPANDED and at["splits"] == below["splits"]
+    assert at["grid"] >= (128 if k == 2048 else 192)
+    for m in (3000, 4000):
+        if m * -(-n // 64) * 64 < 1 << 21:
+            p = g.plan_q4(m, n, k, group, splits=None)
+            assert p["config"] < EXPANDED and p["grid"] >= 128
+    assert g.plan_q4(2048, 2048, k, 64, splits=None)["config"] == EXPANDED

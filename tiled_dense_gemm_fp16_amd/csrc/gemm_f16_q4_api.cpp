@@ -117,15 +117,24 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // 1482, 745; (8192, 2048 x 2048) 71, 86, 105, 57; (2048, 4096 x 4096) 65, 74, 98, 63; but
     // fewer rows, (1024, 8192 x 8192) 147, 155, 188, 136, gain less, and (1536, 8192 x 28672) 759, 920,
     // 1279, 952.  Not where the caller allows no workspace (1 split).
+    // The dense product does not split K: it needs 2^21 outputs (N in whole tiles of
+    // 64) to fill the card, over K of 1024 or less 2^23 to be worth the rounding.  (The
+    // tile's time, this one's, groups of 64) (2048, 64 x 8192) 14, 32; (2048, 256 x 16384) 32,
+    // 60; (2048, 512 x 8192) 32, 37; (2048, 2048 x 1024) 18, 23; but (2048, 2048 x 8192) 88, 64;
+    // (8192, 256 x 8192) 54, 49; (30000, 128 x 8192) 120, 106 and (8192, 2048 x 1024) 45, 35.
+    // Fewer outputs over such a K take either way 5 to 10 us, within 1.5 of each other.
     const int64_t n_blocks = (N + 15) / 16, blocks = (K + 127) / 128;
     const int large = kQ4Expanded - 1, most_m = M > 16 ? 2 : 1;
+    const int64_t outputs = M * ((N + 63) / 64 * 64);
+    const bool expands = M >= 2048 && group < 128 && K > 0 &&
+                         (K > 1024 ? outputs >= 1 << 21 : outputs < 1 << 21 || outputs >= 1 << 23);
     const auto count = [&](int i) {
         const int64_t m = 16 * kQ4Configs[i].m_blocks, n = kQ4Configs[i].n_blocks;
         return (M + m - 1) / m * ((n_blocks + n - 1) / n);
     };
     int c = config;
     if (c == GEMM_F16_CONFIG_AUTO) {
-        if (M >= 2048 && group < 128 && N > 0 && K > 0 && splits == GEMM_F16_SPLITS_AUTO) {
+        if (expands && N > 0 && splits == GEMM_F16_SPLITS_AUTO) {
             c = kQ4Expanded;
         } else if (aligned && M > 64 && count(large) >= 64 && count(large - 1) > (blocks <= 16 ? 512 : blocks <= 32 ? 256 : 0)) {
             c = large;
