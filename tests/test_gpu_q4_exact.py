@@ -87,3 +87,24 @@ def test_scales_whose_largest_value_passes_binary16(group):
         for splits in (1, None):
             if splits == 1 or g.plan_q4(m, n, k, group, splits=splits)["config"] < EXPANDED:
                 assert np.array_equal(ref.host(g.gemm_q4(a.to(DEV), packed, splits=splits)), want), (m, splits)
+
+
+def test_no_room_for_the_expanded_weights():
+    """A product whose automatic workspace the allocator cannot give runs without one."""
+    m, n, k = 2048, 16384, 16384
+    assert g.plan_q4(m, n, k, 64, splits=None)["workspace_bytes"] == 2 * n * k
+    packed = g.q4_compress(torch.randn(n, k, generator=torch.Generator(DEV).manual_seed(0), device=DEV, dtype=torch.float16), 64)
+    a = torch.randn(m, k, generator=torch.Generator(DEV).manual_seed(1), device=DEV, dtype=torch.float16)
+    want, out = g.gemm_q4(a, packed, splits=1), torch.empty(m, n, dtype=torch.float16, device=DEV)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    total = torch.cuda.get_device_properties(0).total_memory
+    try:
+        torch.cuda.set_per_process_memory_fraction((torch.cuda.memory_reserved() + (64 << 20)) / total)
+        assert torch.equal(g.gemm_q4(a, packed, out=out), want)
+        with pytest.raises(torch.OutOfMemoryError):           # asked for, so not replaced
+            g.gemm_q4(a, packed, out=out, config=EXPANDED)
+        assert torch.equal(g.gemm_q4(a[:64], packed, out=out[:64]), g.gemm_q4(a[:64], packed))
+    finally:
+        torch.cuda.set_per_process_memory_fraction(1.0)
+    assert not torch.equal(g.gemm_q4(a, packed), want)        # with room for them the weights are rounded

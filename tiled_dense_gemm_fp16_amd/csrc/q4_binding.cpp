@@ -11,6 +11,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/util/Exception.h>
 #include <hip/hip_runtime_api.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -138,6 +139,7 @@ struct Workspace {
     at::Tensor made;
     void *at = nullptr;
     int64_t bytes = 0;
+    Workspace() = default;
     Workspace(PyObject *given, int64_t need, int index)
     {
         if (given != Py_None) {
@@ -337,7 +339,7 @@ PyObject *gemm(PyObject *const *p)   // a, w, epilogue, out, config, splits, wor
         refuse("inner dimensions differ: a is %lld x %lld, w is %lld x %lld", (long long)m, (long long)k, (long long)w.n,
                (long long)w.k);
     const int epilogue = small(p[2]), config = small(p[4]);
-    const int splits = p[5] == Py_None ? GEMM_F16_SPLITS_AUTO : small(p[5]);
+    int splits = p[5] == Py_None ? GEMM_F16_SPLITS_AUTO : small(p[5]);
     const float alpha = (float)real(p[7]);
     Output out(p[3], {m, w.n}, index);
     int64_t need = 0;
@@ -346,7 +348,14 @@ PyObject *gemm(PyObject *const *p)   // a, w, epilogue, out, config, splits, wor
         check(gemm_f16_plan_q4(m, w.n, k, w.group, from, config, splits, &plan), "gemm_f16_plan_q4");
         need = plan.workspace_bytes;
     }
-    Workspace ws(p[6], need, index);
+    Workspace ws;
+    try {
+        ws = Workspace(p[6], need, index);
+    } catch (const c10::OutOfMemoryError &) {   // every shape also runs without one
+        if (splits != GEMM_F16_SPLITS_AUTO || config != GEMM_F16_CONFIG_AUTO)
+            throw;
+        splits = 1;
+    }
     call(index, "gemm_f16_q4", [&](void *stream) {
         return gemm_f16_q4(m, w.n, k, w.group, from, w.codes, w.words, out.at, alpha, epilogue, config, splits, ws.at, ws.bytes,
                            stream);

@@ -89,7 +89,8 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
     with groups of 32 or 64, expand w for the dense product (2 n k bytes), with a
     workspace from torch's caching allocator.  The expanded weights are rounded
     to float16 (infinite from 65520 on); in all other products they are exact.  1
-    does none of it: every weight is used exactly, whatever the number of rows."""
+    does none of it: every weight is used exactly, whatever the number of rows;
+    None falls back to it where the allocator has no room for the workspace."""
     epi = _EPILOGUES.get(epilogue)
     if epi is None:
         raise ValueError(f"epilogue must be one of {sorted(_EPILOGUES)}, got {epilogue!r}")
