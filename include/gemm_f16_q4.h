@@ -117,7 +117,8 @@ typedef struct gemm_f16_q4_cache {
     int32_t heads, page_size, head_dim, group;
 } gemm_f16_q4_cache_t;
 
-/* Limits (beyond them, and where a launch would have 2^32 work items or more:
+/* Limits (beyond them, where a launch would have 2^32 work items or more, and
+ * where a buffer would have more than 2^56 bytes:
  * GEMM_F16_ERROR_UNSUPPORTED_SIZE). */
 #define GEMM_F16_Q4_MAX_HEADS 4096
 #define GEMM_F16_Q4_MAX_BATCH ((int64_t)1 << 20)

@@ -198,6 +198,10 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     return d.stages > 0 && !launchable(p->grid, p->threads) ? GEMM_F16_ERROR_UNSUPPORTED_SIZE : GEMM_F16_SUCCESS;
 }
 
+// More bytes than an address space has: sizes are refused before their product
+// in 64 bits, or an address plus it, could overflow.
+constexpr int64_t kMostBytes = (int64_t)1 << 56;
+
 // The cache's description and the page table's shape.
 gemm_f16_status_t validate_cache(const gemm_f16_q4_cache_t *c, int64_t batch, int64_t max_pages)
 {
@@ -208,6 +212,9 @@ gemm_f16_status_t validate_cache(const gemm_f16_q4_cache_t *c, int64_t batch, in
     if (c->heads > GEMM_F16_Q4_MAX_HEADS || batch > GEMM_F16_Q4_MAX_BATCH || c->page_size > GEMM_F16_Q4_MAX_PAGE ||
         c->pages > GEMM_F16_Q4_MAX_PAGES || max_pages > GEMM_F16_Q4_MAX_LENGTH / c->page_size)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
+    // (a page's codes have at most 2^35 bytes, its words a quarter of that)
+    if (c->pages > kMostBytes / ((int64_t)c->heads * c->page_size * (c->head_dim / 2)))
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
     if (c->pages > 0 && (!c->k_codes || !c->k_words || !c->v_codes || !c->v_words))
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (((uintptr_t)c->k_codes | (uintptr_t)c->k_words | (uintptr_t)c->v_codes | (uintptr_t)c->v_words) % 16)
@@ -215,8 +222,8 @@ gemm_f16_status_t validate_cache(const gemm_f16_q4_cache_t *c, int64_t batch, in
     return GEMM_F16_SUCCESS;
 }
 
-// Bytes of k_codes (and v_codes), and of k_words (and v_words); sizes are
-// within the limits, so the products fit.
+// Bytes of k_codes (and v_codes), and of k_words (and v_words), at most
+// kMostBytes once the cache is validated.
 int64_t cache_codes_bytes(const gemm_f16_q4_cache_t *c)
 {
     return c->pages * c->heads * c->page_size * (c->head_dim / 2);
@@ -267,9 +274,10 @@ Q4Pages pages_of(const gemm_f16_q4_cache_t *c, const int32_t *table, int64_t bat
     return p;
 }
 
-// Rows of `heads` heads at a pitch of `stride` elements: long enough, 2-byte
-// aligned, and whether 16-byte loads are.
+// Rows of `heads` heads at a pitch of `stride` elements: long enough, within an
+// address space, and whether 16-byte loads are aligned.
 bool rows_fit(int64_t stride, int64_t heads, int head_dim) { return stride >= heads * head_dim; }
+bool rows_reach(int64_t rows, int64_t stride) { return rows <= 0 || stride <= kMostBytes / 2 / rows; }
 bool rows_aligned(const void *p, int64_t stride) { return (uintptr_t)p % 16 == 0 && stride % 8 == 0; }
 int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 0 ? 2 * ((rows - 1) * stride + width) : 0; }
 
@@ -529,6 +537,9 @@ gemm_f16_status_t gemm_f16_q4_cache_append(const gemm_f16_q4_cache_t *cache, int
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (!rows_fit(k_stride, cache->heads, D) || !rows_fit(v_stride, cache->heads, D) || (Q && !rows_fit(q_stride, q_heads, D)))
         return GEMM_F16_ERROR_INVALID_VALUE;
+    if (!rows_reach(tokens, k_stride) || !rows_reach(tokens, v_stride) || (Q && !rows_reach(tokens, q_stride)) ||
+        (cos && positions > kMostBytes / (2 * rotary_dim)))
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
     if (((uintptr_t)K | (uintptr_t)V | (uintptr_t)Q | (uintptr_t)Q_out) & 1u ||
         ((uintptr_t)table | (uintptr_t)lengths | (uintptr_t)starts | (uintptr_t)cos | (uintptr_t)sin) & 3u)
         return GEMM_F16_ERROR_MISALIGNED;
@@ -634,6 +645,8 @@ gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_
     const int64_t width = (int64_t)q_heads * cache->head_dim;
     if (!Q || !out || !lengths || (max_pages > 0 && !table) || (max_pages > 0 && cache->pages == 0) || q_stride < width)
         return GEMM_F16_ERROR_INVALID_VALUE;
+    if (!rows_reach(batch, q_stride))
+        return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
     if (!rows_aligned(Q, q_stride) || (uintptr_t)out % 16 || ((uintptr_t)table | (uintptr_t)lengths) & 3u)
         return GEMM_F16_ERROR_MISALIGNED;
     const int64_t out_bytes = 2 * batch * width, q_bytes = rows_bytes(batch, q_stride, width);

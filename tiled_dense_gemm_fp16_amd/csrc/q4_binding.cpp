@@ -240,9 +240,9 @@ struct Cache {
         if (!codes || codes->dim() != 4)
             refuse("cache.k_codes must be a tensor of pages x heads x page_size x head_dim / 8");
         index = device_of(k, "cache.k_codes", stream_device);
-        const int64_t pages = codes->size(0), heads = codes->size(1), page = codes->size(2), d = 8 * codes->size(3);
-        if (heads > INT32_MAX || page > INT32_MAX || d > INT32_MAX)
+        if (codes->size(1) > INT32_MAX || codes->size(2) > INT32_MAX || codes->size(3) > INT32_MAX / 8)
             refuse("cache.k_codes must be a tensor of pages x heads x page_size x head_dim / 8");
+        const int64_t pages = codes->size(0), heads = codes->size(1), page = codes->size(2), d = 8 * codes->size(3);
         const int64_t words[4] = {pages, heads, d / group, page};
         c.k_codes = buffer(k, "cache.k_codes", at::kInt, codes->sizes(), index);
         c.k_words = buffer(PyTuple_GET_ITEM(cache, 1), "cache.k_words", at::kInt, words, index);
@@ -384,7 +384,7 @@ PyObject *append(PyObject *const *p)   // cache, k, v, table, lengths, starts, q
         if (!t || t->dim() != 2)
             refuse("cos must be a float32 tensor of positions x rotary / 2");
         positions = t->size(0);
-        rotary = 2 * t->size(1);
+        rotary = 2 * std::min<int64_t>(t->size(1), INT32_MAX);
         if (rotary < 16 || rotary > c.head_dim || rotary % 16 || !positions)
             refuse("cos must have 8, 16, ... %d columns and a row at least, got %lld x %lld", (int)(c.head_dim / 2),
                    (long long)positions, (long long)(rotary / 2));
@@ -461,7 +461,9 @@ PyObject *attention(PyObject *const *p)   // q, cache, table, lengths, scale, ou
     int64_t longest = p[8] == Py_None ? 0 : integer(p[8]);
     if (longest < 0)
         refuse("max_length must not be negative");
-    const int64_t room = table.width * c.page_size;
+    int64_t room;   // (a table without rows may be of any width)
+    if (__builtin_mul_overflow(table.width, (int64_t)c.page_size, &room))
+        room = INT64_MAX;
     longest = longest ? std::min(longest, room) : room;
     Output out(p[5], {q.rows, q_heads, (int64_t)c.head_dim}, index);
     int64_t need = 0;
