@@ -192,7 +192,8 @@ gemm_f16_status_t gemm_f16_q4_cache_read(const gemm_f16_q4_cache_t *cache, int64
  *             workspace_bytes, as gemm_f16_split's; NULL when the plan has 1
  *             split.
  * Scores, softmax and sums are fp32; codes enter the matrix cores exactly and
- * probabilities in two binary16 parts; one rounding at the end.
+ * probabilities times scales in two binary16 parts, under a power of two for
+ * each group of d whose scales lie far from the others'; one rounding at the end.
  */
 #define GEMM_F16_Q4_MAX_SPLITS 256
 gemm_f16_status_t gemm_f16_q4_attention(const gemm_f16_q4_cache_t *cache, int64_t batch, int q_heads,

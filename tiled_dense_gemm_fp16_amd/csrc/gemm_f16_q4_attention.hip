@@ -36,11 +36,19 @@
 // groups of 64) 240 remain with SUB 4.
 //
 // p = exp2(x - base), where base is chosen so that P' stays inside binary16:
-// when a block's largest score plus log2 of its largest scale passes base by
+// when a step's largest score plus log2 of its largest scale passes base by
 // more than 15, base moves to 12 below it and the sums are rescaled; between,
-// nothing is (3 bits of slack make that rare).  So P' is below 2^15 and exact
-// to 2^-24, 2^-36 of the largest.  The sums of p and of P' v carry the same
-// factor, which the quotient drops.
+// nothing is (3 bits of slack make that rare).  The two may be different tokens',
+// so where scales of a step differ by more than 5 bits, base moves no further
+// than 6 below the largest p s of any token so far: a large value without weight
+// takes no bits from the others.  A group of d whose own largest p s lies more than
+// 8 bits below 2^12 is lifted by a power of two of its own, taken off its sums at the
+// end, so that its outputs lose none to another group's scale.  So every group's
+// largest P' is between 2^3 and 2^15, and all are exact to 2^-24.  The sums of p and
+// of P' v carry the same factor 2^-base, which the quotient drops.  (Scales of like
+// size skip the tokens' own p s: taken in every wave's first step they cost 0.3 us
+// of 3.7 for one sequence of 100 and 2 of 27 for 32 x 4096; and nothing of this is
+// held in registers, where the two of largest[] cost 2 of 27 us, but in LDS.)
 #include <type_traits>
 
 #include "gemm_f16_q4.h"
@@ -53,6 +61,9 @@ constexpr int WAVES = kQ4AttentionWaves, BLOCK = kQ4AttentionTokens;
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr float kTop = 15.0f, kLift = 12.0f;   // P' stays below 2^kTop and starts below 2^kLift
+constexpr float kLoose = 6.0f;                 // bits that the bound on P' may exceed their largest by, when base moves
+constexpr float kApart = 8.0f;                 // bits between groups of d that share their powers of two
+constexpr float kNone = -0x1p126f;             // base without a token: exp2(kNone) is 0, exp2(-kNone) infinite
 
 // Waves of a SIMD the registers are shared out to: as many as leave the sums,
 // a step's codes and words and the products' operands in registers (groups of
@@ -295,7 +306,21 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     };
     const q4_bits bits;
 
-    float base = -INFINITY, l = 0.0f;
+    float base = kNone, l = 0.0f;
+    // log2 of the largest p s of each group so far, rounded up, is at least base +
+    // kLift - kLoose; once scales have differed by more it is kept where the sums
+    // will go, [group][column]
+    float *const largest = sums + wave * 16 * PITCH + col;
+    bool uneven = false, lifted = false;
+    // 2^exponent(s) is more than |s|, twice that at most; 0 counts as the smallest
+    const auto exponent = [](float v) { return v == 0.0f ? -23.0f : (float)__builtin_amdgcn_frexp_expf(v); };
+    // log2 of the power of two that lifts a group
+    const auto lift = [](float b, float most) {
+        if constexpr (GROUPS == 1)
+            return 0.0f;
+        const float below = b + kLift - most;
+        return below > kApart ? __builtin_floorf(below) : 0.0f;
+    };
     float4v acc[TILES];
 #pragma unroll
     for (int i = 0; i < TILES; ++i)
@@ -327,7 +352,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
                 }
             }
     };
-    const auto attend = [&](int step, const Pages &p, const Step &y, float (&x)[8]) {
+    const auto attend = [&](int step, const Pages &p, const Step &y, float (&x)[8]) __attribute__((always_inline)) {
         const int tg = step * STEP + BLOCK * own + g_token;
         const bool mine = exists(p.own);
         unsigned word[GROUPS][8];
@@ -339,14 +364,16 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
             for (int i = 0; i < 8; ++i)
                 word[n][i] = w[i];
         }
-        if (!__all(mine && tg + 8 <= length)) {   // what lies behind the last token has no weight, whatever it is
+        if (!__all(mine && tg + 8 <= length)) {
+            // what lies behind the last token has no weight, whatever it is, and
+            // a word that is held anyway: of the lane's first token, or 0 without one
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const bool there = mine && tg + i < length;
                 x[i] = there ? x[i] : -INFINITY;
 #pragma unroll
                 for (int n = 0; n < GROUPS; ++n)
-                    word[n][i] = there ? word[n][i] : 0u;
+                    word[n][i] = there ? word[n][i] : i == 0 ? 0u : word[n][0];
             }
         }
         // (the empty asm keeps one conversion of each scale for both uses;
@@ -368,24 +395,78 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 top = __builtin_fmaxf(top, __builtin_fabsf(s[n][i]));
+        const bool some = most != -INFINITY;
         most = column_max(most);
         top = column_max(top);
-        // the place of the largest P', 0 for -infinity times 0 (no token, or scale 0)
-        const float reach = __builtin_fmaf(most, scale, (float)__builtin_amdgcn_frexp_expf(top));
+        // no P' of the step passes this place
+        const float reach = __builtin_fmaf(most, scale, exponent(top));
         const bool grown = reach > base + kTop;
-        if (__any(grown)) {
-            const float to = grown ? reach - kLift : base;
-            const float fade = base == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(base - to);
+        if (lifted || __any(grown)) {
+            // scales within 5 bits of each other: every group has a p s of this size
+            float least = top;
+#pragma unroll
+            for (int n = 0; n < GROUPS; ++n)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    least = __builtin_fminf(least, __builtin_fabsf(s[n][i]));
+            const bool even = !some || least * 32.0f >= top;
+            float to = grown ? reach - kLift : base, f[GROUPS];
+            if (__builtin_expect(!uneven && __all(even || !grown), 1)) {
+#pragma unroll
+                for (int n = 0; n < GROUPS; ++n)
+                    f[n] = 1.0f;
+            } else {
+                // each token's own p s, of the columns that moved or hold a lifted group
+                const bool all_even = column_max(even ? 0.0f : 1.0f) == 0.0f;
+                float most_of[GROUPS], peak = kNone;
+                bool mine = grown, any = false;
+#pragma unroll
+                for (int n = 0; n < GROUPS; ++n) {
+                    most_of[n] = uneven ? largest[16 * n] : base + (kLift - kLoose);
+                    f[n] = lift(base, most_of[n]);
+                    mine |= f[n] > 0.0f;
+                }
+#pragma unroll
+                for (int n = 0; n < GROUPS; ++n) {
+                    float r = kNone;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        r = __builtin_fmaxf(r, __builtin_fmaf(x[i], scale, exponent(s[n][i])));
+                    r = column_max(r);
+                    // (a lifted group's must not be passed; else as above, whatever the other columns do)
+                    r = all_even && f[n] == 0.0f ? reach - kLoose : r;
+                    most_of[n] = mine ? __builtin_fmaxf(most_of[n], r) : most_of[n];
+                    peak = __builtin_fmaxf(peak, most_of[n]);
+                    largest[16 * n] = most_of[n];
+                }
+                q4_wave_fence();
+                to = __builtin_fmaxf(base, __builtin_fminf(to, peak + (kLoose - kLift)));
+#pragma unroll
+                for (int n = 0; n < GROUPS; ++n) {
+                    const float now = lift(to, most_of[n]), up = __builtin_amdgcn_exp2f(now);
+                    any |= now > 0.0f;
+                    f[n] = __builtin_amdgcn_exp2f(now - f[n]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        s[n][i] *= up;
+                }
+                uneven = true;
+                lifted = __any(any);
+            }
+            const float fade = __builtin_amdgcn_exp2f(base - to);
             base = to;
             l *= fade;
 #pragma unroll
-            for (int i = 0; i < TILES; ++i)
-                acc[i] *= fade;
+            for (int n = 0; n < GROUPS; ++n) {
+                f[n] *= fade;
+#pragma unroll
+                for (int i = n * GROUP / 16; i < (n + 1) * GROUP / 16; ++i)
+                    acc[i] *= f[n];
+            }
         }
-        const float from = base == -INFINITY ? 0.0f : -base;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, from));
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -base));
             l += x[i];
         }
 #pragma unroll
@@ -452,6 +533,16 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
         }
     }
     l = column_sum(l);
+    if (lifted) {
+#pragma unroll
+        for (int n = 0; n < GROUPS; ++n) {
+            const float f = __builtin_amdgcn_exp2f(-lift(base, largest[16 * n]));
+#pragma unroll
+            for (int i = n * GROUP / 16; i < (n + 1) * GROUP / 16; ++i)
+                acc[i] *= f;
+        }
+        q4_wave_fence();
+    }
 
     // join the waves and their columns: lane (g, col) holds d = 16 i + 4 g + r
 #pragma unroll
@@ -464,16 +555,15 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_atte
     __syncthreads();
     for (int e = tid; e < rows * (D / 4); e += 64 * WAVES) {
         const int row = e / (D / 4), d = e % (D / 4) * 4;
-        float top = -INFINITY, total = 0.0f;
+        float top = kNone, total = 0.0f;
 #pragma unroll
         for (int w = 0; w < WAVES * SUB; ++w)
             top = __builtin_fmaxf(top, stats[w / SUB * 32 + w % SUB * HEADS + row]);
-        const float from = top == -INFINITY ? 0.0f : top;
         float4v v = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < WAVES * SUB; ++w) {
             const int at = w % SUB * HEADS + row;
-            const float f = __builtin_amdgcn_exp2f(stats[w / SUB * 32 + at] - from);
+            const float f = __builtin_amdgcn_exp2f(stats[w / SUB * 32 + at] - top);
             total += f * stats[w / SUB * 32 + 16 + at];
             const float4v part = *reinterpret_cast<const float4v *>(sums + (w / SUB * 16 + at) * PITCH + d);
             v += f * part;
@@ -519,17 +609,16 @@ __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs 
             total += f * w.y;
             v += f * x;
         };
-        float top = -INFINITY;
+        float top = kNone;
         if constexpr (TEAMS > 1) {   // one head: every wave looks at all parts
             for (int s = threadIdx.x & 63; s < used; s += 64)
                 top = __builtin_fmaxf(top, ml[s].x);
 #pragma unroll
             for (int m = 1; m < 64; m *= 2)
                 top = __builtin_fmaxf(top, __shfl_xor(top, m));
-            const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll 4
             for (int s = team; s < used; s += TEAMS)
-                add(base, ml[s], *reinterpret_cast<const float4v *>(part + s * D));
+                add(top, ml[s], *reinterpret_cast<const float4v *>(part + s * D));
         } else {
             // all parts are read at once, whether the length says that they
             // are used or not: 0.5 us less than one read after the other
@@ -544,11 +633,10 @@ __global__ void __launch_bounds__(256) q4_attention_join_kernel(Q4AttentionArgs 
 #pragma unroll
             for (int i = 0; i < FEW; ++i)
                 top = i < used ? __builtin_fmaxf(top, w[i].x) : top;
-            const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
             for (int i = 0; i < FEW; ++i)
                 if (i < used)
-                    add(base, w[i], x[i]);
+                    add(top, w[i], x[i]);
         }
     }
     if constexpr (TEAMS > 1) {
