@@ -72,9 +72,13 @@ constexpr float kNone = -0x1p126f;             // base without a token: exp2(kNo
 // next step's keys on their way during the softmax and its values during the
 // next scores, in the same registers but for the addresses', 32 x 4096 tokens
 // of groups of 64 take 29 us, not 26.2, and of 128 27.2, not 24.4; only one sequence
-// of 131000 is hardly slower so.
-constexpr int attention_waves(int head_dim, int group)
+// of 131000 is hardly slower so.  Page lookups for every 8 tokens and four blocks
+// side by side do not fit with groups of 64 3 times: with 44 bytes of a lane in
+// scratch, 32 x 4096 tokens in pages of 16 take 34.4 us, not 31.5, and 64 x 4000 59.7, not 49.4.
+constexpr int attention_waves(int head_dim, int group, int sub, bool one)
 {
+    if (head_dim == 128 && group == 64 && sub == 4 && !one)
+        return 2;
     return head_dim == 256 ? (group < 128 ? 1 : 2) : head_dim == 128 && group != 64 ? 2 : 3;
 }
 
@@ -150,7 +154,7 @@ struct AttentionPages {
 // each lane's place in the block.  Else pages are looked up for every granule
 // of 8 tokens.
 template <int D, int GROUP, int SUB, bool ONE>
-__global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP)) q4_attention_kernel(Q4AttentionArgs a)
+__global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE)) q4_attention_kernel(Q4AttentionArgs a)
 {
     constexpr int GROUPS = D / GROUP, JG = GROUP / 32, TILES = D / 16, PITCH = D + 4;
     constexpr int HEADS = 16 / SUB, STEP = BLOCK * SUB;
