@@ -150,9 +150,10 @@ typedef struct gemm_f16_q4_cache {
  * written, and its row of Q_out is zeroed, when its position is negative,
  * past max_pages * page_size or (with cos) not below positions, or its page is
  * not in [0, pages).  Rows of no sequence are left as they were, in the
- * cache and in Q_out.  Sequences must not share the pages they append to, nor
- * a sequence name one of them twice (what such a page then holds of the new
- * tokens is undefined).
+ * cache and in Q_out.  A granule, 8 slots of a page from a multiple of 8 on, is
+ * appended to from one place: not by two sequences, nor by one whose table
+ * names the page twice (what the granule then holds of the new tokens is
+ * undefined; other granules of the page are not touched by it).
  */
 gemm_f16_status_t gemm_f16_q4_cache_append(const gemm_f16_q4_cache_t *cache, int64_t batch, int64_t tokens,
                                            int64_t max_pages, const void *K, int64_t k_stride, const void *V,

@@ -1,5 +1,6 @@
 """GPU tests of the product with 4-bit weights where other tests do not reach:
-rows that hold an infinity, and more rows than one launch's grid holds."""
+rows that hold an infinity, and more rows than one launch's grid holds; and of
+appends that share a page."""
 import numpy as np
 import pytest
 import torch
@@ -48,3 +49,12 @@ def test_more_rows_than_a_grid_holds(splits):
         want = a[i:i + (1 << 18)].double() @ wide.t().contiguous() * 0.5
         worst = max(worst, (got[i:i + (1 << 18)].double() - want).abs().max().item())
     assert worst < 2.0 ** -5                               # half a step of results below 128, and fp32's part of it
+
+
+def test_appends_to_granules_of_one_page():
+    """Two sequences, and one sequence whose table names the page twice, append to neighbouring granules of a page: each slot
+    holds what it would hold alone."""
+    from test_gpu_q4_cache import check_append
+    check_append(128, 64, 32, [0, 8, 16], [8, 5, 3], table=[[0], [0], [0]], positions=32)
+    check_append(64, 32, 32, [8], [24], table=[[3, 3]], positions=64, heads=3)
+    check_append(256, 128, 16, [4, 8], [4, 8], table=[[5], [5]], positions=16)
