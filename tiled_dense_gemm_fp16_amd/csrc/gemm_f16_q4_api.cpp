@@ -63,9 +63,9 @@ bool rows_4_aligned(const void *A, int64_t K) { return (uintptr_t)A % 4 == 0 && 
 // Rows of A that are not 4-byte aligned (an odd K or pointer) are first copied
 // to aligned rows in the workspace, where one is allowed and there are enough
 // of them: every kernel but the one that loads single elements becomes possible.
-// us at (M, N x K) without and with the copy: (48, 8192 x 8193) 58, 24; (300, 4096 x
-// 4097) 69, 32; (1000, 8192 x 8193) 494, 143; (2100, 8192 x 8193) 833, 385; (16, 4096 x
-// 4097) 15.8, 8.9; (8, 8192 x 8193) 21.9, 14.5; but (16, 20000 x 1001) 9.3, 9.6, (8, 20000 x
+// us at (M, N x K) without and with the copy: (48, 8192 x 8193) 57, 24; (300, 4096 x
+// 4097) 68, 31; (1000, 8192 x 8193) 490, 154; (2100, 8192 x 8193) 1040, 386; (16, 4096 x
+// 4097) 14.9, 7.9; (8, 8192 x 8193) 20.9, 14.6; but (16, 20000 x 1001) 9.3, 9.6, (8, 20000 x
 // 1001) 8.4, 9.1 and (1, 8192 x 8193) 11.6, 14.0.
 bool packs(int64_t M, int64_t N, int64_t K, bool aligned, int config, int splits)
 {
@@ -96,8 +96,10 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // With 64 blocks of K or more, splitting K beats narrower workgroups:
     // (24, 2048 x 16384) 18.1 / 13.5 / 12.0 / *11.9 / 13.9; (24, 8192 x 8192) 29.2 / 19.1 /
     // 15.8 / *14.4 / 16.7; and from 33 rows the 64x128 tile does (us, best of the
-    // others): (48, 8192 x 8192) 19.2, 21.3; (64, 28672 x 8192) 49.9, 62.2; (128, 4096 x 14336)
-    // 27.7, 29.2; but (32, 8192 x 8192) 18.1, 16.4 and (64, 5000 x 4100) 12.9, 12.6.
+    // others): (48, 8192 x 8192) 20, 22; (64, 28672 x 8192) 53, 65; (128, 4096 x 14336)
+    // 29, 31; but (32, 8192 x 8192) 18.2, 16.9 and (64, 5000 x 4100) 13.5, 12.8.  Between 4096 and
+    // 8192 of K the border moves with N, within 15 %: (64, 8192 x 7168) 18.8, 20.6; (64, 4096 x
+    // 7168) 14.7, 13.7; (64, 2048 x 8064) 13.9, 12.1; (64, 8192 x 5120) 16.4, 15.6.
     // It also does where the widest workgroup would come in more than one round, as
     // it starts and ends faster: (64, 28672 x 4096) 28, 39; (128, 14336 x 512) 6.8, 11.8;
     // (300, 5000 x 1024) 9.7, 15.3; (300, 4096 x 4096) 25, 33; but (128, 8192 x 4096) 21.2, 18.8.
@@ -113,10 +115,10 @@ gemm_f16_status_t make_plan(int64_t M, int64_t N, int64_t K, int group, bool ali
     // accepted where it saves most: exact products with groups of 128 take a third
     // longer at most, so they stay exact; with groups of 64 they take up to half
     // as long again, with 32 twice as long.  (us, the tile's with groups of 128, 64,
-    // 32, and this) (2048, 8192 x 8192) 271, 284, 373, 205; (8192, 8192 x 8192) 974, 1131,
-    // 1482, 745; (8192, 2048 x 2048) 71, 86, 105, 57; (2048, 4096 x 4096) 65, 74, 98, 63; but
-    // fewer rows, (1024, 8192 x 8192) 147, 155, 188, 136, gain less, and (1536, 8192 x 28672) 759, 920,
-    // 1279, 952.  Not where the caller allows no workspace (1 split).
+    // 32, and this) (2048, 8192 x 8192) 244, 279, 372, 201; (8192, 8192 x 8192) 952, 1094,
+    // 1480, 720; (8192, 2048 x 2048) 71, 86, 105, 57; (2048, 5000 x 4100) 128, 131, 185, 126; but
+    // fewer rows, (1024, 8192 x 8192) 125, 141, 187, 132, gain less, and (1536, 8192 x 28672) 739, 919,
+    // 1279, 950.  Not where the caller allows no workspace (1 split).
     // The dense product does not split K: it needs 2^21 outputs (N in whole tiles of
     // 64) to fill the card, over K of 1024 or less 2^23 to be worth the rounding.  (The
     // tile's time, this one's, groups of 64) (2048, 64 x 8192) 14, 32; (2048, 256 x 16384) 32,
@@ -299,6 +301,9 @@ int64_t rows_bytes(int64_t rows, int64_t stride, int64_t width) { return rows > 
 // costs 2 us at least, so short sequences stay whole (16 x 4 heads of 64 / 128 /
 // 256, whole or in parts: 380 tokens 5.0, 6.4, 10.0 or 6.6, 7.2, 8.7 us; 200
 // tokens 4.4, 5.4, 7.9 or 6.5, 7.2, 8.5; 640 tokens 6.4, 8.5, 13.8 or 7.2, 8.4, 10.0).
+// (Since the exponents of P' follow their groups, times are 1 to 4 % above these.)
+// A table wider than the sequences costs up to a quarter where max_length does not
+// say so: 8 x 1000 tokens 8.0 us, 10.0 with room for 32768; one of 2000 7.7, 9.3.
 gemm_f16_status_t plan_attention(int64_t batch, int q_heads, int heads, int head_dim, int group, int64_t max_length,
                                  int splits, gemm_f16_plan_t *p)
 {

@@ -19,8 +19,10 @@ namespace gemm_f16_impl {
 // granule (about 4096 waves; prompts of up to 1021 tokens of 5 sequences, 48 heads of 128,
 // appended and read back: 30.1 us, 31.0 with 8192 waves, 34.6 with a wave for
 // every head, 37.9 with 2048; 256 sequences of one token, 80 heads: 32.4, 30.5, 44.1, 40.3).  That
-// is 75 % of what a copy of the bytes takes for the prompts; 64 single tokens
-// (5.3 us to append, 7 to read) are bound by the chain of reads.
+// is 75 % of the rate of a copy for the prompts; 64 single tokens (5.7 us to append,
+// 4.2 without starts, 6.1 to read) wait for a chain of reads: the length, the page,
+// the row (which needs neither without starts) and a value's old codes (which need
+// the page only).
 constexpr int kCacheWaves = 4;
 
 __device__ __forceinline__ half8 load8(const half_t *p, bool vec)

@@ -19,25 +19,28 @@
 // multiply-add per output and group, so weights are used exactly, whatever the
 // number of rows.  (A weight rounded to binary16 would need no sums of its own:
 // 246, 251 and 273 us at 2048 x 8192 x 8192 with groups of 128, 64 and 32 where this
-// takes 275, 284 and 373; but s (q - z) has up to 15 bits, the rounding is as large as the
-// result's own, and from 65520 on it is infinite.)
+// took 271, 284 and 373 on the same machine; but s (q - z) has up to 15 bits, the rounding is as large as the
+// result's own, and from 65520 on it is infinite.  Times in this file: captured
+// calls one after the other, codes of random bits, inputs that no cache holds.)
 //
 // q4_128x256_s3 (8 waves): a wave of 128 rows by 32 of W unpacks each code once;
 // for groups of 32, whose multiply-adds fill the vector unit, waves of 64 rows by
 // 64 (two rows of waves, codes unpacked twice, half the reads of LDS) are faster
 // (us at 2048 x 8192 x 8192 with groups of 128, 64, 32: 275, 284, 406 and 277, 299,
 // 373).  Two waves on a SIMD, so that one's vector instructions run beside the
-// other's matrix ones: 4 waves of 128 x 64 take 302, 398, 613.  189 us is the dense
-// kernel's time on binary16 weights.
+// other's matrix ones: 4 waves of 128 x 64 take 302, 398, 613.  Matrix instructions
+// fill half of the SIMDs' cycles, vector ones (64 million) nearly as many; they
+// overlap in part.  With weights of normal distribution, as in the timed case, groups
+// of 128 take 241 (1140 TFLOP/s), and the dense kernel on binary16 weights 189.
 //
-// q4_64x128_s4 (8 waves): 64 x 8192 x 8192, group 64, in four parts of K, 14-16 us
-// and 4 for their sum.  Bound by issue again: about 100 vector instructions
-// and 16 matrix instructions of a wave for each stage, two waves on a SIMD,
-// fill three quarters of its cycles.  Neither 3, 5 or 6 stages, nor two
-// workgroups on a CU (3 stages, 8 parts), nor half the reads of LDS (waves in
+// q4_64x128_s4 (8 waves): 64 x 8192 x 8192, group 64, in four parts of K, 21 us with
+// the 4 of their sum, 18.5 alone under the profiler; whole 47, in two parts 30, in
+// eight 25.  What bounds it is not found: vector instructions take 0.4 of the SIMDs'
+// cycles and matrix ones 0.15, waves wait for 0.3, and neither 3, 5 or 6 stages, nor
+// two workgroups on a CU (3 stages, 8 parts), nor half the reads of LDS (waves in
 // two halves of k, two columns of blocks each), nor workgroups that start at
 // different k change the time by more than 3 %.  Unsplit workgroups of the
-// kernel for few rows take 22-25 us; 4 waves of 32 rows of W 24; 2 x 4 waves 22;
+// kernel for few rows take 23; 4 waves of 32 rows of W 24; 2 x 4 waves 22;
 // codes 8 stages ahead by waves of their own 22; 64 x 256 in 8 parts 23.5.
 #include "gemm_f16_q4_format.h"
 #include "gemm_f16_tile.h"

@@ -51,12 +51,13 @@ hipError_t launch_q4_pack(const _Float16 *A, _Float16 *to, int64_t M, int64_t K,
 // k = 32 j + 8 g + 0..7: four 16-byte pieces of the row, and one 16-byte store
 // of four dwords that is contiguous over the wave.  A group of 32 is one j of
 // the four lanes g, 64 two of them, 128 all four.  Both kernels are bound by the
-// matrix's bytes: at 8192 x 8192 compress takes 30 us (groups of 128; 31 with 32) and
-// expand 32.7 (35.8), 5.6 and 5.2 TB/s, and at 5000 x 4100 with groups of 32, whose
-// rows are only 8-byte aligned, 14.5 and 15.2.  Compress reads the pieces as the
-// tile has them, 64 bytes of a row by four lanes (through LDS, whole rows of
-// 256 bytes at once: 35 us at 8192 x 8192 with groups of 32); expand writes whole rows
-// by way of LDS (64 bytes each: 38.5).
+// matrix's bytes: at 8192 x 8192 compress takes 32 us (groups of 128; 34 with 32) and
+// expand 32.5 (36), 5.3 and 5.2 TB/s, over inputs that no cache holds (26 to expand
+// codes just written), and at 5000 x 4100 with groups of 32, whose rows are only
+// 8-byte aligned, 15.5 and 16.6.  Compress reads the pieces as the tile has them, 64
+// bytes of a row by four lanes (whole rows of 256 bytes at once, through LDS, took 35
+// where this took 31); expand writes whole rows by way of LDS (64 bytes each took
+// 38.5, where this took 32.7).
 
 // A tile row's words, loaded and stored at once.
 template <int GROUPS>
@@ -232,7 +233,7 @@ hipError_t launch_q4_expand(const uint32_t *codes, const uint32_t *words, _Float
 //
 // 1 x 28672 x 8192 with groups of 128 takes 26.2 us, 4.8 TB/s of codes and words,
 // 0.92 of what a copy reaches; 13 x 5000 x 4100 with groups of 32, one round of
-// workgroups of which each wave takes 4 or 5 blocks, 7.6 us: latency.  A wider
+// workgroups of which each wave takes 4 or 5 blocks one after the other, 7.6 us.  A wider
 // workgroup of 64 x 128 outputs spills (43 us at 64 x 8192 x 8192, 27 with 4 waves).
 
 template <int GROUPS>
