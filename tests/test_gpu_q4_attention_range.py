@@ -27,9 +27,9 @@ DEV = "cuda:0"
 SMALL, TINY, ONE, LARGE = 2.0 ** -14, 2.0 ** -24, 1.0, 4096.0     # 15 x 4096 is below binary16's largest
 
 
-def attend(cache, tab, lengths, q, scale, got, page):
+def attend(cache, tab, lengths, q, scale, got, page, exact=False):
     """Every head's output against the definition, with each group's own largest p s in its bound.  Returns how many
-    elements are large against their bound."""
+    elements are large against their bound.  exact: scores have no error."""
     c = arrays(cache)
     keys, values = c.values("k"), c.values("v")
     ks, kz = ref.scale_zero(c.word["k"])
@@ -49,7 +49,7 @@ def attend(cache, tab, lengths, q, scale, got, page):
             p = np.exp(x - x.max())
             p /= p.sum()
             want, mass, most = p @ v, p @ np.abs(v), (p[:, None] * s).max(0)
-            off = (dim / 32 + 40) * 2.0 ** -23 * abs(scale) * 1.4427 * (w @ np.abs(q[b, h])) + 2.0 ** -21      # of each p
+            off = (dim / 32 + 40) * 2.0 ** -23 * abs(scale) * 1.4427 * (w @ np.abs(q[b, h])) * (not exact) + 2.0 ** -21   # of p
             eps = 2.0 ** -20 + (96 + len(pos) / 16) * 2.0 ** -23
             tol = (ref.half_steps(want) * (1 + 2.0 ** -10) + (p * off) @ np.abs(v) + (p @ off + eps) * mass +
                    len(pos) * 2.0 ** -23 * most)
@@ -150,3 +150,29 @@ def test_scales_that_move_with_the_scores(rising):
         for splits in (1, 2, None):
             got = g.attention_q4(q.to(DEV), cache, i32(tab), i32([n]), scale=scale, splits=splits)
             attend(cache, tab, [n], q.double().numpy(), scale, ref.host(got), page)
+
+
+@pytest.mark.parametrize("dim,group", KINDS)
+@pytest.mark.parametrize("ratio", [1, 8, 16])
+@pytest.mark.parametrize("power", [16, 20, 23, 24, 26, 30, 36])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(dim, group, ratio, power, sign):
+    """Scores up to 2^36: the tokens with the largest one share the weight, all others are far behind.
+
+    Every element of a key is s times a code difference, of a query 1 or -1, so that a token's score is dim times a small
+    integer times a power of two, exact in fp32, equal for equal tokens and at least 2^13 apart for others; the output is
+    the mean of the first ones' values."""
+    page, lengths, order = 16, [200, 33, 1], gen(power)
+    tab = make_table(lengths, page, 24, 1, WIDE // page)
+    cache = noise_cache(24, 1, page, dim, group, power)
+    steps = torch.randint(9, 16, (24, page), generator=order) - 8          # 1 .. 7
+    cache.k_codes.copy_(((steps + 8) * 0x11111111 - (1 << 32)).to(torch.int32)[:, None, :, None].expand(cache.k_codes.shape))
+    unit = 2.0 ** (power - 3) / dim                                         # scores: steps times unit times dim
+    key = min(unit, 2.0 ** 12)
+    cache.k_words.fill_((int(torch.tensor(key).to(torch.float16).view(torch.int16)) & 0xFFFF) | 8 << 16)
+    q = torch.full((3, ratio, dim), float(sign), dtype=torch.float16)
+    scale = unit / key
+    for splits in (1, 2, 5):
+        got = g.attention_q4(q.to(DEV), cache, i32(tab), i32(lengths), scale=scale, splits=splits)
+        checked = attend(cache, tab, lengths, q.double().numpy(), scale, ref.host(got), page, exact=True)
+        assert checked > 0

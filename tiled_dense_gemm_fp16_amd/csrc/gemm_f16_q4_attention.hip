@@ -44,11 +44,14 @@
 // takes no bits from the others.  A group of d whose own largest p s lies more than
 // 8 bits below 2^12 is lifted by a power of two of its own, taken off its sums at the
 // end, so that its outputs lose none to another group's scale.  So every group's
-// largest P' is between 2^3 and 2^15, and all are exact to 2^-24.  The sums of p and
-// of P' v carry the same factor 2^-base, which the quotient drops.  (Scales of like
-// size skip the tokens' own p s: taken in every wave's first step they cost 0.3 us
-// of 3.7 for one sequence of 100 and 2 of 27 for 32 x 4096; and nothing of this is
-// held in registers, where the two of largest[] cost 2 of 27 us, but in LDS.)
+// largest P' is between 2^3 and 2^15, and all are exact to 2^-24.  From scores of 2^23
+// on, whose rounding reaches whole powers of two, base is the largest score itself,
+// rounded as the scores are: tokens that share it share the weight, with P' = s.
+// The sums of p and of P' v carry the same factor 2^-base, which the quotient drops.
+//
+// Scales of like size skip the tokens' own p s: taken in every wave's first step
+// they cost 0.3 us of 3.7 for one sequence of 100 and 2 of 27 for 32 x 4096.  And
+// nothing of this is held in registers, where largest[] costs 2 of 27 us, but in LDS.
 #include <type_traits>
 
 #include "gemm_f16_q4.h"
@@ -63,6 +66,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTop = 15.0f, kLift = 12.0f;   // P' stays below 2^kTop and starts below 2^kLift
 constexpr float kLoose = 6.0f;                 // bits that the bound on P' may exceed their largest by, when base moves
 constexpr float kApart = 8.0f;                 // bits between groups of d that share their powers of two
+constexpr float kFar = 0x1p23f;                // scores whose rounding reaches whole powers of two
 constexpr float kNone = -0x1p126f;             // base without a token: exp2(kNone) is 0, exp2(-kNone) infinite
 
 // Waves of a SIMD the registers are shared out to: as many as leave the sums,
@@ -315,7 +319,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
     // kLift - kLoose; once scales have differed by more it is kept where the sums
     // will go, [group][column]
     float *const largest = sums + wave * 16 * PITCH + col;
-    bool uneven = false, lifted = false;
+    bool uneven = false, lifted = false, far = false;
     // 2^exponent(s) is more than |s|, twice that at most; 0 counts as the smallest
     const auto exponent = [](float v) { return v == 0.0f ? -23.0f : (float)__builtin_amdgcn_frexp_expf(v); };
     // log2 of the power of two that lifts a group
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
         if constexpr (GROUPS == 1)
             return 0.0f;
         const float below = b + kLift - most;
-        return below > kApart ? __builtin_floorf(below) : 0.0f;
+        return below > kApart && __builtin_fabsf(b) < kFar ? __builtin_floorf(below) : 0.0f;
     };
     float4v acc[TILES];
 #pragma unroll
@@ -405,7 +409,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
         // no P' of the step passes this place
         const float reach = __builtin_fmaf(most, scale, exponent(top));
         const bool grown = reach > base + kTop;
-        if (lifted || __any(grown)) {
+        if (lifted || far || __any(grown)) {
             // scales within 5 bits of each other: every group has a p s of this size
             float least = top;
 #pragma unroll
@@ -414,7 +418,11 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
                 for (int i = 0; i < 8; ++i)
                     least = __builtin_fminf(least, __builtin_fabsf(s[n][i]));
             const bool even = !some || least * 32.0f >= top;
-            float to = grown ? reach - kLift : base, f[GROUPS];
+            // where 12 is lost in the score's rounding, base is the score itself
+            float peak_score = most * scale;
+            asm("" : "+v"(peak_score));   // (not contracted with what follows)
+            const bool beyond = __builtin_fabsf(peak_score) >= kFar;
+            float to = beyond ? __builtin_fmaxf(base, peak_score) : grown ? reach - kLift : base, f[GROUPS];
             if (__builtin_expect(!uneven && __all(even || !grown), 1)) {
 #pragma unroll
                 for (int n = 0; n < GROUPS; ++n)
@@ -444,7 +452,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
                     largest[16 * n] = most_of[n];
                 }
                 q4_wave_fence();
-                to = __builtin_fmaxf(base, __builtin_fminf(to, peak + (kLoose - kLift)));
+                to = beyond ? to : __builtin_fmaxf(base, __builtin_fminf(to, peak + (kLoose - kLift)));
 #pragma unroll
                 for (int n = 0; n < GROUPS; ++n) {
                     const float now = lift(to, most_of[n]), up = __builtin_amdgcn_exp2f(now);
@@ -459,6 +467,7 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
             }
             const float fade = __builtin_amdgcn_exp2f(base - to);
             base = to;
+            far = __any(__builtin_fabsf(base) >= kFar && base > kNone);
             l *= fade;
 #pragma unroll
             for (int n = 0; n < GROUPS; ++n) {
@@ -468,11 +477,22 @@ __global__ void __launch_bounds__(64 * WAVES, attention_waves(D, GROUP, SUB, ONE
                     acc[i] *= f[n];
             }
         }
+        if (__builtin_expect(far, 0)) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -base));
-            l += x[i];
+            for (int i = 0; i < 8; ++i) {
+                float t = x[i] * scale;
+                asm("" : "+v"(t));
+                const float d = __builtin_fabsf(base) >= kFar ? t - base : __builtin_fmaf(x[i], scale, -base);
+                x[i] = __builtin_amdgcn_exp2f(d);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], scale, -base));
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            l += x[i];
 #pragma unroll
         for (int n = 0; n < GROUPS; ++n) {
             const unsigned *w = word[n];
