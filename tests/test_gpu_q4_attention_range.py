@@ -176,3 +176,45 @@ def test_scores_of_any_size(dim, group, ratio, power, sign):
         got = g.attention_q4(q.to(DEV), cache, i32(tab), i32(lengths), scale=scale, splits=splits)
         checked = attend(cache, tab, lengths, q.double().numpy(), scale, ref.host(got), page, exact=True)
         assert checked > 0
+
+
+@pytest.mark.parametrize("dim,group", KINDS)
+@pytest.mark.parametrize("ratio", [1, 4, 8, 16])
+def test_scales_of_any_size_in_whole_pages(dim, group, ratio):
+    """As test_scales_of_any_size, in pages that hold whole blocks of tokens, with pages left out and empty sequences."""
+    lengths, page = [3, 0, 65, 128, 500, 31], 64
+    for seed in range(4):
+        tab = make_table(lengths, page, 24, seed, WIDE // page if seed % 2 else None)
+        tab[4][2] = tab[3][0] = -1
+        cache = noise_cache(24, 2, page, dim, group, seed)
+        r = gen(seed + 19)
+        size = 2.0 ** torch.randint(-24, 13, cache.v_words.shape, generator=r).float()
+        size[torch.rand(cache.v_words.shape, generator=r) < 0.1] = 0.0
+        set_scales(cache, size)
+        for spread in (0.3, 4.0):
+            run(cache, tab, lengths, 2 * ratio, page, spread=spread, seed=seed, splits=(1, 2, 5, None)[seed])
+
+
+def test_far_scores_stay_in_their_head():
+    """A head whose scores pass 2^23, and one with groups far apart, do not change a bit of the heads beside them."""
+    for width, ratio in ((32, 4), (1024, 4), (1024, 8)):
+        cache = noise_cache(100, 2, 16, 128, 64, 0)
+        lengths = [90, 300, 40, 500]
+        table = i32(make_table(lengths, 16, 100, 0, width))
+        q = torch.randn(4, 2 * ratio, 128, generator=gen(1)).to(torch.float16).to(DEV)
+        want = g.attention_q4(q, cache, table, i32(lengths))
+        odd = q.clone()
+        odd[1, 3] *= 2.0 ** 14
+        odd[2, ratio + 1] *= -2.0 ** 12
+        scale = 128 ** -0.5
+        got = g.attention_q4(odd, cache, table, i32(lengths), scale=scale)
+        keep = torch.ones(4, 2 * ratio, dtype=torch.bool, device=DEV)
+        keep[1, 3] = keep[2, ratio + 1] = False
+        assert torch.equal(got[keep], want[keep]) and bool(got.isfinite().all())
+        huge = q.clone()
+        huge[0, 0], huge[3, 2 * ratio - 1] = 60000.0, -60000.0
+        got = g.attention_q4(huge, cache, table, i32(lengths), scale=1000.0)
+        want = g.attention_q4(q, cache, table, i32(lengths), scale=1000.0)
+        keep = torch.ones(4, 2 * ratio, dtype=torch.bool, device=DEV)
+        keep[0, 0] = keep[3, 2 * ratio - 1] = False
+        assert torch.equal(got[keep], want[keep]) and bool(got.isfinite().all())

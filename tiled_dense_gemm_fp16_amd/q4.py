@@ -86,8 +86,8 @@ def gemm_q4(a, w: Q4Matrix, epilogue: str = "none", out=None, config: int = CONF
 
     ``splits`` and ``workspace`` as in gemm(): None lets the planner split K
     when that pays, copy rows of odd length to aligned ones and, from 2048 rows
-    with groups of 32 or 64, expand w for the dense product (2 n k bytes), with a
-    workspace from torch's caching allocator.  The expanded weights are rounded
+    with groups of 32 or 64, expand w for the dense product (2 n k bytes) unless its
+    outputs are few, with a workspace from torch's caching allocator.  The expanded weights are rounded
     to float16 (infinite from 65520 on); in all other products they are exact.  1
     does none of it: every weight is used exactly, whatever the number of rows;
     None falls back to it where the allocator has no room for the workspace."""
