@@ -17,6 +17,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgemm_f16.so")
 BINDING_PATH = os.path.join(_HERE, "_q4_binding.so")
+I8_BINDING_PATH = os.path.join(_HERE, "_i8_binding.so")
 PROBE_LIB_PATH = os.path.join(_HERE, "libgemm_f16_probe.so")
 
 SUCCESS = 0
@@ -91,6 +92,23 @@ Q4_SIGNATURES = {
     "gemm_f16_q4_config_name": ([_int], ctypes.c_char_p),
 }
 
+# the products with 8-bit operands and the routed experts (mirrors include/gemm_f16_i8.h)
+I8_SIGNATURES = {
+    "gemm_f16_i8_pitch": ([_i64], _i64),
+    "gemm_f16_i8_compress": ([_i64, _i64, _vp, _i64, _vp, _vp, _vp], _int),
+    "gemm_f16_i8_expand": ([_i64, _i64, _vp, _i64, _vp, _vp, _vp], _int),
+    "gemm_f16_i8": ([_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _f32, _int, _int, _int, _vp, _i64, _vp], _int),
+    "gemm_f16_plan_i8": ([_i64, _i64, _i64, _int, _int, ctypes.POINTER(Plan)], _int),
+    "gemm_f16_i8_num_configs": ([], _int),
+    "gemm_f16_i8_config_name": ([_int], ctypes.c_char_p),
+    "gemm_f16_route": ([_i64, _int, _int, _vp, _int, _i64, _int, _vp, _int, _int, _int, _f32, _vp, _vp, _vp], _int),
+    "gemm_f16_expert_order": ([_i64, _int, _vp, _vp, _vp, _vp], _int),
+    "gemm_f16_i8_experts": ([_i64, _i64, _int, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _f32, _int, _int, _vp],
+                            _int),
+    "gemm_f16_plan_i8_experts": ([_i64, _i64, _int, _i64, _i64, _int, ctypes.POINTER(Plan)], _int),
+    "gemm_f16_expert_sum": ([_i64, _i64, _i64, _vp, _vp, _vp, _vp], _int),
+}
+
 _lib = None
 
 
@@ -118,7 +136,7 @@ def lib() -> ctypes.CDLL:
             raise RuntimeError(f"{LIB_PATH} is missing: build the HIP library first "
                                "(python -c 'import __graft_entry__ as g; g.build()')")
         h = ctypes.CDLL(LIB_PATH)
-        for name, (args, res) in {**SIGNATURES, **Q4_SIGNATURES}.items():
+        for name, (args, res) in {**SIGNATURES, **Q4_SIGNATURES, **I8_SIGNATURES}.items():
             fn = getattr(h, name)
             fn.argtypes = args
             fn.restype = res
@@ -464,3 +482,8 @@ def probe_mfma_tflops(mode: int, seconds: float = 0.3, seed: int = 0) -> float:
 
 from .q4 import (Q4Cache, Q4Matrix, attention_q4, gemm_q4, plan_attention_q4, plan_q4, q4_cache,  # noqa: E402,F401
                  q4_cache_append, q4_cache_read, q4_compress, q4_config_name, q4_expand, q4_num_configs)
+
+# ---- products with 8-bit operands, routed experts (include/gemm_f16_i8.h) ------------------
+
+from .i8 import (ExpertOrder, I8Matrix, expert_order, expert_sum, gemm_i8, gemm_i8_experts, i8_compress,  # noqa: E402,F401
+                 i8_config_name, i8_expand, i8_num_configs, plan_i8, plan_i8_experts, route)

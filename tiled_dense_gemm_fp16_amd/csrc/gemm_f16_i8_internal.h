@@ -1,0 +1,70 @@
+// gemm_f16_i8_internal.h -- shared between the host API of the 8-bit operators
+// and the routed experts (gemm_f16_i8_api.cpp) and their kernels.  Not part of
+// the public ABI.
+#ifndef GEMM_F16_I8_INTERNAL_H
+#define GEMM_F16_I8_INTERNAL_H
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_f16_i8.h"
+#include "gemm_f16_internal.h"
+
+namespace gemm_f16_impl {
+
+// A compiled configuration of the product.
+struct I8Config {
+    const char *name;
+    int block_m, block_n;
+    int waves;
+    int stages;   // LDS stages of 128 bytes of k; 0: the kernel for few rows, which takes its operands straight from memory
+};
+constexpr int kI8BlockK = 128;       // k of a tile's step
+constexpr int kI8StreamK = 256;      // k of a step of the kernel for few rows
+constexpr int kNumI8Configs = 4;
+extern const I8Config kI8Configs[kNumI8Configs];
+
+struct I8Args {
+    const int8_t *A, *W;
+    const float *a_scales, *w_scales;
+    _Float16 *C;
+    int *partial;          // a split's sums: splits x M x N; null unless split
+    int64_t a_pitch, w_pitch;   // bytes, at most 2^22
+    int M, N, K;           // M rows of A; K rounded up to a multiple of 16
+    int tiles_m, tiles_n;  // (experts: tiles_m is what the grid has room for)
+    int splits, k_split;   // k of a split, a multiple of the configuration's step; >= K unless split
+    float alpha;
+    int relu;
+    int vec_c;             // 8: C's rows take 16-byte stores; 4: 8-byte; 1: 2-byte
+    // experts: W is experts x N rows, and C has a row for each pair
+    const int32_t *order, *starts;
+    int experts, pairs, pairs_per_row;
+};
+
+hipError_t launch_i8(int config, const I8Args &a, int64_t grid, hipStream_t s);
+hipError_t launch_i8_experts(int config, const I8Args &a, int64_t grid, hipStream_t s);
+// C = rne16(epi(alpha a_scales w_scales (sum of the splits' partial sums)))
+hipError_t launch_i8_reduce(const I8Args &a, hipStream_t s);
+
+hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, float *scales, int64_t rows, int64_t K,
+                              hipStream_t s);
+hipError_t launch_i8_expand(const int8_t *codes, int64_t pitch, const float *scales, _Float16 *X, int64_t rows, int64_t K,
+                            hipStream_t s);
+
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int64_t stride;
+    int tokens, experts, top_k, half, sigmoid, groups, top_groups, renormalise;
+    float scale;
+};
+hipError_t launch_route(const RouteArgs &a, hipStream_t s);
+hipError_t launch_expert_order(const int32_t *ids, int32_t *order, int32_t *starts, int pairs, int experts, hipStream_t s);
+hipError_t launch_expert_sum(const _Float16 *Y, const float *weights, _Float16 *out, int64_t tokens, int top_k, int64_t N,
+                             hipStream_t s);
+
+} // namespace gemm_f16_impl
+
+#endif

@@ -1,0 +1,246 @@
+// gemm_f16_i8_rows.hip -- rows of binary16 to 8-bit codes and back, and the
+// weighted sum of the experts' results: kernels that read and write each
+// element once and are bound by memory.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gemm_f16_i8_internal.h"
+
+namespace gemm_f16_impl {
+
+namespace {
+
+typedef _Float16 half_t;
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef half8 half8_any __attribute__((aligned(2)));   // 16-byte accesses at any element's address
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+// Sixteen elements of a row from column c on, zeros past K.
+__device__ __forceinline__ void load16(const half_t *row, int64_t K, int64_t c, half_t (&x)[16])
+{
+    if (c + 16 <= K) {
+        const half8 lo = *reinterpret_cast<const half8_any *>(row + c), hi = *reinterpret_cast<const half8_any *>(row + c + 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = lo[i];
+            x[8 + i] = hi[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = c + i < K ? row[c + i] : (half_t)0;
+    }
+}
+
+// NaN as 0, infinities as 65504
+__device__ __forceinline__ float finite(half_t x)
+{
+    const float f = (float)x;
+    return f != f ? 0.0f : __builtin_fminf(__builtin_fmaxf(f, -65504.0f), 65504.0f);
+}
+
+// rint(127 x / m) for binary16 |x| <= m.  t = 127 x is exact in fp32 (18 bits).
+// y is the quotient but for 2^-22 of itself; r = t - y m is exact (at most 2^-22
+// of t, on a grid of 2^-33 of it), so y + r / m is the quotient but for 2^-46 of
+// itself, rounded once to fp32: exactly the half where the quotient is one.  Any
+// other quotient near a half h in 2^(6 - e) .. 2^(7 - e) differs from it by at least
+// 2^-(11 + e) (an integer over m's 11 bits, shifted by as much as x is smaller),
+// while half a step of fp32 there is 2^-(18 + e).
+__device__ __forceinline__ int code_of(float x, float m, float inverse)
+{
+    const float t = 127.0f * x;
+    float y = t * inverse;
+    y = __builtin_fmaf(__builtin_fmaf(-y, m, t), inverse, y);
+    return (int)__builtin_rintf(y);
+}
+
+// THREADS threads of a workgroup of 256 take a row, 16 elements each at a time;
+// up to HELD of those stay in registers between the search for the largest
+// magnitude and the rounding, longer rows are read again.
+template <int THREADS, int HELD>
+__global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restrict__ X, int64_t stride, int8_t *__restrict__ codes,
+                                                          float *__restrict__ scales, int64_t rows, int64_t K)
+{
+    constexpr int ROWS = 256 / THREADS;
+    __shared__ float most_of[4];
+    const int t = threadIdx.x % THREADS;
+    const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS, pitch = (K + 15) / 16 * 16;
+    if (THREADS <= 64 && r >= rows)
+        return;
+    const half_t *row = X + r * stride;
+    half_t x[HELD][16];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int64_t c = 16 * (int64_t)(t + i * THREADS);
+        if (c < K) {
+            load16(row, K, c, x[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                x[i][j] = (half_t)0;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < HELD; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            m = __builtin_fmaxf(m, __builtin_fabsf(finite(x[i][j])));
+    for (int64_t c = 16 * (int64_t)(t + HELD * THREADS); c < K; c += 16 * THREADS) {
+        half_t y[16];
+        load16(row, K, c, y);
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            m = __builtin_fmaxf(m, __builtin_fabsf(finite(y[j])));
+    }
+#pragma unroll
+    for (int d = 1; d < (THREADS < 64 ? THREADS : 64); d *= 2)
+        m = __builtin_fmaxf(m, __shfl_xor(m, d));
+    if constexpr (THREADS > 64) {
+        if (threadIdx.x % 64 == 0)
+            most_of[threadIdx.x / 64] = m;
+        __syncthreads();
+        m = __builtin_fmaxf(__builtin_fmaxf(most_of[0], most_of[1]), __builtin_fmaxf(most_of[2], most_of[3]));
+    }
+    const float inverse = m > 0.0f ? 1.0f / m : 0.0f;
+    if (t == 0)
+        scales[r] = m / 127.0f;
+    const auto put = [&](int64_t c, const half_t (&y)[16]) {
+        int4v v;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            int packed = 0;
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                packed |= (code_of(finite(y[4 * w + b]), m, inverse) & 255) << (8 * b);
+            v[w] = packed;
+        }
+        *reinterpret_cast<int4v *>(codes + r * pitch + c) = v;
+    };
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+        const int64_t c = 16 * (int64_t)(t + i * THREADS);
+        if (c < K)
+            put(c, x[i]);
+    }
+    for (int64_t c = 16 * (int64_t)(t + HELD * THREADS); c < K; c += 16 * THREADS) {
+        half_t y[16];
+        load16(row, K, c, y);
+        put(c, y);
+    }
+}
+
+// Sixteen codes of a row a thread.
+__global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ codes, int64_t pitch,
+                                                        const float *__restrict__ scales, half_t *__restrict__ X, int64_t items,
+                                                        int64_t K, int64_t per_row)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / per_row, c = (i - r * per_row) * 16;
+        const int4v v = *reinterpret_cast<const int4v *>(codes + r * pitch + c);
+        const float s = scales[r];
+        half_t x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            x[j] = (half_t)(s * (float)((int)((unsigned)v[j / 4] << (24 - 8 * (j % 4))) >> 24));
+        half_t *to = X + r * K + c;
+        if (c + 16 <= K) {
+            *reinterpret_cast<half8_any *>(to) = half8{x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]};
+            *reinterpret_cast<half8_any *>(to + 8) = half8{x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]};
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < K)
+                    to[j] = x[j];
+        }
+    }
+}
+
+// Eight columns of a token's sum a thread, in fp32 and in the order of the slots.
+__global__ void __launch_bounds__(256) expert_sum_kernel(const half_t *__restrict__ Y, const float *__restrict__ weights,
+                                                         half_t *__restrict__ out, int64_t items, int top_k, int64_t N,
+                                                         int64_t per_row)
+{
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per_row, c = (i - t * per_row) * 8;
+        const half_t *from = Y + t * top_k * N + c;
+        const float *w = weights + t * top_k;
+        const int n = (int)(N - c < 8 ? N - c : 8);
+        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int j = 0; j < top_k; ++j, from += N) {
+            const float wj = w[j];
+            if (n == 8) {
+                const half8 y = *reinterpret_cast<const half8_any *>(from);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] = __builtin_fmaf(wj, (float)y[e], sum[e]);
+            } else {
+                for (int e = 0; e < 8; ++e)
+                    if (e < n)
+                        sum[e] = __builtin_fmaf(wj, (float)from[e], sum[e]);
+            }
+        }
+        half_t *to = out + t * N + c;
+        half_t h[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            h[e] = (half_t)sum[e];
+        if (n == 8) {
+            *reinterpret_cast<half8_any *>(to) = half8{h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e < n)
+                    to[e] = h[e];
+        }
+    }
+}
+
+unsigned blocks_for(int64_t items) { return (unsigned)std::min<int64_t>((items + 255) / 256, 256 * 32); }
+
+} // namespace
+
+hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, float *scales, int64_t rows, int64_t K,
+                              hipStream_t s)
+{
+    constexpr int64_t most = 1 << 22;   // rows of a launch: its work items are counted in 32 bits
+    for (; rows > most; rows -= most) {
+        const hipError_t e = launch_i8_compress(X, stride, codes, scales, most, K, s);
+        if (e != hipSuccess)
+            return e;
+        X += most * stride;
+        codes += most * ((K + 15) / 16 * 16);
+        scales += most;
+    }
+    if (K <= 256)
+        hipLaunchKernelGGL((i8_compress_kernel<16, 1>), dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, X, stride, codes,
+                           scales, rows, K);
+    else if (K <= 2048)
+        hipLaunchKernelGGL((i8_compress_kernel<64, 2>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, X, stride, codes,
+                           scales, rows, K);
+    else
+        hipLaunchKernelGGL((i8_compress_kernel<256, 2>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, scales, rows,
+                           K);
+    return hipGetLastError();
+}
+
+hipError_t launch_i8_expand(const int8_t *codes, int64_t pitch, const float *scales, _Float16 *X, int64_t rows, int64_t K,
+                            hipStream_t s)
+{
+    const int64_t per_row = (K + 15) / 16, items = rows * per_row;
+    hipLaunchKernelGGL(i8_expand_kernel, dim3(blocks_for(items)), dim3(256), 0, s, codes, pitch, scales, X, items, K, per_row);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_sum(const _Float16 *Y, const float *weights, _Float16 *out, int64_t tokens, int top_k, int64_t N,
+                             hipStream_t s)
+{
+    const int64_t per_row = (N + 7) / 8, items = tokens * per_row;
+    hipLaunchKernelGGL(expert_sum_kernel, dim3(blocks_for(items)), dim3(256), 0, s, Y, weights, out, items, top_k, N, per_row);
+    return hipGetLastError();
+}
+
+} // namespace gemm_f16_impl

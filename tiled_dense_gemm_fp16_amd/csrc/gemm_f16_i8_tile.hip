@@ -1,0 +1,337 @@
+// gemm_f16_i8_tile.hip -- the product of two 8-bit matrices in LDS-staged tiles,
+// dense or over the routed pairs of each expert.
+//
+// v_mfma_i32_16x16x64_i8 takes 16 bytes of each operand a lane and as many
+// cycles as v_mfma_f32_16x16x32_f16 does, for twice the k.  Two neighbouring codes
+// lie where one binary16 number would, so a tile is staged, swizzled and read
+// as the binary16 tile of half the k is (Operand of gemm_f16_tile.h: 16-byte direct
+// loads, conflict-free 16-byte fragment reads), and the balance of loads,
+// LDS reads and matrix instructions is that tile's, at twice the rate.
+//
+// Sums are int32 and exact.  The product is computed transposed (W's fragment
+// first), so a lane holds four neighbouring columns of one row of C.
+//
+// Experts: a tile's rows of A are those of up to BM pairs of one expert, each
+// fetched from where its row is (a direct load takes an address of its own
+// for every 16 bytes anyway), and its rows of C go where their pairs are.
+#include "gemm_f16_i8_device.h"
+
+namespace gemm_f16_impl {
+
+namespace {
+
+// How a tile leaves: through LDS as 16-byte pieces of whole rows (C's rows
+// 16-byte aligned), as a split's partial sums, or straight from the registers
+// in 8- or 2-byte pieces.  Kernels of their own, as in gemm_f16_tile.h: a branch
+// over them would move the accumulator out of the matrix unit's registers.
+enum { kStaged, kPartial, kPieces };
+
+template <int BM, int BN, int WM, int WN, int STAGES, int PARTS, int OUT, bool EXPERTS>
+__global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+i8_tile_kernel(I8Args p)
+{
+    constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
+    constexpr int BK = kI8BlockK / 2;                  // as pairs of codes
+    constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 blocks of a wave
+    using Op_a = Operand<true, BM, BK, THREADS, true, 8, true>;
+    using Op_b = Operand<true, BN, BK, THREADS, true, 8, true>;
+    constexpr int A_STAGE = Op_a::STAGE, B_STAGE = Op_b::STAGE, LOADS = Op_a::LOADS + Op_b::LOADS;
+    constexpr int STAGE_HALVES = STAGES * (A_STAGE + B_STAGE), OUT_HALVES = OUT == kStaged ? BM * BN : 0;
+    constexpr int LDS_HALVES = STAGE_HALVES > OUT_HALVES ? STAGE_HALVES : OUT_HALVES;
+    static_assert(LDS_HALVES * 2 + (EXPERTS ? BM * 4 : 0) <= 163840, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) half_t lds[LDS_HALVES];
+    __shared__ int pairs[EXPERTS ? BM : 1];
+    half_t *const As = lds, *const Bs = lds + STAGES * A_STAGE;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm0 = (wave / WN) * (BM / WM), wn0 = (wave % WN) * (BN / WN);
+
+    int m0 = 0, n0, rows, split = 0;
+    const int8_t *W = p.W;
+    const float *w_scales = p.w_scales;
+    bool none = false;
+    if constexpr (EXPERTS) {
+        I8Tile t;
+        if (!i8_find_tile<BM>(p, blockIdx.x, lane, t))
+            return;
+        rows = t.rows;
+        n0 = t.tn * BN;
+        for (int i = tid; i < BM; i += THREADS)
+            pairs[i] = i8_pair(p, t, i);
+        __syncthreads();
+        none = t.expert >= p.experts;
+        W += (int64_t)t.expert * p.N * p.w_pitch;
+        w_scales += (int64_t)t.expert * p.N;
+        if (none) {   // pairs of no expert: zeros
+            const int most = min(BN, p.N - n0);
+            for (int i = wave; i < rows; i += WAVES) {
+                if (pairs[i] < 0)
+                    continue;
+                for (int n = lane; n < most; n += 64)
+                    p.C[(int64_t)pairs[i] * p.N + n0 + n] = (half_t)0;
+            }
+            return;
+        }
+    } else {
+        int tm, tn;
+        tile_coords(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, 4, tm, tn, split);
+        m0 = tm * BM;
+        n0 = tn * BN;
+        rows = min(BM, p.M - m0);
+    }
+
+    const int k_begin = split * p.k_split, k_end = min(p.K, k_begin + p.k_split);
+    const int nk = (k_end - k_begin + kI8BlockK - 1) / kI8BlockK;
+
+    Op_a opa;
+    Op_b opb;
+    opa.init(reinterpret_cast<const half_t *>(p.A), (int)(p.a_pitch / 2), m0, p.M, k_begin / 2, k_end / 2, tid, wave, lane);
+    opb.init(reinterpret_cast<const half_t *>(W), (int)(p.w_pitch / 2), n0, p.N, k_begin / 2, k_end / 2, tid, wave, lane);
+    if constexpr (EXPERTS) {
+        opa.panel = make_rsrc(p.A, (uint32_t)p.M * (uint32_t)p.a_pitch);
+#pragma unroll
+        for (int i = 0; i < Op_a::DMA; ++i) {
+            const int pair = pairs[(wave * 64 + lane) / Op_a::CHUNKS + i * Op_a::ROW_STEP];
+            const int col = Op_a::ALT_COLUMN && (i & 1) ? opa.kcol1 : opa.kcol0;
+            opa.voff[i] = pair < 0 ? 0x80000000u
+                                   : (uint32_t)(pair / p.pairs_per_row) * (uint32_t)p.a_pitch + (uint32_t)(2 * col);
+        }
+    }
+
+    int4v acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            acc[i][j] = int4v{0, 0, 0, 0};
+
+    struct Frags {
+        half8 x[TN], y[TM];
+    };
+    const auto load_frags = [&](Frags &f, const half_t *as, const half_t *bs, int ks) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            f.y[i] = opa.frag16(as, wm0 + 16 * i, ks, lane);
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            f.x[j] = opb.frag16(bs, wn0 + 16 * j, ks, lane);
+    };
+    const auto mma = [&](const Frags &f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int jj = 0; jj < TN; ++jj) {
+                const int j = (i & 1) ? TN - 1 - jj : jj;   // neighbours share an operand
+                acc[i][j] = i8_mfma(__builtin_bit_cast(int4v, f.x[j]), __builtin_bit_cast(int4v, f.y[i]), acc[i][j]);
+            }
+    };
+    // Among the matrix instructions of one half step: the fragment reads of the
+    // next one and the requests of a later slice, as in gemm_f16_tile.h.
+    constexpr int MFMAS = TM * TN, READS = TM + TN;
+    constexpr int READ_EVERY = MFMAS >= 2 * READS ? 2 : 1, READ_PER = (READS * READ_EVERY + MFMAS - 1) / MFMAS;
+    const auto interleave = [&](int loads) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < MFMAS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);          // one MFMA
+#pragma unroll
+            for (int r = 0; r < READ_PER; ++r)
+                if (i % READ_EVERY == 0 && i / READ_EVERY * READ_PER + r < READS)
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+            if (i % 2 == 0 && i / 2 < loads)
+                __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // one global load
+        }
+    };
+    static_assert(PARTS == 1 || PARTS == 2, "a slice is requested in one or both half steps");
+    const auto issue = [&](int kt, half_t *a, half_t *b, int part, int parts) __attribute__((always_inline)) {
+        opa.issue(kt, a, wave, part, parts);
+        opb.issue(kt, b, wave, part, parts);
+    };
+    // One slice, read from (rd_a, rd_b) while slice `next` is requested into
+    // (wr_a, wr_b): f1 holds the second half of the slice before (zeros at first).
+    Frags f0, f1 = {};
+    const auto step = [&](const half_t *__restrict__ rd_a, const half_t *__restrict__ rd_b, half_t *__restrict__ wr_a,
+                          half_t *__restrict__ wr_b, int next) __attribute__((always_inline)) {
+        issue(next, wr_a, wr_b, 0, PARTS);
+        load_frags(f0, rd_a, rd_b, 0);
+        mma(f1);
+        interleave(LOADS / PARTS);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (PARTS == 2)
+            issue(next, wr_a, wr_b, 1, PARTS);
+        load_frags(f1, rd_a, rd_b, 1);
+        mma(f0);
+        interleave(PARTS == 2 ? LOADS / PARTS : 0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // Slice kt has landed for every wave, and every wave is done with the stage
+    // that the next request fills.
+    const auto ready = [&](int kt) __attribute__((always_inline)) {
+        if (kt + STAGES - 2 < nk)
+            wait_vm_lgkm0<(STAGES - 2) * LOADS>();
+        else
+            wait_vm_lgkm0<0>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < nk)
+            issue(s, As + s * A_STAGE, Bs + s * B_STAGE, 0, 1);
+    for (int kt0 = 0; kt0 < nk; kt0 += STAGES) {
+#pragma unroll
+        for (int s = 0; s < STAGES; ++s) {
+            constexpr int AHEAD = STAGES - 1;
+            const int w = (s + AHEAD) % STAGES;
+            if (kt0 + s < nk) {
+                ready(kt0 + s);
+                step(As + s * A_STAGE, Bs + s * B_STAGE, As + w * A_STAGE, Bs + w * B_STAGE, kt0 + s + AHEAD);
+            }
+        }
+    }
+    mma(f1);
+    wait_vmcnt<0>();   // the last requests land before the LDS is used again, or given up
+
+    // Lane l holds, in block (i, j), columns wn0 + 16 j + 4 (l / 16) .. + 3 of row wm0 + 16 i + l % 16.
+    const int row0 = wm0 + (lane & 15), col0 = wn0 + 4 * (lane >> 4);
+    if constexpr (OUT == kPartial) {
+        int *const to = p.partial + ((int64_t)split * p.M + m0) * p.N + n0;
+        const __amdgpu_buffer_rsrc_t r = make_rsrc(to, ((uint32_t)rows * (uint32_t)p.N - (uint32_t)n0) * 4u);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const int col = col0 + 16 * j;
+                const uint32_t off = ((uint32_t)(row0 + 16 * i) * (uint32_t)p.N + (uint32_t)col) * 4u;
+                if (p.N % 4 == 0) {
+                    __builtin_amdgcn_raw_buffer_store_b128(acc[i][j], r, off | oob_unless(n0 + col < p.N), 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        __builtin_amdgcn_raw_buffer_store_b32(acc[i][j][e], r, (off + 4u * e) | oob_unless(n0 + col + e < p.N), 0, 0);
+                }
+            }
+    } else {
+        // the factors of this lane's rows and columns (past the edges: any, their products are not stored)
+        float factor[TM], column[TN][4];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            const int r = min(row0 + 16 * i, rows - 1);
+            int at = m0 + r;
+            if constexpr (EXPERTS)
+                at = max(pairs[r], 0) / p.pairs_per_row;
+            factor[i] = p.alpha * p.a_scales[at];
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                column[j][e] = w_scales[min(n0 + col0 + 16 * j + e, p.N - 1)];
+        const auto out4 = [&](int i, int j, half_t (&h)[4]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = i8_out(acc[i][j][e], factor[i], column[j][e], p.relu);
+        };
+        // where row r of the tile goes, null for none
+        const auto row_of_c = [&](int r) __attribute__((always_inline)) {
+            if constexpr (EXPERTS)
+                return pairs[r] < 0 ? (half_t *)nullptr : p.C + (int64_t)pairs[r] * p.N;
+            else
+                return r < rows ? p.C + (int64_t)(m0 + r) * p.N : (half_t *)nullptr;
+        };
+        if constexpr (OUT == kStaged) {
+            // [BM][BN] in LDS, 8-byte units XOR-ed by row as in gemm_f16_tile.h
+            constexpr int UNITS = BN / 4, UMASK = (UNITS < 32 ? UNITS : 32) - 1;
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();   // every wave is done with the stages
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    half_t h[4];
+                    out4(i, j, h);
+                    const int r = row0 + 16 * i, u = (col0 + 16 * j) / 4;
+                    *reinterpret_cast<half4 *>(lds + r * BN + 4 * (u ^ (r & UMASK))) = half4{h[0], h[1], h[2], h[3]};
+                }
+            wait_lgkm0();
+            __builtin_amdgcn_s_barrier();
+            constexpr int PIECES = BN / 8, EACH = BM * PIECES / THREADS;
+            static_assert(BM * PIECES % THREADS == 0, "pieces split evenly");
+#pragma unroll
+            for (int q = 0; q < EACH; ++q) {
+                const int id = tid + q * THREADS, r = id / PIECES, c = id % PIECES, sw = r & UMASK;
+                int4v v = *reinterpret_cast<const int4v *>(lds + r * BN + 4 * ((2 * c ^ sw) & ~1));
+                if (sw & 1)
+                    v = int4v{v[2], v[3], v[0], v[1]};
+                half_t *const to = row_of_c(r);
+                if (to && n0 + 8 * c < p.N)
+                    __builtin_nontemporal_store(v, reinterpret_cast<int4v *>(to + n0 + 8 * c));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                half_t *const to = row_of_c(row0 + 16 * i);
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int n = n0 + col0 + 16 * j;
+                    half_t h[4];
+                    out4(i, j, h);
+                    if (!to)
+                        continue;
+                    if (p.vec_c == 4) {
+                        if (n < p.N)
+                            __builtin_nontemporal_store(half4{h[0], h[1], h[2], h[3]}, reinterpret_cast<half4 *>(to + n));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (n + e < p.N)
+                                to[n + e] = h[e];
+                    }
+                }
+            }
+        }
+    }
+}
+
+} // namespace
+
+template <int BM, int BN, int WM, int WN, int STAGES, int PARTS>
+static hipError_t launch_tile(const I8Args &a, int64_t grid, bool experts, hipStream_t s)
+{
+#define GEMM_F16_I8(OUT, EXPERTS)                                                                                        \
+    hipLaunchKernelGGL((i8_tile_kernel<BM, BN, WM, WN, STAGES, PARTS, OUT, EXPERTS>), dim3((unsigned)grid),             \
+                       dim3(64 * WM * WN), 0, s, a)
+    if (experts && a.vec_c == 8)
+        GEMM_F16_I8(kStaged, true);
+    else if (experts)
+        GEMM_F16_I8(kPieces, true);
+    else if (a.partial)
+        GEMM_F16_I8(kPartial, false);
+    else if (a.vec_c == 8)
+        GEMM_F16_I8(kStaged, false);
+    else
+        GEMM_F16_I8(kPieces, false);
+#undef GEMM_F16_I8
+    return hipGetLastError();
+}
+
+hipError_t launch_i8_stream(int n_blocks, const I8Args &a, int64_t grid, bool experts, hipStream_t s);
+
+static hipError_t launch_config(int config, const I8Args &a, int64_t grid, bool experts, hipStream_t s)
+{
+    switch (config) {
+    case 0: return launch_i8_stream(1, a, grid, experts, s);
+    case 1: return launch_i8_stream(4, a, grid, experts, s);
+    case 2: return launch_tile<128, 128, 2, 2, 4, 1>(a, grid, experts, s);
+    case 3: return launch_tile<256, 256, 2, 2, 2, 2>(a, grid, experts, s);
+    default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_i8(int config, const I8Args &a, int64_t grid, hipStream_t s) { return launch_config(config, a, grid, false, s); }
+hipError_t launch_i8_experts(int config, const I8Args &a, int64_t grid, hipStream_t s)
+{
+    return launch_config(config, a, grid, true, s);
+}
+
+} // namespace gemm_f16_impl

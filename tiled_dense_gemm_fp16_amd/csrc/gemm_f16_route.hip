@@ -1,0 +1,306 @@
+// gemm_f16_route.hip -- choice of experts from a token's logits, and the order
+// of the chosen pairs by expert.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gemm_f16_i8_internal.h"
+
+namespace gemm_f16_impl {
+
+namespace {
+
+typedef unsigned long long u64;
+
+// What DPP control CTRL brings from another lane; lanes that it leaves out keep `old`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned dpp(unsigned old, unsigned x)
+{
+    return (unsigned)__builtin_amdgcn_update_dpp((int)old, (int)x, CTRL, ROWS, 0xf, false);
+}
+// Largest of a wave's 64 values: four steps inside the rows of 16 lanes, two across them.
+__device__ __forceinline__ unsigned wave_max(unsigned x)
+{
+    x = max(x, dpp<0x111, 0xf>(0u, x));   // row_shr:1
+    x = max(x, dpp<0x112, 0xf>(0u, x));   // row_shr:2
+    x = max(x, dpp<0x114, 0xf>(0u, x));   // row_shr:4
+    x = max(x, dpp<0x118, 0xf>(0u, x));   // row_shr:8
+    x = max(x, dpp<0x142, 0xa>(0u, x));   // row_bcast:15
+    x = max(x, dpp<0x143, 0xc>(0u, x));   // row_bcast:31
+    return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ double wave_sum(double x)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        x += __shfl_xor(x, d);
+    return x;
+}
+__device__ __forceinline__ double lane_value(double x, int lane)
+{
+    const u64 b = __builtin_bit_cast(u64, x);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)b, lane);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(b >> 32), lane);
+    return __builtin_bit_cast(double, (u64)hi << 32 | lo);
+}
+
+// Numbers as integers of the same order, all above 0, which stands for
+// "closed" (+0 and -0 become one).
+__device__ __forceinline__ u64 ordered(double x)
+{
+    const u64 b = __builtin_bit_cast(u64, x + 0.0);
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ u64 ordered(float x)
+{
+    const unsigned b = __builtin_bit_cast(unsigned, x + 0.0f);
+    return (u64)(b >> 31 ? ~b : b | 1u << 31) << 32;
+}
+
+// The lane with the largest key, the lowest of equals; -1 where all are closed.
+// High halves decide but for ties, which a second search resolves.
+__device__ __forceinline__ int first_best(u64 key)
+{
+    const unsigned hi = (unsigned)(key >> 32), most = wave_max(hi);
+    u64 at = __ballot(hi == most);
+    if ((at & (at - 1)) != 0) {
+        if (most == 0)   // (no number's high half)
+            return -1;
+        const unsigned lo = hi == most ? (unsigned)key : 0u, low = wave_max(lo);
+        at = __ballot(hi == most && lo == low);
+    }
+    return __ffsll(at) - 1;
+}
+
+constexpr int kTokens = 4;   // waves of a workgroup, each with a token
+
+// A wave takes a token; lane l holds the experts EACH l .. EACH l + EACH - 1, so
+// that among equal keys the lowest lane has the lowest index.
+// Keys are compared as integers, in 64 bits where scores enter them, so the
+// choice is the definition's; without bias they are the logits themselves.
+// A choice is a search over the wave in the vector unit's own lane moves
+// (6 instructions where no two keys share their high half).
+template <int EACH>
+__global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
+{
+    extern __shared__ double shared_keys[];   // groups: [kTokens][experts]
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t token = (int64_t)blockIdx.x * kTokens + wave;
+    const int64_t from = (token < p.tokens ? token : p.tokens - 1) * p.stride;
+
+    float x[EACH];
+    double score[EACH];
+    u64 key[EACH];
+    float high = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = lane * EACH + i;
+        x[i] = -INFINITY;
+        if (e < p.experts) {
+            const float v = p.half ? (float)((const _Float16 *)p.logits)[from + e] : ((const float *)p.logits)[from + e];
+            const float b = p.bias ? p.bias[e] : 0.0f;
+            if (v > -INFINITY && b > -INFINITY)   // (neither is NaN)
+                x[i] = __builtin_fminf(v, 3.402823466e38f);
+        }
+        high = __builtin_fmaxf(high, x[i]);
+    }
+    double total = 1.0;
+    if (!p.sigmoid) {
+        const unsigned top = wave_max((unsigned)(ordered(high) >> 32));
+        high = __builtin_bit_cast(float, top >> 31 ? top ^ 1u << 31 : ~top);
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            score[i] = x[i] > -INFINITY ? exp((double)x[i] - (double)high) : 0.0;
+            sum += score[i];
+        }
+        total = wave_sum(sum);
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            score[i] = total > 0.0 ? score[i] / total : 0.0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            score[i] = x[i] > -INFINITY ? 1.0 / (1.0 + exp(-(double)x[i])) : 0.0;
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        const int e = lane * EACH + i;
+        key[i] = 0;
+        if (x[i] > -INFINITY)
+            key[i] = p.bias ? ordered(score[i] + (double)p.bias[e]) : ordered(x[i]);
+    }
+
+    if (p.groups > 1) {
+        // two best keys of each group: a team of lanes for each, by way of LDS
+        double *const mine = shared_keys + wave * p.experts;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int e = lane * EACH + i;
+            if (e < p.experts)
+                mine[e] = x[i] > -INFINITY ? score[i] + (p.bias ? (double)p.bias[e] : 0.0) : -INFINITY;
+        }
+        __syncthreads();
+        int team = 64;
+        while (team * p.groups > 64)
+            team /= 2;
+        const int size = p.experts / p.groups, g = lane / team;
+        double a = -INFINITY, b = -INFINITY;   // the best and the next
+        if (g < p.groups)
+            for (int i = lane % team; i < size; i += team) {
+                const double v = mine[g * size + i];
+                b = v > a ? a : (v > b ? v : b);
+                a = v > a ? v : a;
+            }
+        for (int d = 1; d < team; d *= 2) {
+            const double oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+            b = oa > a ? (a > ob ? a : ob) : (b > oa ? b : oa);
+            a = oa > a ? oa : a;
+        }
+        u64 best = 0;
+        if (lane % team == 0 && g < p.groups && a > -INFINITY)
+            best = ordered(b > -INFINITY ? a + b : a);
+        u64 stay = 0;
+        for (int j = 0; j < p.top_groups; ++j) {
+            const int at = first_best(best);
+            if (at < 0)
+                break;
+            stay |= 1ull << (at / team);
+            if (lane == at)
+                best = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            const int e = lane * EACH + i;
+            if (e < p.experts && !(stay >> (e / size) & 1))
+                key[i] = 0;
+        }
+    }
+
+    int my_id = -1;
+    double my_score = 0.0, sum = 0.0;
+    for (int j = 0; j < p.top_k; ++j) {
+        u64 best = key[0];
+        int which = 0;
+        double its = score[0];
+#pragma unroll
+        for (int i = 1; i < EACH; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                which = i;
+                its = score[i];
+            }
+        const int at = first_best(best);
+        if (at < 0)
+            break;
+        const int e = at * EACH + __builtin_amdgcn_readlane(which, at);
+        const double s = lane_value(its, at);
+        sum += s;
+        if (lane == j) {
+            my_id = e;
+            my_score = s;
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            if (lane == at && which == i)
+                key[i] = 0;
+    }
+    if (lane < p.top_k && token < p.tokens) {
+        if (p.renormalise)
+            my_score = sum > 0.0 ? my_score / sum : 0.0;
+        p.ids[token * p.top_k + lane] = my_id;
+        p.weights[token * p.top_k + lane] = my_id < 0 ? 0.0f : (float)((double)p.scale * my_score);
+    }
+}
+
+// ---- the pairs by expert -----------------------------------------------------------
+// A workgroup for each expert, and one for the pairs of none, finds the place
+// of its first pair by counting the smaller ids itself, then writes its pairs:
+// nothing passes between workgroups, and the order is that of the pairs.
+constexpr int kOrderWaves = 16;
+
+__global__ void __launch_bounds__(64 * kOrderWaves) expert_order_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ order,
+                                                                        int32_t *__restrict__ starts, int pairs, int experts)
+{
+    __shared__ int below[kOrderWaves], equal[kOrderWaves];
+    const int expert = blockIdx.x, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    constexpr int kRound = 4 * 64;   // ids of a wave in flight
+    const int share = (pairs + kRound * kOrderWaves - 1) / (kRound * kOrderWaves) * kRound;
+    const int begin = min(wave * share, pairs), end = min(begin + share, pairs);
+    // the bins of ids i + 64 r + lane, past `end` one of no expert
+    const auto load = [&](int i, int (&bin)[4]) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int at = i + 64 * r + lane;
+            const int id = at < end ? ids[at] : 0;
+            bin[r] = at >= end ? experts + 1 : id >= 0 && id < experts ? id : experts;
+        }
+    };
+    int less = 0, same = 0;
+    for (int i = begin; i < end; i += kRound) {
+        int bin[4];
+        load(i, bin);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            less += __popcll(__ballot(bin[r] < expert));
+            same += __popcll(__ballot(bin[r] == expert));
+        }
+    }
+    if (lane == 0) {
+        below[wave] = less;
+        equal[wave] = same;
+    }
+    __syncthreads();
+    int place = 0;
+    for (int w = 0; w < kOrderWaves; ++w)
+        place += below[w];
+    if (threadIdx.x == 0)
+        starts[expert] = place;
+    for (int w = 0; w < wave; ++w)
+        place += equal[w];
+    if (same == 0)
+        return;
+    for (int i = begin; i < end; i += kRound) {
+        int bin[4];
+        load(i, bin);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const u64 here = __ballot(bin[r] == expert);
+            if (bin[r] == expert)
+                order[place + __popcll(here & ((1ull << lane) - 1))] = i + 64 * r + lane;
+            place += __popcll(here);
+        }
+    }
+}
+
+} // namespace
+
+hipError_t launch_route(const RouteArgs &a, hipStream_t s)
+{
+    const dim3 grid((unsigned)((a.tokens + kTokens - 1) / kTokens));
+    const unsigned lds = a.groups > 1 ? (unsigned)(kTokens * a.experts * sizeof(double)) : 0;
+#define GEMM_F16_ROUTE(EACH) hipLaunchKernelGGL(route_kernel<EACH>, grid, dim3(64 * kTokens), lds, s, a)
+    if (a.experts <= 64)
+        GEMM_F16_ROUTE(1);
+    else if (a.experts <= 128)
+        GEMM_F16_ROUTE(2);
+    else if (a.experts <= 256)
+        GEMM_F16_ROUTE(4);
+    else if (a.experts <= 512)
+        GEMM_F16_ROUTE(8);
+    else
+        GEMM_F16_ROUTE(16);
+#undef GEMM_F16_ROUTE
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_order(const int32_t *ids, int32_t *order, int32_t *starts, int pairs, int experts, hipStream_t s)
+{
+    hipLaunchKernelGGL(expert_order_kernel, dim3((unsigned)(experts + 1)), dim3(64 * kOrderWaves), 0, s, ids, order, starts,
+                       pairs, experts);
+    return hipGetLastError();
+}
+
+} // namespace gemm_f16_impl
