@@ -31,34 +31,45 @@ struct I8Tile {
     int tm, tn;
 };
 
-__device__ __forceinline__ int i8_start(const I8Args &p, int e) { return min(max(p.starts[e], 0), p.pairs); }
+// Inclusive sums over the wave, in the vector unit's own lane moves.
+__device__ __forceinline__ int wave_prefix(int x)
+{
+#define GEMM_F16_STEP(CTRL, ROWS) x += __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false)
+    GEMM_F16_STEP(0x111, 0xf);   // row_shr:1, 2, 4, 8
+    GEMM_F16_STEP(0x112, 0xf);
+    GEMM_F16_STEP(0x114, 0xf);
+    GEMM_F16_STEP(0x118, 0xf);
+    GEMM_F16_STEP(0x142, 0xa);   // row_bcast:15, :31
+    GEMM_F16_STEP(0x143, 0xc);
+#undef GEMM_F16_STEP
+    return x;
+}
 
 // Find tile `wg` of the grid.  Expert e's pairs make ceil(count / BM) tiles of
-// rows; each lane adds up those of neighbouring experts, a scan over the wave
-// gives every lane its first one, and the lane whose range holds the tile looks
-// for the expert.  (An order whose starts decrease gives tiles that are empty or
-// not reached, never places outside of [0, pairs).)  Workgroups past the last
-// tile return false.  The remap over XCDs is that of tile_coords, on the tiles
-// that there are, so that each XCD has an equal share of them.
-template <int BM>
-__device__ __forceinline__ bool i8_find_tile(const I8Args &p, int wg, int lane, I8Tile &t)
+// rows; each lane adds up those of EACH neighbouring experts, a scan over the
+// wave gives every lane its first one, and the lane whose range holds the tile
+// looks for the expert.  (An order whose starts decrease gives tiles that are
+// empty or not reached, never places outside of [0, pairs).)  Workgroups past the
+// last tile return false.  The remap over XCDs is that of tile_coords, on the
+// tiles that there are, so that each XCD has an equal share of them.
+template <int BM, int EACH>
+__device__ __forceinline__ bool i8_search(const I8Args &p, int wg, int lane, I8Tile &t)
 {
-    const int bins = p.experts + 1, per = (bins + 63) / 64;
-    const auto tiles_of = [&](int e, int &begin, int &end) {
-        begin = i8_start(p, e);
-        end = e < p.experts ? i8_start(p, e + 1) : p.pairs;
-        return max(0, end - begin + BM - 1) / BM;
-    };
-    int begin, end, mine = 0;
-    for (int i = 0; i < per; ++i)
-        if (lane * per + i < bins)
-            mine += tiles_of(lane * per + i, begin, end);
-    int upto = mine;
+    int start[EACH + 1], n[EACH], mine = 0;   // experts EACH lane, ...: their starts and numbers of tiles
+    // (buffer loads and no choice between values: all are in flight together)
+    const __amdgpu_buffer_rsrc_t starts = make_rsrc(p.starts, (uint32_t)(p.experts + 1) * 4u);
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int other = __shfl_up(upto, d);
-        upto += lane >= d ? other : 0;
+    for (int i = 0; i <= EACH; ++i)
+        start[i] = __builtin_amdgcn_raw_buffer_load_b32(starts, (uint32_t)(lane * EACH + i) * 4u, 0, 0);
+#pragma unroll
+    for (int i = 0; i <= EACH; ++i)
+        start[i] = max(min(max(start[i], 0), p.pairs), lane * EACH + i > p.experts ? p.pairs : 0);
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        n[i] = (max(0, start[i + 1] - start[i]) + BM - 1) / BM;
+        mine += n[i];
     }
+    const int upto = wave_prefix(mine);
     const int tiles_m = min(__builtin_amdgcn_readlane(upto, 63), p.tiles_m), total = tiles_m * p.tiles_n;
     // (an XCD's share, and this workgroup's place in it)
     const int share = total / 8 + (wg % 8 < total % 8 ? 1 : 0);
@@ -72,31 +83,35 @@ __device__ __forceinline__ bool i8_find_tile(const I8Args &p, int wg, int lane, 
     t.tn = in_group / high;
     const int owner = __ffsll((unsigned long long)__ballot(upto > t.tm)) - 1;   // the first whose range ends behind the tile
     int expert = 0, first = 0, rows = 0, at = upto - mine;
-    if (lane == owner)
-        for (int i = 0; i < per && lane * per + i < bins; ++i) {
-            const int n = tiles_of(lane * per + i, begin, end);
-            if (t.tm < at + n) {
-                expert = lane * per + i;
-                first = begin + (t.tm - at) * BM;
-                rows = min(BM, end - first);
-                break;
-            }
-            at += n;
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+        if (t.tm >= at && t.tm < at + n[i]) {
+            expert = lane * EACH + i;
+            first = start[i] + (t.tm - at) * BM;
+            rows = min(BM, start[i + 1] - first);
         }
+        at += n[i];
+    }
     t.expert = __builtin_amdgcn_readlane(expert, owner);
     t.first = __builtin_amdgcn_readlane(first, owner);
     t.rows = __builtin_amdgcn_readlane(rows, owner);
     return true;
 }
 
+// (65 places for 64 lanes: the pairs of none come behind the last expert)
+template <int BM>
+__device__ __forceinline__ bool i8_find_tile(const I8Args &p, int wg, int lane, I8Tile &t)
+{
+    return p.experts < 128 ? i8_search<BM, 2>(p, wg, lane, t) : p.experts < 320 ? i8_search<BM, 5>(p, wg, lane, t)
+                                                                                : i8_search<BM, 17>(p, wg, lane, t);
+}
+
 // The pair at place `i` of a tile's rows, -1 past them or where order does not
 // name one.
 __device__ __forceinline__ int i8_pair(const I8Args &p, const I8Tile &t, int i)
 {
-    if (i >= t.rows)
-        return -1;
-    const int pair = p.order[t.first + i];
-    return pair >= 0 && pair < p.pairs ? pair : -1;
+    const int pair = p.order[min(t.first + i, p.pairs - 1)];
+    return i < t.rows && pair >= 0 && pair < p.pairs ? pair : -1;
 }
 
 } // namespace gemm_f16_impl

@@ -38,16 +38,22 @@ i8_tile_kernel(I8Args p)
     constexpr int A_STAGE = Op_a::STAGE, B_STAGE = Op_b::STAGE, LOADS = Op_a::LOADS + Op_b::LOADS;
     constexpr int STAGE_HALVES = STAGES * (A_STAGE + B_STAGE), OUT_HALVES = OUT == kStaged ? BM * BN : 0;
     constexpr int LDS_HALVES = STAGE_HALVES > OUT_HALVES ? STAGE_HALVES : OUT_HALVES;
-    static_assert(LDS_HALVES * 2 + (EXPERTS ? BM * 4 : 0) <= 163840, "LDS budget");
-    __shared__ __attribute__((aligned(1024))) half_t lds[LDS_HALVES];
-    __shared__ int pairs[EXPERTS ? BM : 1];
+    constexpr int TABLE = (EXPERTS ? 2 * BM : BM) + BN;   // words behind the stages
+    static_assert(LDS_HALVES * 2 + TABLE * 4 <= 163840, "LDS budget");
+    // (One array: with several, the compiler no longer sees that the loads into
+    // one stage leave the others alone, and waits for them before every read:
+    // 8192^3 425 us, 628 so.)
+    __shared__ __attribute__((aligned(1024))) half_t lds[LDS_HALVES + 2 * TABLE];
+    float *const column_scale = reinterpret_cast<float *>(lds + LDS_HALVES), *const row_factor = column_scale + BN;
+    int *const pairs = reinterpret_cast<int *>(row_factor + BM);   // experts
     half_t *const As = lds, *const Bs = lds + STAGES * A_STAGE;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm0 = (wave / WN) * (BM / WM), wn0 = (wave % WN) * (BN / WN);
 
-    int m0 = 0, n0, rows, split = 0;
+    constexpr int MINE = (BM + THREADS - 1) / THREADS;   // rows tid, tid + THREADS, ... of the tile
+    int m0 = 0, n0, rows, split = 0, my_pair[MINE], my_row[MINE];
     const int8_t *W = p.W;
     const float *w_scales = p.w_scales;
     bool none = false;
@@ -57,13 +63,18 @@ i8_tile_kernel(I8Args p)
             return;
         rows = t.rows;
         n0 = t.tn * BN;
-        for (int i = tid; i < BM; i += THREADS)
-            pairs[i] = i8_pair(p, t, i);
-        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+            my_pair[i] = i8_pair(p, t, tid + i * THREADS);
         none = t.expert >= p.experts;
         W += (int64_t)t.expert * p.N * p.w_pitch;
         w_scales += (int64_t)t.expert * p.N;
         if (none) {   // pairs of no expert: zeros
+#pragma unroll
+            for (int i = 0; i < MINE; ++i)
+                if (tid + i * THREADS < BM)
+                    pairs[tid + i * THREADS] = my_pair[i];
+            __syncthreads();
             const int most = min(BN, p.N - n0);
             for (int i = wave; i < rows; i += WAVES) {
                 if (pairs[i] < 0)
@@ -88,17 +99,6 @@ i8_tile_kernel(I8Args p)
     Op_b opb;
     opa.init(reinterpret_cast<const half_t *>(p.A), (int)(p.a_pitch / 2), m0, p.M, k_begin / 2, k_end / 2, tid, wave, lane);
     opb.init(reinterpret_cast<const half_t *>(W), (int)(p.w_pitch / 2), n0, p.N, k_begin / 2, k_end / 2, tid, wave, lane);
-    if constexpr (EXPERTS) {
-        opa.panel = make_rsrc(p.A, (uint32_t)p.M * (uint32_t)p.a_pitch);
-#pragma unroll
-        for (int i = 0; i < Op_a::DMA; ++i) {
-            const int pair = pairs[(wave * 64 + lane) / Op_a::CHUNKS + i * Op_a::ROW_STEP];
-            const int col = Op_a::ALT_COLUMN && (i & 1) ? opa.kcol1 : opa.kcol0;
-            opa.voff[i] = pair < 0 ? 0x80000000u
-                                   : (uint32_t)(pair / p.pairs_per_row) * (uint32_t)p.a_pitch + (uint32_t)(2 * col);
-        }
-    }
-
     int4v acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -148,13 +148,14 @@ i8_tile_kernel(I8Args p)
         opb.issue(kt, b, wave, part, parts);
     };
     // One slice, read from (rd_a, rd_b) while slice `next` is requested into
-    // (wr_a, wr_b): f1 holds the second half of the slice before (zeros at first).
+    // (wr_a, wr_b): f1 holds the second half of the slice before, if there is one.
     Frags f0, f1 = {};
-    const auto step = [&](const half_t *__restrict__ rd_a, const half_t *__restrict__ rd_b, half_t *__restrict__ wr_a,
+    const auto step = [&](auto first, const half_t *__restrict__ rd_a, const half_t *__restrict__ rd_b, half_t *__restrict__ wr_a,
                           half_t *__restrict__ wr_b, int next) __attribute__((always_inline)) {
         issue(next, wr_a, wr_b, 0, PARTS);
         load_frags(f0, rd_a, rd_b, 0);
-        mma(f1);
+        if constexpr (!decltype(first)::value)
+            mma(f1);
         interleave(LOADS / PARTS);
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (PARTS == 2)
@@ -174,20 +175,71 @@ i8_tile_kernel(I8Args p)
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
+    // The first requests: W's, which need no pairs, before A's.
+    if (nk > 0)
+        opb.issue(0, Bs, wave);
+    if constexpr (EXPERTS) {
+        // where the tile's rows come from and go: places in A and C by way of LDS
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < nk)
-            issue(s, As + s * A_STAGE, Bs + s * B_STAGE, 0, 1);
-    for (int kt0 = 0; kt0 < nk; kt0 += STAGES) {
-#pragma unroll
-        for (int s = 0; s < STAGES; ++s) {
-            constexpr int AHEAD = STAGES - 1;
-            const int w = (s + AHEAD) % STAGES;
-            if (kt0 + s < nk) {
-                ready(kt0 + s);
-                step(As + s * A_STAGE, Bs + s * B_STAGE, As + w * A_STAGE, Bs + w * B_STAGE, kt0 + s + AHEAD);
+        for (int i = 0; i < MINE; ++i) {
+            const int at = tid + i * THREADS;
+            my_row[i] = (int)((uint32_t)max(my_pair[i], 0) / (uint32_t)p.pairs_per_row);
+            if (at < BM) {
+                pairs[at] = my_pair[i];
+                // (row_factor's place is free until then)
+                reinterpret_cast<int *>(row_factor)[at] = my_pair[i] < 0 ? -1 : my_row[i];
             }
         }
+        wait_lgkm0();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        opa.panel = make_rsrc(p.A, (uint32_t)p.M * (uint32_t)p.a_pitch);
+#pragma unroll
+        for (int i = 0; i < Op_a::DMA; ++i) {
+            const int row = reinterpret_cast<const int *>(row_factor)[(wave * 64 + lane) / Op_a::CHUNKS + i * Op_a::ROW_STEP];
+            const int col = Op_a::ALT_COLUMN && (i & 1) ? opa.kcol1 : opa.kcol0;
+            opa.voff[i] = row < 0 ? 0x80000000u : (uint32_t)row * (uint32_t)p.a_pitch + (uint32_t)(2 * col);
+        }
+        wait_lgkm0();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+    } else {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+            my_row[i] = m0 + min(tid + i * THREADS, rows - 1);
+    }
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s)
+        if (s < nk) {
+            opa.issue(s, As + s * A_STAGE, wave);
+            if (s > 0)
+                opb.issue(s, Bs + s * B_STAGE, wave);
+        }
+    // the factors of the tile's rows and columns, for the end (past the edges:
+    // any, their products are not stored)
+    if constexpr (OUT != kPartial) {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+            if (tid + i * THREADS < BM)
+                row_factor[tid + i * THREADS] = p.alpha * p.a_scales[my_row[i]];
+        for (int i = tid; i < BN; i += THREADS)
+            column_scale[i] = w_scales[min(n0 + i, p.N - 1)];
+        asm volatile("" ::: "memory");   // written before the slices' barriers
+    }
+    constexpr int AHEAD = STAGES - 1;
+    const auto stage = [&](auto first, int s, int kt) __attribute__((always_inline)) {
+        const int w = (s + AHEAD) % STAGES;
+        ready(kt);
+        step(first, As + s * A_STAGE, Bs + s * B_STAGE, As + w * A_STAGE, Bs + w * B_STAGE, kt + AHEAD);
+    };
+    if (nk > 0)
+        stage(std::integral_constant<bool, true>{}, 0, 0);
+    // slices 1 ... in groups of STAGES, unrolled so that every stage is a constant
+    for (int kt0 = 1; kt0 < nk; kt0 += STAGES) {
+#pragma unroll
+        for (int u = 0; u < STAGES; ++u)
+            if (kt0 + u < nk)
+                stage(std::integral_constant<bool, false>{}, (1 + u) % STAGES, kt0 + u);
     }
     mma(f1);
     wait_vmcnt<0>();   // the last requests land before the LDS is used again, or given up
@@ -212,21 +264,16 @@ i8_tile_kernel(I8Args p)
                 }
             }
     } else {
-        // the factors of this lane's rows and columns (past the edges: any, their products are not stored)
-        float factor[TM], column[TN][4];
+        if (nk == 0)
+            __syncthreads();   // (the slices' barriers have ordered them otherwise)
+        float factor[TM];
+        float4v column[TN];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int r = min(row0 + 16 * i, rows - 1);
-            int at = m0 + r;
-            if constexpr (EXPERTS)
-                at = max(pairs[r], 0) / p.pairs_per_row;
-            factor[i] = p.alpha * p.a_scales[at];
-        }
+        for (int i = 0; i < TM; ++i)
+            factor[i] = row_factor[row0 + 16 * i];
 #pragma unroll
         for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                column[j][e] = w_scales[min(n0 + col0 + 16 * j + e, p.N - 1)];
+            column[j] = *reinterpret_cast<const float4v *>(column_scale + col0 + 16 * j);
         const auto out4 = [&](int i, int j, half_t (&h)[4]) __attribute__((always_inline)) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
