@@ -35,12 +35,13 @@ extern "C" {
  * GEMM_F16_ERROR_UNSUPPORTED_SIZE). */
 #define GEMM_F16_I8_MAX_K (((int64_t)1 << 17) - 1)
 
-/* K rounded up to a multiple of 16; -1 for a K out of range. */
+/* The pitch of the rows that gemm_f16_i8_compress writes: K rounded up to a
+ * multiple of 16, from 65 on of 128 (whole cache lines); -1 for a K out of range. */
 int64_t gemm_f16_i8_pitch(int64_t K);
 
 /*
  * Round rows of X (binary16, x_stride >= K elements apart, 2-byte aligned) to
- * codes (pitch gemm_f16_i8_pitch(K), padding included) and scales.  With
+ * codes (pitch gemm_f16_i8_pitch(K), with zeros from K to the pitch) and scales.  With
  * m = max |x| of the row, NaN counting as 0 and infinities as 65504:
  *   scale = m / 127, rounded to fp32
  *   code  = 127 x / m, rounded to the nearest integer, halves to the even one

@@ -4,13 +4,17 @@ import numpy as np
 import torch
 
 
+def pitch(k):
+    return -(-k // 16) * 16 if k <= 64 else -(-k // 128) * 128
+
+
 def compress(x):
-    """(codes, scales) of the rows of a float16 array, codes padded to a multiple of 16 columns.  127 x and m are exact
+    """(codes, scales) of the rows of a float16 array, codes padded to pitch(k) columns.  127 x and m are exact
     in 64 bits, and a quotient of theirs that is no half keeps 2^-20 from one: the rounding is the definition's."""
     x = np.nan_to_num(np.asarray(x).astype(np.float64), nan=0.0, posinf=65504.0, neginf=-65504.0)
     m = np.abs(x).max(-1, initial=0.0)
     q = np.rint(127.0 * x / np.where(m > 0, m, 1.0)[..., None])
-    pad = [(0, 0)] * (x.ndim - 1) + [(0, -x.shape[-1] % 16)]
+    pad = [(0, 0)] * (x.ndim - 1) + [(0, pitch(x.shape[-1]) - x.shape[-1])]
     # (64 bits then 32: a double rounding is innocuous, 53 >= 2 * 24 + 2)
     return np.pad(q, pad).astype(np.int8), (m / 127.0).astype(np.float32)
 

@@ -67,7 +67,7 @@ def test_rows_apart_and_unaligned(shift, stride):
     same(x[3:4].cpu(), g.i8_compress(x[3:4]))
     cube = base[shift:shift + 24 * stride].view(4, 6, stride)[:, :, 1:100]
     packed = g.i8_compress(cube)
-    assert packed.codes.shape == (4, 6, 112)
+    assert packed.codes.shape == (4, 6, 128)
     same(cube.cpu(), packed)
     out = torch.full((24 * 130 + 9,), 7.0, dtype=torch.float16, device=DEV)
     g.i8_expand(g.i8_compress(x), out=out[1:-8].view(24, 130))
@@ -76,9 +76,9 @@ def test_rows_apart_and_unaligned(shift, stride):
 
 
 def test_nothing_beside_the_codes_is_written():
-    for r, k in [(3, 17), (5, 300), (2, 4100)]:
+    for r, k in [(3, 17), (4, 65), (5, 300), (2, 4100)]:
         x = rows(r, k, 1).to(DEV)
-        pitch = -(-k // 16) * 16
+        pitch = ref.pitch(k)
         room = torch.full((r * pitch + 64,), 77, dtype=torch.int8, device=DEV)
         scales = torch.full((r + 2,), 7.0, device=DEV)
         st = g.lib().gemm_f16_i8_compress(r, k, x.data_ptr(), k, room[32:].data_ptr(), scales[1:].data_ptr(),

@@ -42,7 +42,8 @@ def test_every_declared_symbol_is_exported():
 
 def test_pitch():
     h = g.lib()
-    assert [h.gemm_f16_i8_pitch(k) for k in (0, 1, 16, 17, 4100, 131071)] == [0, 16, 16, 32, 4112, 131072]
+    for k in (0, 1, 16, 17, 64, 65, 128, 129, 4100, 131071):
+        assert h.gemm_f16_i8_pitch(k) == ref.pitch(k)
     assert h.gemm_f16_i8_pitch(-1) == -1 and h.gemm_f16_i8_pitch(1 << 17) == -1
 
 
@@ -57,7 +58,7 @@ def test_rows_refusals():
 
     for fn in (compress, expand):
         for bad in (dict(rows=-1), dict(k=-1), dict(x=None), dict(codes=None), dict(scales=None), dict(x=at(1)), dict(x=at(2)),
-                    dict(x=at(1) + 4 * 112 - 2)):
+                    dict(x=at(1) + 4 * 112 - 2), dict(rows=1, x=at(1) + 110)):
             assert fn(**bad) == INVALID, bad
         for bad in (dict(x=at(0) + 1), dict(codes=at(1) + 8), dict(scales=at(2) + 2)):
             assert fn(**bad) == MISALIGNED, bad

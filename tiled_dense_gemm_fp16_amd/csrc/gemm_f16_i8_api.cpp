@@ -13,10 +13,16 @@
 namespace gemm_f16_impl {
 
 const I8Config kI8Configs[kNumI8Configs] = {
-    {"i8_16x16", 16, 16, 8, 0},
-    {"i8_16x64", 16, 64, 8, 0},
-    {"i8_128x128_s4", 128, 128, 4, 4},
-    {"i8_256x256_s2", 256, 256, 4, 2},
+    {"i8_16x16", 16, 16, 8, 0, 4, 1.29f, 2.8f, 1.3f, 5.5f},
+    {"i8_32x32_s8", 32, 32, 4, 8, 2, 0.093f, 3.8f, 0.28f, 4.7f},
+    {"i8_32x64_s6", 32, 64, 4, 6, 2, 0.148f, 4.1f, 0.17f, 4.3f},
+    {"i8_64x64_s6", 64, 64, 4, 6, 1, 0.233f, 3.6f, 0.27f, 3.5f},
+    {"i8_64x128_s4", 64, 128, 4, 4, 1, 0.348f, 3.9f, 0.32f, 3.9f},
+    {"i8_64x256_s3", 64, 256, 4, 3, 1, 0.60f, 4.9f, 0.62f, 3.9f},
+    {"i8_128x128_s4", 128, 128, 4, 4, 1, 0.494f, 4.9f, 0.46f, 5.0f},
+    {"i8_128x256_s3", 128, 256, 4, 3, 1, 0.69f, 7.3f, 0.72f, 6.3f},
+    {"i8_256x128_s3", 256, 128, 4, 3, 1, 0.652f, 7.3f, 0.74f, 6.2f},
+    {"i8_256x256_s2", 256, 256, 4, 2, 1, 1.258f, 10.0f, 1.0f, 9.5f},
 };
 
 namespace {
@@ -31,6 +37,10 @@ bool launchable(int64_t workgroups, int64_t threads) { return workgroups <= 0xff
 gemm_f16_status_t status_of(hipError_t e) { return e == hipSuccess ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_LAUNCH_FAILED; }
 
 int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
+
+// Rows that compress writes start on cache lines, but the shortest: 1000 x 5000 x
+// 4100 with rows of 4112 bytes 39.7 us, of 4224 31.7; 8192 x 8192 x 4100 292, 247.
+int64_t made_pitch(int64_t K) { return K <= 64 ? padded(K) : (K + 127) / 128 * 128; }
 
 // a * b without overflow, beyond kMostBytes where it is more (a, b not negative)
 int64_t bytes_of(int64_t a, int64_t b) { return b > 0 && a > kMostBytes / b ? kMostBytes + 1 : a * b; }
@@ -74,6 +84,70 @@ void describe(int c, gemm_f16_plan_t *p)
                                 : d.waves * d.block_n * 64;
 }
 
+// A product's time in us, for the choice of a configuration and split: rounds of
+// workgroups over 256 CUs, or the time to bring W from memory and the tiles'
+// operands from the L2s if that is longer, and a split's partial sums and second
+// launch.  The configurations' constants and the rates below were fitted to what
+// 731 shapes (M 1 to 4096, N 256 to 28672, K 512 to 16384) took in every
+// configuration and split, so that the choice comes out right: it took 2 %
+// longer than the best one on average, 37 % at most (16 x 5000 x 4096: 10.8, 7.9).
+// us of some choices and others: (1, 28672 x 8192) 16x16 44, 32x64 52; (64, 8192 x
+// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 256x128 31, 128x128
+// 41, 256x256 53; (8192, 8192 x 8192) 256x256 420, 256x128 455, 128x128 559.
+double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
+{
+    const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n) * splits;
+    const int64_t step_k = d.stages > 0 ? kI8BlockK : 8 * kI8StreamK;
+    const double fixed = d.fixed, steps = (double)ceil_div(ceil_div(K, splits), step_k);
+    const double rounds = (double)ceil_div(tiles, 256 * d.resident);
+    const double memory = ((double)N * K + 2.0 * M * N) / 13.2e6 +
+                          (double)tiles * ceil_div(K, splits) * (double)(std::min<int64_t>(d.block_m, M) + d.block_n) / 18.4e6;
+    return std::max(rounds * (fixed + steps * d.step), fixed + memory) + (splits > 1 ? 2.9 + 8.0 * M * N * splits / 8.4e6 : 0.0);
+}
+
+// The same over experts, of which only the number of pairs is known here: as
+// many experts as may be have an equal share, in tiles of which the last is half
+// full, and an uneven load fills a third of a round more.  Fitted to 186 loads (8 to
+// 256 experts, 1 to 4096 tokens, 2 or 8 experts each, some experts more popular): 3 %
+// longer than the best on average.  us: 64 tokens, 8 of 256 experts of 4096 x 2048
+// 64x256 243, 32x64 315, 128x128 284; 2048 tokens, 8 of 64 of 2048 x 4096 256x256
+// 190, 128x256 195, 128x128 253; 1 token, 8 of 256 of 2048 x 4096 32x64 15.2, 64x256 20.6.
+double estimate_experts(const I8Config &d, int64_t pairs, int experts, int64_t N, int64_t K)
+{
+    const double hit = (double)std::min<int64_t>(experts, pairs), rows = (double)pairs / hit;
+    const double tiles = hit * std::max(1.0, rows / d.block_m + 0.5) * (double)ceil_div(N, d.block_n);
+    const double fixed = d.experts_fixed, steps = (double)ceil_div(K, d.stages > 0 ? kI8BlockK : 8 * kI8StreamK);
+    const double memory = (hit * (double)N * (double)K + 2.0 * (double)pairs * (double)N) / 14e6 +
+                          tiles * (double)K * (std::min((double)d.block_m, rows) + d.block_n) / 16e6;
+    return std::max(std::max(1.0, tiles / (256.0 * d.resident) + 0.36) * (fixed + steps * d.experts_step), fixed + memory);
+}
+
+// Choices that this thread made last, so that a program that repeats its shapes
+// does not search again (0.7 us).
+struct Choice {
+    int64_t key[5] = {-1, -1, -1, -1, -1};
+    int config = 0, splits = 0;
+};
+Choice &remembered(const int64_t (&key)[5])
+{
+    static thread_local Choice choices[64];
+    uint64_t h = 0;
+    for (int64_t k : key)
+        h = (h ^ (uint64_t)k) * 0x9e3779b97f4a7c15ull;
+    return choices[h >> 58];
+}
+bool same(const int64_t (&a)[5], const int64_t (&b)[5]) { return std::equal(a, a + 5, b); }
+
+// Splits of an automatic plan: parts of 4 steps and more that make no more
+// than two workgroups for each CU.
+constexpr int kSplits[] = {1, 2, 4, 8};
+bool may_split(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
+{
+    const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n);
+    return splits == 1 || (tiles < 256 && tiles * splits <= 512 && N <= (int64_t)1 << 20 &&
+                           ceil_div(K, d.stages > 0 ? kI8BlockK : kI8StreamK) >= 4 * splits);
+}
+
 gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int splits, gemm_f16_plan_t *p)
 {
     if (M < 0 || N < 0 || K < 0 || (config != GEMM_F16_CONFIG_AUTO && (config < 0 || config >= kNumI8Configs)) || splits < 0 ||
@@ -81,12 +155,35 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (M > GEMM_F16_MAX_DIM || N > GEMM_F16_MAX_N || K > GEMM_F16_I8_MAX_K)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
-    int c = config;
-    if (c == GEMM_F16_CONFIG_AUTO) {
-        if (M <= 16)
-            c = N >= 64 * 150 ? 1 : 0;
-        else
-            c = ceil_div(M, 256) * ceil_div(N, 256) >= 192 ? 3 : 2;
+    int c = config == GEMM_F16_CONFIG_AUTO ? 0 : config;
+    const int64_t key[5] = {M, N, K, config, splits};
+    Choice &last = remembered(key);
+    if (same(last.key, key)) {
+        c = last.config;
+        splits = last.splits;
+    } else if (config == GEMM_F16_CONFIG_AUTO || splits == GEMM_F16_SPLITS_AUTO) {
+        double best = HUGE_VAL;
+        int request = splits;
+        for (int i = 0; i < kNumI8Configs; ++i) {
+            if ((config != GEMM_F16_CONFIG_AUTO && i != config) || (config == GEMM_F16_CONFIG_AUTO && i == 0 && M > 16))
+                continue;
+            for (int s : kSplits) {
+                if (splits != GEMM_F16_SPLITS_AUTO)
+                    s = splits;
+                else if (!may_split(kI8Configs[i], M, N, K, s))
+                    continue;
+                const double t = estimate(kI8Configs[i], M, N, K, s);
+                if (t < best) {
+                    best = t;
+                    c = i;
+                    request = s;
+                }
+            }
+        }
+        splits = request;
+        std::copy(key, key + 5, last.key);
+        last.config = c;
+        last.splits = splits;
     }
     const I8Config &d = kI8Configs[c];
     describe(c, p);
@@ -95,11 +192,6 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
     p->tiles_m = ceil_div(M, d.block_m);
     p->tiles_n = ceil_div(N, d.block_n);
     const int64_t tiles = p->tiles_m * p->tiles_n, steps = ceil_div(K, p->block_k);
-    if (splits == GEMM_F16_SPLITS_AUTO) {
-        splits = 1;
-        if (d.stages > 0 && tiles > 0 && tiles < 256)
-            splits = (int)std::max<int64_t>(1, std::min<int64_t>(256 / tiles, steps / 8));
-    }
     const int64_t per = steps > 0 ? ceil_div(steps, splits) : 0;
     p->splits = per > 0 ? (int)ceil_div(steps, per) : 1;   // none empty
     // (a split's sums of a tile's rows are reached by offsets of 31 bits)
@@ -119,9 +211,25 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
         return GEMM_F16_ERROR_INVALID_VALUE;
     if (pairs > GEMM_F16_MAX_PAIRS || experts > GEMM_F16_MAX_EXPERTS || N > GEMM_F16_MAX_N || K > GEMM_F16_I8_MAX_K)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
-    int c = config;
-    if (c == GEMM_F16_CONFIG_AUTO)
-        c = pairs <= 16 * experts ? 1 : pairs < 192 * (int64_t)experts ? 2 : 3;
+    int c = config == GEMM_F16_CONFIG_AUTO ? 0 : config;
+    const int64_t key[5] = {pairs, N, K, experts, -2};   // (no product's)
+    Choice &last = remembered(key);
+    if (config == GEMM_F16_CONFIG_AUTO && same(last.key, key)) {
+        c = last.config;
+    } else if (config == GEMM_F16_CONFIG_AUTO && pairs > 0) {
+        double best = HUGE_VAL;
+        for (int i = 0; i < kNumI8Configs; ++i) {
+            if (i == 0 && pairs > 16 * (int64_t)experts)
+                continue;
+            const double t = estimate_experts(kI8Configs[i], pairs, experts, N, K);
+            if (t < best) {
+                best = t;
+                c = i;
+            }
+        }
+        std::copy(key, key + 5, last.key);
+        last.config = c;
+    }
     const I8Config &d = kI8Configs[c];
     describe(c, p);
     p->splits = 1;
@@ -169,7 +277,7 @@ using namespace gemm_f16_impl;
 
 extern "C" {
 
-int64_t gemm_f16_i8_pitch(int64_t K) { return K < 0 || K > GEMM_F16_I8_MAX_K ? -1 : padded(K); }
+int64_t gemm_f16_i8_pitch(int64_t K) { return K < 0 || K > GEMM_F16_I8_MAX_K ? -1 : made_pitch(K); }
 
 gemm_f16_status_t gemm_f16_i8_compress(int64_t rows, int64_t K, const void *X, int64_t x_stride, void *codes, float *scales,
                                        void *stream)
@@ -185,14 +293,14 @@ gemm_f16_status_t gemm_f16_i8_compress(int64_t rows, int64_t K, const void *X, i
         return GEMM_F16_ERROR_MISALIGNED;
     if (bytes_of(rows, x_stride) > kMostBytes / 2)
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
-    const int64_t x_bytes = 2 * ((rows - 1) * x_stride + K), c_bytes = rows * padded(K);
+    const int64_t x_bytes = 2 * ((rows - 1) * x_stride + K), pitch = made_pitch(K), c_bytes = rows * pitch;
     if (overlaps(codes, c_bytes, X, x_bytes) || overlaps(scales, 4 * rows, X, x_bytes) || overlaps(codes, c_bytes, scales, 4 * rows))
         return GEMM_F16_ERROR_INVALID_VALUE;
     int dev = -1;
     st = check_device(&dev);
     if (st != GEMM_F16_SUCCESS)
         return st;
-    return status_of(launch_i8_compress((const _Float16 *)X, x_stride, (int8_t *)codes, scales, rows, K, (hipStream_t)stream));
+    return status_of(launch_i8_compress((const _Float16 *)X, x_stride, (int8_t *)codes, pitch, scales, rows, K, (hipStream_t)stream));
 }
 
 gemm_f16_status_t gemm_f16_i8_expand(int64_t rows, int64_t K, const void *codes, int64_t pitch, const float *scales, void *X,

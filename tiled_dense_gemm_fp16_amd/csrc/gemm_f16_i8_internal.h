@@ -18,10 +18,14 @@ struct I8Config {
     int block_m, block_n;
     int waves;
     int stages;   // LDS stages of 128 bytes of k; 0: the kernel for few rows, which takes its operands straight from memory
+    int resident; // workgroups of a CU, by LDS and registers
+    // us of a step of k (the kernel for few rows: of 8 steps, one for each of its
+    // waves) and of the rest of a tile, dense and over experts (see estimate())
+    float step, fixed, experts_step, experts_fixed;
 };
 constexpr int kI8BlockK = 128;       // k of a tile's step
 constexpr int kI8StreamK = 256;      // k of a step of the kernel for few rows
-constexpr int kNumI8Configs = 4;
+constexpr int kNumI8Configs = 10;
 extern const I8Config kI8Configs[kNumI8Configs];
 
 struct I8Args {
@@ -46,8 +50,8 @@ hipError_t launch_i8_experts(int config, const I8Args &a, int64_t grid, hipStrea
 // C = rne16(epi(alpha a_scales w_scales (sum of the splits' partial sums)))
 hipError_t launch_i8_reduce(const I8Args &a, hipStream_t s);
 
-hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, float *scales, int64_t rows, int64_t K,
-                              hipStream_t s);
+hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, int64_t pitch, float *scales, int64_t rows,
+                              int64_t K, hipStream_t s);
 hipError_t launch_i8_expand(const int8_t *codes, int64_t pitch, const float *scales, _Float16 *X, int64_t rows, int64_t K,
                             hipStream_t s);
 

@@ -62,12 +62,12 @@ __device__ __forceinline__ int code_of(float x, float m, float inverse)
 // magnitude and the rounding, longer rows are read again.
 template <int THREADS, int HELD>
 __global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restrict__ X, int64_t stride, int8_t *__restrict__ codes,
-                                                          float *__restrict__ scales, int64_t rows, int64_t K)
+                                                          int64_t pitch, float *__restrict__ scales, int64_t rows, int64_t K)
 {
     constexpr int ROWS = 256 / THREADS;
     __shared__ float most_of[4];
     const int t = threadIdx.x % THREADS;
-    const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS, pitch = (K + 15) / 16 * 16;
+    const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
     if (THREADS <= 64 && r >= rows)
         return;
     const half_t *row = X + r * stride;
@@ -123,10 +123,10 @@ __global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restri
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
         const int64_t c = 16 * (int64_t)(t + i * THREADS);
-        if (c < K)
+        if (c < pitch)
             put(c, x[i]);
     }
-    for (int64_t c = 16 * (int64_t)(t + HELD * THREADS); c < K; c += 16 * THREADS) {
+    for (int64_t c = 16 * (int64_t)(t + HELD * THREADS); c < pitch; c += 16 * THREADS) {
         half_t y[16];
         load16(row, K, c, y);
         put(c, y);
@@ -203,27 +203,27 @@ unsigned blocks_for(int64_t items) { return (unsigned)std::min<int64_t>((items +
 
 } // namespace
 
-hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, float *scales, int64_t rows, int64_t K,
-                              hipStream_t s)
+hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, int64_t pitch, float *scales, int64_t rows,
+                              int64_t K, hipStream_t s)
 {
     constexpr int64_t most = 1 << 22;   // rows of a launch: its work items are counted in 32 bits
     for (; rows > most; rows -= most) {
-        const hipError_t e = launch_i8_compress(X, stride, codes, scales, most, K, s);
+        const hipError_t e = launch_i8_compress(X, stride, codes, pitch, scales, most, K, s);
         if (e != hipSuccess)
             return e;
         X += most * stride;
-        codes += most * ((K + 15) / 16 * 16);
+        codes += most * pitch;
         scales += most;
     }
     if (K <= 256)
         hipLaunchKernelGGL((i8_compress_kernel<16, 1>), dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, s, X, stride, codes,
-                           scales, rows, K);
+                           pitch, scales, rows, K);
     else if (K <= 2048)
         hipLaunchKernelGGL((i8_compress_kernel<64, 2>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, X, stride, codes,
-                           scales, rows, K);
+                           pitch, scales, rows, K);
     else
-        hipLaunchKernelGGL((i8_compress_kernel<256, 2>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, scales, rows,
-                           K);
+        hipLaunchKernelGGL((i8_compress_kernel<256, 2>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, pitch, scales,
+                           rows, K);
     return hipGetLastError();
 }
 

@@ -148,23 +148,13 @@ __global__ void __launch_bounds__(64 * kWaves) i8_stream_kernel(I8Args p)
 
 } // namespace
 
-template <int NB, int DEPTH>
-static hipError_t launch_nb(const I8Args &a, int64_t grid, bool experts, hipStream_t s)
+hipError_t launch_i8_stream(const I8Args &a, int64_t grid, bool experts, hipStream_t s)
 {
     if (experts)
-        hipLaunchKernelGGL((i8_stream_kernel<NB, DEPTH, true>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
+        hipLaunchKernelGGL((i8_stream_kernel<1, 2, true>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
     else
-        hipLaunchKernelGGL((i8_stream_kernel<NB, DEPTH, false>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
+        hipLaunchKernelGGL((i8_stream_kernel<1, 2, false>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
     return hipGetLastError();
-}
-
-hipError_t launch_i8_stream(int n_blocks, const I8Args &a, int64_t grid, bool experts, hipStream_t s)
-{
-    switch (n_blocks) {
-    case 1: return launch_nb<1, 2>(a, grid, experts, s);
-    case 4: return launch_nb<4, 2>(a, grid, experts, s);
-    default: return hipErrorInvalidValue;
-    }
 }
 
 // ---- the sum of a split's parts ---------------------------------------------------

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_
 i8_tile_kernel(I8Args p)
 {
     constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
-    constexpr int BK = kI8BlockK / 2;                  // as pairs of codes
+    constexpr int BK = kI8BlockK / 2;                     // of a slice, as pairs of codes
     constexpr int TM = BM / WM / 16, TN = BN / WN / 16;   // 16 x 16 blocks of a wave
     using Op_a = Operand<true, BM, BK, THREADS, true, 8, true>;
     using Op_b = Operand<true, BN, BK, THREADS, true, 8, true>;
@@ -148,7 +148,8 @@ i8_tile_kernel(I8Args p)
         opb.issue(kt, b, wave, part, parts);
     };
     // One slice, read from (rd_a, rd_b) while slice `next` is requested into
-    // (wr_a, wr_b): f1 holds the second half of the slice before, if there is one.
+    // (wr_a, wr_b).  Fragments are read one 64-deep step ahead of their products:
+    // f1 holds the second half of the slice before, if there is one.
     Frags f0, f1 = {};
     const auto step = [&](auto first, const half_t *__restrict__ rd_a, const half_t *__restrict__ rd_b, half_t *__restrict__ wr_a,
                           half_t *__restrict__ wr_b, int next) __attribute__((always_inline)) {
@@ -302,11 +303,12 @@ i8_tile_kernel(I8Args p)
                 }
             wait_lgkm0();
             __builtin_amdgcn_s_barrier();
-            constexpr int PIECES = BN / 8, EACH = BM * PIECES / THREADS;
-            static_assert(BM * PIECES % THREADS == 0, "pieces split evenly");
+            constexpr int PIECES = BN / 8, EACH = (BM * PIECES + THREADS - 1) / THREADS;
 #pragma unroll
             for (int q = 0; q < EACH; ++q) {
                 const int id = tid + q * THREADS, r = id / PIECES, c = id % PIECES, sw = r & UMASK;
+                if (BM * PIECES % THREADS != 0 && id >= BM * PIECES)
+                    break;
                 int4v v = *reinterpret_cast<const int4v *>(lds + r * BN + 4 * ((2 * c ^ sw) & ~1));
                 if (sw & 1)
                     v = int4v{v[2], v[3], v[0], v[1]};
@@ -362,15 +364,21 @@ static hipError_t launch_tile(const I8Args &a, int64_t grid, bool experts, hipSt
     return hipGetLastError();
 }
 
-hipError_t launch_i8_stream(int n_blocks, const I8Args &a, int64_t grid, bool experts, hipStream_t s);
+hipError_t launch_i8_stream(const I8Args &a, int64_t grid, bool experts, hipStream_t s);
 
 static hipError_t launch_config(int config, const I8Args &a, int64_t grid, bool experts, hipStream_t s)
 {
     switch (config) {
-    case 0: return launch_i8_stream(1, a, grid, experts, s);
-    case 1: return launch_i8_stream(4, a, grid, experts, s);
-    case 2: return launch_tile<128, 128, 2, 2, 4, 1>(a, grid, experts, s);
-    case 3: return launch_tile<256, 256, 2, 2, 2, 2>(a, grid, experts, s);
+    case 0: return launch_i8_stream(a, grid, experts, s);
+    case 1: return launch_tile<32, 32, 2, 2, 8, 1>(a, grid, experts, s);
+    case 2: return launch_tile<32, 64, 1, 4, 6, 1>(a, grid, experts, s);
+    case 3: return launch_tile<64, 64, 2, 2, 6, 1>(a, grid, experts, s);
+    case 4: return launch_tile<64, 128, 2, 2, 4, 1>(a, grid, experts, s);
+    case 5: return launch_tile<64, 256, 1, 4, 3, 1>(a, grid, experts, s);
+    case 6: return launch_tile<128, 128, 2, 2, 4, 1>(a, grid, experts, s);
+    case 7: return launch_tile<128, 256, 2, 2, 3, 1>(a, grid, experts, s);
+    case 8: return launch_tile<256, 128, 2, 2, 3, 1>(a, grid, experts, s);
+    case 9: return launch_tile<256, 256, 2, 2, 2, 2>(a, grid, experts, s);
     default: return hipErrorInvalidValue;
     }
 }

@@ -39,7 +39,7 @@ struct Matrix {
         index = device_of(codes_tensor, name, stream_device);
         sizes = t->sizes();
         pitch = sizes.back();
-        if (k < 0 || k > GEMM_F16_I8_MAX_K || pitch < gemm_f16_i8_pitch(k) || pitch % 16)
+        if (k < 0 || k > GEMM_F16_I8_MAX_K || pitch < (k + 15) / 16 * 16 || pitch % 16)
             refuse("%s.codes must have rows of k = %lld codes padded to a multiple of 16, got %lld", name, (long long)k,
                    (long long)pitch);
         for (size_t i = 0; i + 1 < sizes.size(); ++i)

@@ -66,7 +66,8 @@ def _epilogue(name):
 
 class I8Matrix(NamedTuple):
     """Rows of ``k`` elements in 8 bits: element e of a row stands for its
-    scale times its code."""
+    scale times its code.  (Products are faster where rows start on cache
+    lines, as i8_compress's do from 65 elements on: a pitch of a multiple of 128.)"""
     codes: object    # int8 [..., rows, pitch], pitch a multiple of 16 and at least k; zeros from k to the next multiple of 16
     scales: object   # float32 [..., rows]
     k: int
