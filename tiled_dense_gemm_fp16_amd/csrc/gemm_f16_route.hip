@@ -6,6 +6,7 @@
 #include <algorithm>
 
 #include "gemm_f16_i8_internal.h"
+#include "gemm_f16_tile.h"
 
 namespace gemm_f16_impl {
 
@@ -217,60 +218,161 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
 // ---- the pairs by expert -----------------------------------------------------------
 // A workgroup for each expert, and one for the pairs of none, finds the place
 // of its first pair by counting the smaller ids itself, then writes its pairs:
-// nothing passes between workgroups, and the order is that of the pairs.
-constexpr int kOrderWaves = 16;
-
-__global__ void __launch_bounds__(64 * kOrderWaves) expert_order_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ order,
-                                                                        int32_t *__restrict__ starts, int pairs, int experts)
+// nothing passes between workgroups, and the order is that of the pairs.  Every
+// workgroup reads all ids, from the L2s.  Where CUs are left over, several share an
+// expert, each writing the pairs of one part of the ids (it counts the equal ids
+// of the parts before it, too).
+//
+// It is bound by the instructions for each id, so a wave keeps of its part's ids
+// only one bit each, ROUNDS times 4 a lane, and the ranks of three rounds
+// (256 ids each, at most 256 equal) pass through one sum over the wave.
+__device__ __forceinline__ unsigned wave_upto(unsigned x)   // inclusive sums
 {
-    __shared__ int below[kOrderWaves], equal[kOrderWaves];
+    x += dpp<0x111, 0xf>(0u, x);
+    x += dpp<0x112, 0xf>(0u, x);
+    x += dpp<0x114, 0xf>(0u, x);
+    x += dpp<0x118, 0xf>(0u, x);
+    x += dpp<0x142, 0xa>(0u, x);
+    x += dpp<0x143, 0xc>(0u, x);
+    return x;
+}
+
+template <int WAVES, int ROUNDS>
+__global__ void __launch_bounds__(64 * WAVES) expert_order_kernel(const int32_t *__restrict__ ids, int32_t *__restrict__ order,
+                                                                  int32_t *__restrict__ starts, int pairs, int experts, int part)
+{
+    static_assert(ROUNDS % 3 == 0 && ROUNDS <= 8 * 2 * 3, "whole sums");
+    constexpr int WORDS = (ROUNDS + 5) / 6;   // 6 rounds' bits in a word
+    __shared__ int below[WAVES], earlier[WAVES], equal[WAVES];
     const int expert = blockIdx.x, lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRound = 4 * 64;   // ids of a wave in flight
-    const int share = (pairs + kRound * kOrderWaves - 1) / (kRound * kOrderWaves) * kRound;
-    const int begin = min(wave * share, pairs), end = min(begin + share, pairs);
-    // the bins of ids i + 64 r + lane, past `end` one of no expert
-    const auto load = [&](int i, int (&bin)[4]) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int at = i + 64 * r + lane;
-            const int id = at < end ? ids[at] : 0;
-            bin[r] = at >= end ? experts + 1 : id >= 0 && id < experts ? id : experts;
-        }
+    const bool none = expert == experts;
+    const __amdgpu_buffer_rsrc_t all = make_rsrc(ids, (uint32_t)pairs * 4u);   // past the end: zeros
+    const auto load = [&](int at) {
+        return __builtin_bit_cast(int4v, __builtin_amdgcn_raw_buffer_load_b128(all, (uint32_t)(at + 4 * lane) * 4u, 0, 0));
     };
-    int less = 0, same = 0;
-    for (int i = begin; i < end; i += kRound) {
-        int bin[4];
-        load(i, bin);
+    const auto is_less = [&](int id) { return (unsigned)id < (unsigned)expert; };
+    const auto is_mine = [&](int id) { return none ? (unsigned)id >= (unsigned)experts : id == expert; };
+
+    // the other parts, 256 ids at a time (a part is a multiple of that)
+    const int first = min((int)blockIdx.y * part, pairs), last = min(first + part, pairs);
+    int less = 0, before = 0;
+    if (gridDim.y > 1) {
+        constexpr int AT_ONCE = 4;
+        for (int at0 = wave * AT_ONCE * 256; at0 < pairs; at0 += WAVES * AT_ONCE * 256) {
+            int4v v[AT_ONCE];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            less += __popcll(__ballot(bin[r] < expert));
-            same += __popcll(__ballot(bin[r] == expert));
+            for (int i = 0; i < AT_ONCE; ++i)
+                v[i] = load(at0 + 256 * i);
+#pragma unroll
+            for (int i = 0; i < AT_ONCE; ++i) {
+                const int at = at0 + 256 * i;
+                if (at >= pairs || (at >= first && at < last))
+                    continue;
+                if (at < first) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        less += is_less(v[i][r]);
+                        before += is_mine(v[i][r]);
+                    }
+                } else {
+                    const bool whole = at + 256 <= pairs;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        less += is_less(v[i][r]) && (whole || at + 4 * lane + r < pairs);
+                }
+            }
         }
     }
-    if (lane == 0) {
+
+    // this part: a run of `rounds` rounds for each wave, ROUNDS of them at a time
+    const int rounds = (last - first + 256 * WAVES - 1) / (256 * WAVES);
+    const int begin = first + wave * rounds * 256;
+    unsigned bits[WORDS];
+    const auto look = [&](int r0) __attribute__((always_inline)) {
+        int4v v[ROUNDS];
+#pragma unroll
+        for (int h = 0; h < ROUNDS; ++h)
+            if (r0 + h < rounds)
+                v[h] = load(begin + (r0 + h) * 256);
+        int smaller = 0;
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w)
+            bits[w] = 0;
+#pragma unroll
+        for (int h = 0; h < ROUNDS; ++h) {
+            if (r0 + h >= rounds)
+                continue;
+            const int at = begin + (r0 + h) * 256;
+            unsigned four = 0;
+            if (at + 256 <= last) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    smaller += is_less(v[h][r]);
+                    four |= is_mine(v[h][r]) ? 1u << r : 0u;
+                }
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const bool in = at + 4 * lane + r < last;
+                    smaller += in && is_less(v[h][r]);
+                    four |= in && is_mine(v[h][r]) ? 1u << r : 0u;
+                }
+            }
+            bits[h / 6] |= four << (4 * (h % 6));
+        }
+        return smaller;
+    };
+    int same = 0;
+    for (int r0 = 0; r0 < rounds; r0 += ROUNDS) {
+        less += look(r0);
+#pragma unroll
+        for (int w = 0; w < WORDS; ++w)
+            same += __popc(bits[w]);
+    }
+    less = (int)wave_upto((unsigned)less);
+    before = (int)wave_upto((unsigned)before);
+    same = (int)wave_upto((unsigned)same);
+    if (lane == 63) {
         below[wave] = less;
+        earlier[wave] = before;
         equal[wave] = same;
     }
     __syncthreads();
     int place = 0;
-    for (int w = 0; w < kOrderWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         place += below[w];
-    if (threadIdx.x == 0)
+    if (threadIdx.x == 0 && blockIdx.y == 0)
         starts[expert] = place;
+    for (int w = 0; w < WAVES; ++w)
+        place += earlier[w];
     for (int w = 0; w < wave; ++w)
         place += equal[w];
-    if (same == 0)
+    if (__builtin_amdgcn_readlane(same, 63) == 0)
         return;
-    for (int i = begin; i < end; i += kRound) {
-        int bin[4];
-        load(i, bin);
+    for (int r0 = 0; r0 < rounds; r0 += ROUNDS) {
+        if (rounds > ROUNDS)
+            look(r0);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const u64 here = __ballot(bin[r] == expert);
-            if (bin[r] == expert)
-                order[place + __popcll(here & ((1ull << lane) - 1))] = i + 64 * r + lane;
-            place += __popcll(here);
+        for (int h0 = 0; h0 < ROUNDS; h0 += 3) {
+            unsigned mine = 0;   // of three rounds, in 10 bits each
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                mine |= (unsigned)__popc(bits[(h0 + i) / 6] >> (4 * ((h0 + i) % 6)) & 15u) << (10 * i);
+            const unsigned upto = wave_upto(mine), total = (unsigned)__builtin_amdgcn_readlane((int)upto, 63);
+            if (total == 0)
+                continue;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                unsigned four = bits[(h0 + i) / 6] >> (4 * ((h0 + i) % 6)) & 15u;
+                int to = place + (int)((upto - mine) >> (10 * i) & 1023u);
+                const int at = begin + (r0 + h0 + i) * 256 + 4 * lane;
+                while (four) {
+                    order[to++] = at + __ffs(four) - 1;
+                    four &= four - 1;
+                }
+                place += (int)(total >> (10 * i) & 1023u);
+            }
         }
     }
 }
@@ -298,8 +400,16 @@ hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 
 hipError_t launch_expert_order(const int32_t *ids, int32_t *order, int32_t *starts, int pairs, int experts, hipStream_t s)
 {
-    hipLaunchKernelGGL(expert_order_kernel, dim3((unsigned)(experts + 1)), dim3(64 * kOrderWaves), 0, s, ids, order, starts,
-                       pairs, experts);
+    if (pairs <= 4 * 3 * 256) {
+        hipLaunchKernelGGL((expert_order_kernel<4, 3>), dim3((unsigned)(experts + 1)), dim3(256), 0, s, ids, order, starts, pairs,
+                           experts, pairs);
+    } else {
+        // parts of 4096 ids and more, as many as leave each workgroup a CU
+        const int parts = std::max(1, std::min(256 / (experts + 1), pairs / 4096));
+        const int part = ((pairs + parts - 1) / parts + 255) / 256 * 256;
+        hipLaunchKernelGGL((expert_order_kernel<16, 12>), dim3((unsigned)(experts + 1), (unsigned)parts), dim3(1024), 0, s, ids, order,
+                           starts, pairs, experts, part);
+    }
     return hipGetLastError();
 }
 
