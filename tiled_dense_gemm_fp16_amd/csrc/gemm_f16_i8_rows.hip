@@ -57,15 +57,17 @@ __device__ __forceinline__ int code_of(float x, float m, float inverse)
     return (int)__builtin_rintf(y);
 }
 
-// THREADS threads of a workgroup of 256 take a row, 16 elements each at a time;
-// up to HELD of those stay in registers between the search for the largest
-// magnitude and the rounding, longer rows are read again.
+// THREADS threads take a row, 16 elements each at a time; up to HELD of those stay
+// in registers between the search for the largest magnitude and the rounding,
+// longer rows are read again.  Bound by memory where rows are many (8192 x 8192 33
+// us, 6 TB/s), else by the latency of load, search and store (13 x 4100 4.4 us).
+constexpr int block_of(int threads) { return threads > 256 ? threads : 256; }
 template <int THREADS, int HELD>
-__global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restrict__ X, int64_t stride, int8_t *__restrict__ codes,
+__global__ void __launch_bounds__(block_of(THREADS)) i8_compress_kernel(const half_t *__restrict__ X, int64_t stride, int8_t *__restrict__ codes,
                                                           int64_t pitch, float *__restrict__ scales, int64_t rows, int64_t K)
 {
-    constexpr int ROWS = 256 / THREADS;
-    __shared__ float most_of[4];
+    constexpr int ROWS = block_of(THREADS) / THREADS, WAVES = block_of(THREADS) / 64;
+    __shared__ float most_of[WAVES];
     const int t = threadIdx.x % THREADS;
     const int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / THREADS;
     if (THREADS <= 64 && r >= rows)
@@ -103,7 +105,10 @@ __global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restri
         if (threadIdx.x % 64 == 0)
             most_of[threadIdx.x / 64] = m;
         __syncthreads();
-        m = __builtin_fmaxf(__builtin_fmaxf(most_of[0], most_of[1]), __builtin_fmaxf(most_of[2], most_of[3]));
+        m = most_of[0];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w)
+            m = __builtin_fmaxf(m, most_of[w]);
     }
     const float inverse = m > 0.0f ? 1.0f / m : 0.0f;
     if (t == 0)
@@ -133,13 +138,19 @@ __global__ void __launch_bounds__(256) i8_compress_kernel(const half_t *__restri
     }
 }
 
+// i / n for 0 <= i < items, n >= 1: in 32 bits where those do, a 64-bit division takes longer than the rest of a small kernel.
+__device__ __forceinline__ int64_t quotient(int64_t i, int64_t n, int64_t items)
+{
+    return items < (int64_t)1 << 31 ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
+}
+
 // Sixteen codes of a row a thread.
 __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ codes, int64_t pitch,
                                                         const float *__restrict__ scales, half_t *__restrict__ X, int64_t items,
                                                         int64_t K, int64_t per_row)
 {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / per_row, c = (i - r * per_row) * 16;
+        const int64_t r = quotient(i, per_row, items), c = (i - r * per_row) * 16;
         const int4v v = *reinterpret_cast<const int4v *>(codes + r * pitch + c);
         const float s = scales[r];
         half_t x[16];
@@ -159,42 +170,62 @@ __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict
     }
 }
 
-// Eight columns of a token's sum a thread, in fp32 and in the order of the slots.
+// V columns of a token's sum a thread, in fp32 and in the order of the slots,
+// the results of eight slots in flight (1 token of 8 x 2048: 4.8 us one after the other, 3.4).
+template <int V>
 __global__ void __launch_bounds__(256) expert_sum_kernel(const half_t *__restrict__ Y, const float *__restrict__ weights,
                                                          half_t *__restrict__ out, int64_t items, int top_k, int64_t N,
                                                          int64_t per_row)
 {
+    typedef _Float16 vec __attribute__((ext_vector_type(V)));
+    typedef vec vec_any __attribute__((aligned(2)));
+    constexpr int AHEAD = 8;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < items; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per_row, c = (i - t * per_row) * 8;
+        const int64_t t = quotient(i, per_row, items), c = (i - t * per_row) * V;
         const half_t *from = Y + t * top_k * N + c;
         const float *w = weights + t * top_k;
-        const int n = (int)(N - c < 8 ? N - c : 8);
-        float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int j = 0; j < top_k; ++j, from += N) {
-            const float wj = w[j];
-            if (n == 8) {
-                const half8 y = *reinterpret_cast<const half8_any *>(from);
+        const int n = (int)(N - c < V ? N - c : V);
+        float sum[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum[e] = __builtin_fmaf(wj, (float)y[e], sum[e]);
-            } else {
-                for (int e = 0; e < 8; ++e)
-                    if (e < n)
-                        sum[e] = __builtin_fmaf(wj, (float)from[e], sum[e]);
+        for (int e = 0; e < V; ++e)
+            sum[e] = 0.0f;
+        if (n == V) {
+            for (int j0 = 0; j0 < top_k; j0 += AHEAD) {
+                vec y[AHEAD];
+                float wj[AHEAD];
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    const int at = min(j0 + j, top_k - 1);   // (again the last one: not added)
+                    y[j] = *reinterpret_cast<const vec_any *>(from + (int64_t)at * N);
+                    wj[j] = w[at];
+                }
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j)
+                    if (j0 + j < top_k) {
+#pragma unroll
+                        for (int e = 0; e < V; ++e)
+                            sum[e] = __builtin_fmaf(wj[j], (float)y[j][e], sum[e]);
+                    }
             }
+        } else {
+            for (int j = 0; j < top_k; ++j)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (e < n)
+                        sum[e] = __builtin_fmaf(w[j], (float)from[(int64_t)j * N + e], sum[e]);
         }
         half_t *to = out + t * N + c;
-        half_t h[8];
+        if (n == V) {
+            vec h;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            h[e] = (half_t)sum[e];
-        if (n == 8) {
-            *reinterpret_cast<half8_any *>(to) = half8{h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7]};
+            for (int e = 0; e < V; ++e)
+                h[e] = (half_t)sum[e];
+            *reinterpret_cast<vec_any *>(to) = h;
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < V; ++e)
                 if (e < n)
-                    to[e] = h[e];
+                    to[e] = (half_t)sum[e];
         }
     }
 }
@@ -206,7 +237,7 @@ unsigned blocks_for(int64_t items) { return (unsigned)std::min<int64_t>((items +
 hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, int64_t pitch, float *scales, int64_t rows,
                               int64_t K, hipStream_t s)
 {
-    constexpr int64_t most = 1 << 22;   // rows of a launch: its work items are counted in 32 bits
+    constexpr int64_t most = 1 << 21;   // rows of a launch: its work items are counted in 32 bits
     for (; rows > most; rows -= most) {
         const hipError_t e = launch_i8_compress(X, stride, codes, pitch, scales, most, K, s);
         if (e != hipSuccess)
@@ -221,8 +252,14 @@ hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, 
     else if (K <= 2048)
         hipLaunchKernelGGL((i8_compress_kernel<64, 2>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, X, stride, codes,
                            pitch, scales, rows, K);
-    else
+    else if (K <= 8192)
         hipLaunchKernelGGL((i8_compress_kernel<256, 2>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, pitch, scales,
+                           rows, K);
+    else if (K <= 16384 && rows >= 256)   // (8192 x 14336: 1024 threads 110 us)
+        hipLaunchKernelGGL((i8_compress_kernel<256, 4>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, pitch, scales,
+                           rows, K);
+    else   // (1 x 28672: 256 threads, which hold 8192 elements, 7.8 us; 5.6 so)
+        hipLaunchKernelGGL((i8_compress_kernel<1024, 2>), dim3((unsigned)rows), dim3(1024), 0, s, X, stride, codes, pitch, scales,
                            rows, K);
     return hipGetLastError();
 }
@@ -238,8 +275,13 @@ hipError_t launch_i8_expand(const int8_t *codes, int64_t pitch, const float *sca
 hipError_t launch_expert_sum(const _Float16 *Y, const float *weights, _Float16 *out, int64_t tokens, int top_k, int64_t N,
                              hipStream_t s)
 {
-    const int64_t per_row = (N + 7) / 8, items = tokens * per_row;
-    hipLaunchKernelGGL(expert_sum_kernel, dim3(blocks_for(items)), dim3(256), 0, s, Y, weights, out, items, top_k, N, per_row);
+    // two columns a thread where eight would leave CUs without work
+    const int v = tokens * N < 256 * 256 * 8 ? 2 : 8;
+    const int64_t per_row = (N + v - 1) / v, items = tokens * per_row;
+    if (v == 2)
+        hipLaunchKernelGGL(expert_sum_kernel<2>, dim3(blocks_for(items)), dim3(256), 0, s, Y, weights, out, items, top_k, N, per_row);
+    else
+        hipLaunchKernelGGL(expert_sum_kernel<8>, dim3(blocks_for(items)), dim3(256), 0, s, Y, weights, out, items, top_k, N, per_row);
     return hipGetLastError();
 }
 

@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(256) i8_reduce_kernel(I8Args p)
     constexpr int V = VEC4 ? 4 : 1;
     const int64_t mn = (int64_t)p.M * p.N;
     for (int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V; e < mn; e += (int64_t)gridDim.x * 256 * V) {
-        const int64_t m = e / p.N, n = e - m * p.N;
+        const int64_t m = mn < (int64_t)1 << 31 ? (int64_t)((uint32_t)e / (uint32_t)p.N) : e / p.N, n = e - m * p.N;
         int sum[V];
 #pragma unroll
         for (int r = 0; r < V; ++r)

@@ -31,19 +31,28 @@ __device__ __forceinline__ unsigned wave_max(unsigned x)
     x = max(x, dpp<0x143, 0xc>(0u, x));   // row_bcast:31
     return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
 }
-__device__ __forceinline__ double wave_sum(double x)
-{
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2)
-        x += __shfl_xor(x, d);
-    return x;
-}
 __device__ __forceinline__ double lane_value(double x, int lane)
 {
     const u64 b = __builtin_bit_cast(u64, x);
     const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)b, lane);
     const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(b >> 32), lane);
     return __builtin_bit_cast(double, (u64)hi << 32 | lo);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double x)   // 0 where there is no other lane
+{
+    const u64 b = __builtin_bit_cast(u64, x);
+    return __builtin_bit_cast(double, (u64)dpp<CTRL, ROWS>(0u, (unsigned)(b >> 32)) << 32 | dpp<CTRL, ROWS>(0u, (unsigned)b));
+}
+__device__ __forceinline__ double wave_sum(double x)
+{
+    x += dpp<0x111, 0xf>(x);
+    x += dpp<0x112, 0xf>(x);
+    x += dpp<0x114, 0xf>(x);
+    x += dpp<0x118, 0xf>(x);
+    x += dpp<0x142, 0xa>(x);
+    x += dpp<0x143, 0xc>(x);
+    return lane_value(x, 63);
 }
 
 // Numbers as integers of the same order, all above 0, which stands for
@@ -81,32 +90,45 @@ constexpr int kTokens = 4;   // waves of a workgroup, each with a token
 // Keys are compared as integers, in 64 bits where scores enter them, so the
 // choice is the definition's; without bias they are the logits themselves.
 // A choice is a search over the wave in the vector unit's own lane moves
-// (6 instructions where no two keys share their high half).
+// (6 instructions where no two keys share their high half).  It is bound by the
+// latency of these: each lane sorts its few keys first, so that a choice only
+// moves up one lane's, and scores wait in LDS until the choices are made.
 template <int EACH>
 __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
 {
-    extern __shared__ double shared_keys[];   // groups: [kTokens][experts]
+    extern __shared__ double shared[];   // [kTokens][2][experts]: scores, and keys where there are groups
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t token = (int64_t)blockIdx.x * kTokens + wave;
     const int64_t from = (token < p.tokens ? token : p.tokens - 1) * p.stride;
+    double *const scores = shared + 2 * wave * p.experts, *const keys = scores + p.experts;
 
-    float x[EACH];
-    double score[EACH];
-    u64 key[EACH];
+    float x[EACH], bias[EACH];
+    // (one branch around all loads, so that they are in flight together)
+    if (p.half) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            x[i] = (float)((const _Float16 *)p.logits)[from + min(lane * EACH + i, p.experts - 1)];
+    } else {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            x[i] = ((const float *)p.logits)[from + min(lane * EACH + i, p.experts - 1)];
+    }
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        bias[i] = 0.0f;
+    if (p.bias) {
+#pragma unroll
+        for (int i = 0; i < EACH; ++i)
+            bias[i] = p.bias[min(lane * EACH + i, p.experts - 1)];
+    }
     float high = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-        const int e = lane * EACH + i;
-        x[i] = -INFINITY;
-        if (e < p.experts) {
-            const float v = p.half ? (float)((const _Float16 *)p.logits)[from + e] : ((const float *)p.logits)[from + e];
-            const float b = p.bias ? p.bias[e] : 0.0f;
-            if (v > -INFINITY && b > -INFINITY)   // (neither is NaN)
-                x[i] = __builtin_fminf(v, 3.402823466e38f);
-        }
+        const bool open = lane * EACH + i < p.experts && x[i] > -INFINITY && bias[i] > -INFINITY;   // (neither is NaN)
+        x[i] = open ? __builtin_fminf(x[i], 3.402823466e38f) : -INFINITY;
         high = __builtin_fmaxf(high, x[i]);
     }
-    double total = 1.0;
+    double score[EACH];
     if (!p.sigmoid) {
         const unsigned top = wave_max((unsigned)(ordered(high) >> 32));
         high = __builtin_bit_cast(float, top >> 31 ? top ^ 1u << 31 : ~top);
@@ -116,7 +138,7 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
             score[i] = x[i] > -INFINITY ? exp((double)x[i] - (double)high) : 0.0;
             sum += score[i];
         }
-        total = wave_sum(sum);
+        const double total = wave_sum(sum);
 #pragma unroll
         for (int i = 0; i < EACH; ++i)
             score[i] = total > 0.0 ? score[i] / total : 0.0;
@@ -125,24 +147,23 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
         for (int i = 0; i < EACH; ++i)
             score[i] = x[i] > -INFINITY ? 1.0 / (1.0 + exp(-(double)x[i])) : 0.0;
     }
+    u64 key[EACH];
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
         const int e = lane * EACH + i;
-        key[i] = 0;
-        if (x[i] > -INFINITY)
-            key[i] = p.bias ? ordered(score[i] + (double)p.bias[e]) : ordered(x[i]);
+        const bool open = x[i] > -INFINITY;
+        const double value = score[i] + (double)bias[i];
+        key[i] = !open ? 0 : p.bias ? ordered(value) : ordered(x[i]);
+        if (e < p.experts) {
+            scores[e] = score[i];
+            if (p.groups > 1)
+                keys[e] = open ? value : -INFINITY;
+        }
     }
+    __syncthreads();
 
     if (p.groups > 1) {
         // two best keys of each group: a team of lanes for each, by way of LDS
-        double *const mine = shared_keys + wave * p.experts;
-#pragma unroll
-        for (int i = 0; i < EACH; ++i) {
-            const int e = lane * EACH + i;
-            if (e < p.experts)
-                mine[e] = x[i] > -INFINITY ? score[i] + (p.bias ? (double)p.bias[e] : 0.0) : -INFINITY;
-        }
-        __syncthreads();
         int team = 64;
         while (team * p.groups > 64)
             team /= 2;
@@ -150,7 +171,7 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
         double a = -INFINITY, b = -INFINITY;   // the best and the next
         if (g < p.groups)
             for (int i = lane % team; i < size; i += team) {
-                const double v = mine[g * size + i];
+                const double v = keys[g * size + i];
                 b = v > a ? a : (v > b ? v : b);
                 a = v > a ? v : a;
             }
@@ -174,44 +195,71 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int e = lane * EACH + i;
-            if (e < p.experts && !(stay >> (e / size) & 1))
+            if (e < p.experts && !(stay >> ((unsigned)e / (unsigned)size) & 1))
                 key[i] = 0;
         }
     }
 
+    // the lane's own keys, the largest first, equals in the order of their indexes
+    int which[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i)
+        which[i] = i;
+    constexpr bool SORTED = EACH <= 4;
+    if constexpr (SORTED) {
+#pragma unroll
+        for (int n = EACH - 1; n > 0; --n)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                const bool swap = key[i + 1] > key[i];
+                const u64 k = swap ? key[i] : key[i + 1];
+                const int w = swap ? which[i] : which[i + 1];
+                key[i] = swap ? key[i + 1] : key[i];
+                which[i] = swap ? which[i + 1] : which[i];
+                key[i + 1] = k;
+                which[i + 1] = w;
+            }
+    }
     int my_id = -1;
-    double my_score = 0.0, sum = 0.0;
     for (int j = 0; j < p.top_k; ++j) {
         u64 best = key[0];
-        int which = 0;
-        double its = score[0];
+        int its = which[0];
+        if constexpr (!SORTED) {
 #pragma unroll
-        for (int i = 1; i < EACH; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                which = i;
-                its = score[i];
-            }
+            for (int i = 1; i < EACH; ++i)
+                if (key[i] > best) {
+                    best = key[i];
+                    its = i;
+                }
+        }
         const int at = first_best(best);
         if (at < 0)
             break;
-        const int e = at * EACH + __builtin_amdgcn_readlane(which, at);
-        const double s = lane_value(its, at);
-        sum += s;
-        if (lane == j) {
+        const int e = at * EACH + __builtin_amdgcn_readlane(its, at);
+        if (lane == j)
             my_id = e;
-            my_score = s;
-        }
 #pragma unroll
-        for (int i = 0; i < EACH; ++i)
-            if (lane == at && which == i)
+        for (int i = 0; i < EACH; ++i) {
+            if constexpr (SORTED) {
+                if (lane == at) {
+                    key[i] = i + 1 < EACH ? key[i + 1] : 0;
+                    which[i] = i + 1 < EACH ? which[i + 1] : 0;
+                }
+            } else if (lane == at && its == i) {
                 key[i] = 0;
+            }
+        }
+    }
+    double my_score = my_id >= 0 ? scores[my_id] : 0.0;
+    if (p.renormalise) {
+        double sum = my_score;
+        for (int d = 1; d < p.top_k; d *= 2)   // (lanes from top_k on hold 0)
+            sum += __shfl_xor(sum, d);
+        my_score = sum > 0.0 ? my_score / sum : 0.0;
     }
     if (lane < p.top_k && token < p.tokens) {
-        if (p.renormalise)
-            my_score = sum > 0.0 ? my_score / sum : 0.0;
         p.ids[token * p.top_k + lane] = my_id;
-        p.weights[token * p.top_k + lane] = my_id < 0 ? 0.0f : (float)((double)p.scale * my_score);
+        p.weights[token * p.top_k + lane] = (float)((double)p.scale * my_score);
     }
 }
 
@@ -382,7 +430,7 @@ __global__ void __launch_bounds__(64 * WAVES) expert_order_kernel(const int32_t 
 hipError_t launch_route(const RouteArgs &a, hipStream_t s)
 {
     const dim3 grid((unsigned)((a.tokens + kTokens - 1) / kTokens));
-    const unsigned lds = a.groups > 1 ? (unsigned)(kTokens * a.experts * sizeof(double)) : 0;
+    const unsigned lds = (unsigned)(kTokens * 2 * a.experts * sizeof(double));
 #define GEMM_F16_ROUTE(EACH) hipLaunchKernelGGL(route_kernel<EACH>, grid, dim3(64 * kTokens), lds, s, a)
     if (a.experts <= 64)
         GEMM_F16_ROUTE(1);
