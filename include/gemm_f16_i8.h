@@ -50,7 +50,7 @@ int64_t gemm_f16_i8_pitch(int64_t K);
 gemm_f16_status_t gemm_f16_i8_compress(int64_t rows, int64_t K, const void *X, int64_t x_stride, void *codes,
                                        float *scales, void *stream);
 
-/* X = rne16(scale code), rows x K row-major, contiguous. */
+/* X = scale code, rounded to fp32 and then to binary16, rows x K row-major, contiguous. */
 gemm_f16_status_t gemm_f16_i8_expand(int64_t rows, int64_t K, const void *codes, int64_t pitch, const float *scales,
                                      void *X, void *stream);
 
@@ -84,12 +84,12 @@ const char *gemm_f16_i8_config_name(int config);
  * top_k + slot belongs to the expert ids[token][slot], or to none (an id that
  * is not in [0, experts)).  Limits: experts <= GEMM_F16_MAX_EXPERTS, top_k
  * <= GEMM_F16_MAX_TOP_K, groups <= GEMM_F16_MAX_EXPERT_GROUPS, tokens top_k <
- * 2^26.
+ * 2^25.
  */
 #define GEMM_F16_MAX_EXPERTS 1024
 #define GEMM_F16_MAX_TOP_K 64
 #define GEMM_F16_MAX_EXPERT_GROUPS 64
-#define GEMM_F16_MAX_PAIRS (((int64_t)1 << 26) - 1)
+#define GEMM_F16_MAX_PAIRS (((int64_t)1 << 25) - 1)
 
 #define GEMM_F16_SCORE_SOFTMAX 0
 #define GEMM_F16_SCORE_SIGMOID 1

@@ -115,8 +115,8 @@ def test_route_refusals():
         assert call(**bad) == INVALID, bad
     for bad in (dict(x=at(0) + 2), dict(x=at(0) + 1, half=1), dict(ids=at(1) + 2), dict(w=at(2) + 1), dict(bias=at(3) + 2)):
         assert call(**bad) == MISALIGNED, bad
-    for bad in (dict(e=1025, stride=2000), dict(e=128, stride=128, k=65), dict(e=260, stride=260, groups=65), dict(t=1 << 26),
-                dict(t=1 << 23, stride=1 << 50)):
+    for bad in (dict(e=1025, stride=2000), dict(e=128, stride=128, k=65), dict(e=260, stride=260, groups=65), dict(t=1 << 25, k=1),
+                dict(t=1 << 22, stride=1 << 50)):
         assert call(**bad) == SIZE, bad
     assert call(t=0, x=None, ids=None, w=None) == 0
     if not torch.cuda.is_available():
@@ -134,7 +134,7 @@ def test_order_and_sum_refusals():
         assert order(**bad) == INVALID, bad
     for bad in (dict(ids=at(0) + 2), dict(to=at(1) + 1), dict(starts=at(2) + 2)):
         assert order(**bad) == MISALIGNED, bad
-    assert order(p=1 << 26) == SIZE and order(e=1025) == SIZE
+    assert order(p=1 << 25) == SIZE and order(e=1025) == SIZE
 
     def add(t=4, k=6, n=100, y=at(0), w=at(1), out=at(2)):
         return h.gemm_f16_expert_sum(t, k, n, y, w, out, None)
@@ -143,7 +143,7 @@ def test_order_and_sum_refusals():
         assert add(**bad) == INVALID, bad
     for bad in (dict(y=at(0) + 1), dict(w=at(1) + 2), dict(out=at(2) + 1)):
         assert add(**bad) == MISALIGNED, bad
-    assert add(n=(1 << 22) + 1) == SIZE and add(k=1025) == SIZE and add(t=1 << 26) == SIZE
+    assert add(n=(1 << 22) + 1) == SIZE and add(k=1025) == SIZE and add(t=1 << 25) == SIZE
     assert add(t=0, y=None, out=None) == 0 and add(n=0, y=None, out=None) == 0
     if not torch.cuda.is_available():
         assert order() == NO_DEVICE and order(p=0, ids=None, to=None) == NO_DEVICE
@@ -165,7 +165,7 @@ def test_experts_refusals():
     for bad in (dict(a=at(0) + 8), dict(w=at(2) + 4), dict(sa=at(1) + 2), dict(sw=at(3) + 1), dict(order=at(4) + 2), dict(starts=at(5) + 1),
                 dict(c=at(6) + 1)):
         assert call(**bad) == MISALIGNED, bad
-    for bad in (dict(p=1 << 26, per=1), dict(e=1025), dict(n=(1 << 22) + 1), dict(k=1 << 17), dict(p=1 << 23, per=1),
+    for bad in (dict(p=1 << 25, per=1), dict(e=1025), dict(n=(1 << 22) + 1), dict(k=1 << 17), dict(p=1 << 23, per=1),
                 dict(ap=(1 << 22) + 16)):
         assert call(**bad) == SIZE, bad
     assert call(p=0) == 0 and call(n=0, w=None, sw=None, c=None) == 0
@@ -199,6 +199,9 @@ def test_plans():
             p = g.plan_i8(m, n, k, splits=None)
             assert p["splits"] * p["k_split"] >= k
     assert g.i8_config_name(-1) is None and g.i8_config_name(g.i8_num_configs()) is None
+    # as many rows as a call may have: a tile that makes few enough workgroups
+    assert g.plan_i8((1 << 31) - 1, 16, 64, splits=None)["block_m"] == 256
+    assert g.plan_i8_experts((1 << 25) - 1, 1, 8, 4096, 64)["grid"] < 1 << 24
     for bad in (dict(m=-1), dict(k=1 << 17), dict(config=99), dict(splits=65)):
         with pytest.raises(g.GemmError):
             g.plan_i8(**{**dict(m=1, n=16, k=128), **bad})

@@ -163,9 +163,12 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
         splits = last.splits;
     } else if (config == GEMM_F16_CONFIG_AUTO || splits == GEMM_F16_SPLITS_AUTO) {
         double best = HUGE_VAL;
-        int request = splits;
+        int request = std::max(splits, 1);
         for (int i = 0; i < kNumI8Configs; ++i) {
             if ((config != GEMM_F16_CONFIG_AUTO && i != config) || (config == GEMM_F16_CONFIG_AUTO && i == 0 && M > 16))
+                continue;
+            const int64_t tiles = ceil_div(M, kI8Configs[i].block_m) * ceil_div(N, kI8Configs[i].block_n);
+            if (config == GEMM_F16_CONFIG_AUTO && !launchable(tiles * std::max(splits, 1), 64 * kI8Configs[i].waves))
                 continue;
             for (int s : kSplits) {
                 if (splits != GEMM_F16_SPLITS_AUTO)
@@ -204,6 +207,12 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
     return launchable(p->grid, p->threads) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
 }
 
+// Tiles of `rows` pairs at most: each expert's last one, and that of the pairs of none, may hold one pair.
+int64_t most_tiles(int64_t pairs, int experts, int rows)
+{
+    return std::min<int64_t>(pairs, (pairs + std::min<int64_t>(pairs, experts + 1) * (rows - 1)) / rows);
+}
+
 gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int64_t N, int64_t K, int config, gemm_f16_plan_t *p)
 {
     if (pairs < 0 || per_row < 1 || pairs % per_row != 0 || experts < 1 || N < 0 || K < 0 ||
@@ -219,7 +228,9 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
     } else if (config == GEMM_F16_CONFIG_AUTO && pairs > 0) {
         double best = HUGE_VAL;
         for (int i = 0; i < kNumI8Configs; ++i) {
-            if (i == 0 && pairs > 16 * (int64_t)experts)
+            const I8Config &d = kI8Configs[i];
+            if ((i == 0 && pairs > 16 * (int64_t)experts) ||
+                !launchable(most_tiles(pairs, experts, d.block_m) * ceil_div(N, d.block_n), 64 * d.waves))
                 continue;
             const double t = estimate_experts(kI8Configs[i], pairs, experts, N, K);
             if (t < best) {
@@ -237,8 +248,7 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
     p->k_tiles = ceil_div(K, p->block_k);
     p->flops = 2.0 * (double)pairs * (double)N * (double)K;
     p->min_bytes = ((double)experts * (double)N + (double)(pairs / per_row)) * ((double)K + 4.0) + 2.0 * (double)pairs * (double)N;
-    // at most: each expert's last tile, and that of the pairs of none, may hold one pair
-    p->tiles_m = std::min<int64_t>(pairs, (pairs + std::min<int64_t>(pairs, experts + 1) * (d.block_m - 1)) / d.block_m);
+    p->tiles_m = most_tiles(pairs, experts, d.block_m);
     p->tiles_n = ceil_div(N, d.block_n);
     p->grid = p->tiles_m * p->tiles_n;
     return launchable(p->grid, p->threads) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
