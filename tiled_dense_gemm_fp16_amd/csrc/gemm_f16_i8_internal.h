@@ -63,6 +63,9 @@ struct RouteArgs {
     int64_t stride;
     int tokens, experts, top_k, half, sigmoid, groups, top_groups, renormalise;
     float scale;
+    // made by launch_route(): experts of a group, 2^22 over that, and log2 of the lanes of a group
+    int group_size, team_shift;
+    unsigned group_magic;
 };
 hipError_t launch_route(const RouteArgs &a, hipStream_t s);
 hipError_t launch_expert_order(const int32_t *ids, int32_t *order, int32_t *starts, int pairs, int experts, hipStream_t s);

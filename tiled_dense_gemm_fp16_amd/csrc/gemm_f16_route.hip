@@ -31,12 +31,11 @@ __device__ __forceinline__ unsigned wave_max(unsigned x)
     x = max(x, dpp<0x143, 0xc>(0u, x));   // row_bcast:31
     return (unsigned)__builtin_amdgcn_readlane((int)x, 63);
 }
-__device__ __forceinline__ double lane_value(double x, int lane)
+__device__ __forceinline__ u64 lane_bits(u64 x, int lane)
 {
-    const u64 b = __builtin_bit_cast(u64, x);
-    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)b, lane);
-    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(b >> 32), lane);
-    return __builtin_bit_cast(double, (u64)hi << 32 | lo);
+    const unsigned lo = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)x, lane);
+    const unsigned hi = (unsigned)__builtin_amdgcn_readlane((int)(unsigned)(x >> 32), lane);
+    return (u64)hi << 32 | lo;
 }
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp(double x)   // 0 where there is no other lane
@@ -52,7 +51,7 @@ __device__ __forceinline__ double wave_sum(double x)
     x += dpp<0x118, 0xf>(x);
     x += dpp<0x142, 0xa>(x);
     x += dpp<0x143, 0xc>(x);
-    return lane_value(x, 63);
+    return __builtin_bit_cast(double, lane_bits(__builtin_bit_cast(u64, x), 63));
 }
 
 // Numbers as integers of the same order, all above 0, which stands for
@@ -164,38 +163,45 @@ __global__ void __launch_bounds__(64 * kTokens) route_kernel(RouteArgs p)
 
     if (p.groups > 1) {
         // two best keys of each group: a team of lanes for each, by way of LDS
-        int team = 64;
-        while (team * p.groups > 64)
-            team /= 2;
-        const int size = p.experts / p.groups, g = lane / team;
+        const int shift = p.team_shift, team = 1 << shift, size = p.group_size, g = lane >> shift;
         double a = -INFINITY, b = -INFINITY;   // the best and the next
         if (g < p.groups)
-            for (int i = lane % team; i < size; i += team) {
+#pragma unroll 4
+            for (int i = lane & (team - 1); i < size; i += team) {
                 const double v = keys[g * size + i];
                 b = v > a ? a : (v > b ? v : b);
                 a = v > a ? v : a;
             }
-        for (int d = 1; d < team; d *= 2) {
-            const double oa = __shfl_xor(a, d), ob = __shfl_xor(b, d);
+        // (a team's lanes hold the same after each step, so a mirrored row swaps its halves)
+        const auto merge = [&](double oa, double ob) {
             b = oa > a ? (a > ob ? a : ob) : (b > oa ? b : oa);
             a = oa > a ? oa : a;
-        }
+        };
+        if (team > 1)
+            merge(dpp<0xb1, 0xf>(a), dpp<0xb1, 0xf>(b));     // quad_perm 1 0 3 2
+        if (team > 2)
+            merge(dpp<0x4e, 0xf>(a), dpp<0x4e, 0xf>(b));     // quad_perm 2 3 0 1
+        if (team > 4)
+            merge(dpp<0x141, 0xf>(a), dpp<0x141, 0xf>(b));   // row_half_mirror
+        if (team > 8)
+            merge(dpp<0x140, 0xf>(a), dpp<0x140, 0xf>(b));   // row_mirror
+        for (int d = 16; d < team; d *= 2)
+            merge(__shfl_xor(a, d), __shfl_xor(b, d));
         u64 best = 0;
-        if (lane % team == 0 && g < p.groups && a > -INFINITY)
+        if ((lane & (team - 1)) == 0 && g < p.groups && a > -INFINITY)
             best = ordered(b > -INFINITY ? a + b : a);
-        u64 stay = 0;
-        for (int j = 0; j < p.top_groups; ++j) {
-            const int at = first_best(best);
-            if (at < 0)
-                break;
-            stay |= 1ull << (at / team);
-            if (lane == at)
-                best = 0;
+        // a group stays if fewer than top_groups come before it
+        int rank = 0;
+        for (int other = 0; other < p.groups; ++other) {
+            const u64 its = lane_bits(best, other << shift);
+            rank += its > best || (its == best && other < g);
         }
+        const u64 stay = __ballot(best != 0 && rank < p.top_groups);   // at the first lane of each team
 #pragma unroll
         for (int i = 0; i < EACH; ++i) {
             const int e = lane * EACH + i;
-            if (e < p.experts && !(stay >> ((unsigned)e / (unsigned)size) & 1))
+            // e / size: the product is above the quotient by e / 2^22 at most, less than 1 / size
+            if (e < p.experts && !(stay >> ((unsigned)e * p.group_magic >> 22 << shift) & 1))
                 key[i] = 0;
         }
     }
@@ -427,8 +433,14 @@ __global__ void __launch_bounds__(64 * WAVES) expert_order_kernel(const int32_t 
 
 } // namespace
 
-hipError_t launch_route(const RouteArgs &a, hipStream_t s)
+hipError_t launch_route(const RouteArgs &args, hipStream_t s)
 {
+    RouteArgs a = args;
+    a.group_size = a.experts / a.groups;
+    a.group_magic = (1u << 22) / (unsigned)a.group_size + 1;
+    a.team_shift = 6;
+    while (a.groups << a.team_shift > 64)
+        --a.team_shift;
     const dim3 grid((unsigned)((a.tokens + kTokens - 1) / kTokens));
     const unsigned lds = (unsigned)(kTokens * 2 * a.experts * sizeof(double));
 #define GEMM_F16_ROUTE(EACH) hipLaunchKernelGGL(route_kernel<EACH>, grid, dim3(64 * kTokens), lds, s, a)
