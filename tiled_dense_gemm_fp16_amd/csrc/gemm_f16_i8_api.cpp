@@ -13,16 +13,16 @@
 namespace gemm_f16_impl {
 
 const I8Config kI8Configs[kNumI8Configs] = {
-    {"i8_16x16", 16, 16, 8, 0, 4, 1.29f, 2.8f, 1.3f, 5.5f},
-    {"i8_32x32_s8", 32, 32, 4, 8, 2, 0.093f, 3.8f, 0.28f, 4.7f},
-    {"i8_32x64_s6", 32, 64, 4, 6, 2, 0.148f, 4.1f, 0.17f, 4.3f},
-    {"i8_64x64_s6", 64, 64, 4, 6, 1, 0.233f, 3.6f, 0.27f, 3.5f},
-    {"i8_64x128_s4", 64, 128, 4, 4, 1, 0.348f, 3.9f, 0.32f, 3.9f},
-    {"i8_64x256_s3", 64, 256, 4, 3, 1, 0.60f, 4.9f, 0.62f, 3.9f},
-    {"i8_128x128_s4", 128, 128, 4, 4, 1, 0.494f, 4.9f, 0.46f, 5.0f},
-    {"i8_128x256_s3", 128, 256, 4, 3, 1, 0.69f, 7.3f, 0.72f, 6.3f},
-    {"i8_256x128_s3", 256, 128, 4, 3, 1, 0.652f, 7.3f, 0.74f, 6.2f},
-    {"i8_256x256_s2", 256, 256, 4, 2, 1, 1.258f, 10.0f, 1.0f, 9.5f},
+    {"i8_16x16", 16, 16, 8, 0, 4, 1.3f, 2.2f, 1.0f, 4.5f},
+    {"i8_32x32_s8", 32, 32, 4, 8, 2, 0.099f, 3.7f, 0.28f, 5.2f},
+    {"i8_32x64_s6", 32, 64, 4, 6, 2, 0.156f, 3.7f, 0.17f, 4.2f},
+    {"i8_64x64_s6", 64, 64, 8, 6, 1, 0.228f, 3.7f, 0.31f, 3.6f},
+    {"i8_64x128_s4", 64, 128, 8, 4, 1, 0.353f, 3.7f, 0.38f, 3.8f},
+    {"i8_64x256_s3", 64, 256, 8, 3, 1, 0.542f, 4.6f, 0.71f, 3.6f},
+    {"i8_128x128_s4", 128, 128, 8, 4, 1, 0.495f, 4.6f, 0.5f, 4.6f},
+    {"i8_128x256_s3", 128, 256, 8, 3, 1, 0.766f, 4.9f, 0.74f, 5.2f},
+    {"i8_256x128_s3", 256, 128, 4, 3, 1, 0.736f, 6.0f, 0.69f, 6.7f},
+    {"i8_256x256_s2", 256, 256, 8, 2, 1, 1.25f, 7.2f, 1.3f, 8.6f},
 };
 
 namespace {
@@ -89,37 +89,42 @@ void describe(int c, gemm_f16_plan_t *p)
 // operands from the L2s if that is longer, and a split's partial sums and second
 // launch.  The configurations' constants and the rates below were fitted to what
 // 731 shapes (M 1 to 4096, N 256 to 28672, K 512 to 16384) took in every
-// configuration and split, so that the choice comes out right: it took 2 %
-// longer than the best one on average, 37 % at most (16 x 5000 x 4096: 10.8, 7.9).
-// us of some choices and others: (1, 28672 x 8192) 16x16 44, 32x64 52; (64, 8192 x
-// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 256x128 31, 128x128
-// 41, 256x256 53; (8192, 8192 x 8192) 256x256 420, 256x128 455, 128x128 559.
+// configuration and split, not for the times but so that the choice comes out
+// right: it took 2 % longer than the best one on average, a quarter at most but for
+// a few shapes.  (The kernel for few rows keeps a CU's loads busy by itself, so
+// where some CUs have two of its workgroups and the others one, it is half as fast:
+// (16, 5000 x 4096) 10.8 us, 32x32 7.9.)  us of some choices and others: (1, 28672 x
+// 8192) 16x16 44, 32x64 52; (32, 8192 x 8192) 32x64 20, 32x32 16, 64x64 21; (64, 8192 x
+// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 256x128 31, 128x128 40,
+// 256x256 49; (8192, 8192 x 8192) 256x256 414, 256x128 455, 128x128 559.
 double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
 {
     const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n) * splits;
     const int64_t step_k = d.stages > 0 ? kI8BlockK : 8 * kI8StreamK;
     const double fixed = d.fixed, steps = (double)ceil_div(ceil_div(K, splits), step_k);
-    const double rounds = (double)ceil_div(tiles, 256 * d.resident);
-    const double memory = ((double)N * K + 2.0 * M * N) / 13.2e6 +
-                          (double)tiles * ceil_div(K, splits) * (double)(std::min<int64_t>(d.block_m, M) + d.block_n) / 18.4e6;
-    return std::max(rounds * (fixed + steps * d.step), fixed + memory) + (splits > 1 ? 2.9 + 8.0 * M * N * splits / 8.4e6 : 0.0);
+    double rounds = (double)ceil_div(tiles, 256 * d.resident);
+    if (d.stages == 0 && tiles > 256 && tiles < 448)
+        rounds = 1.5;
+    const double memory = ((double)N * K + 2.0 * M * N) / 16e6 +
+                          (double)tiles * ceil_div(K, splits) * (double)(std::min<int64_t>(d.block_m, M) + d.block_n) / 20e6;
+    return std::max(rounds * (fixed + steps * d.step), fixed + memory) + (splits > 1 ? 2.7 + 8.0 * M * N * splits / 5.2e6 : 0.0);
 }
 
 // The same over experts, of which only the number of pairs is known here: as
 // many experts as may be have an equal share, in tiles of which the last is half
-// full, and an uneven load fills a third of a round more.  Fitted to 186 loads (8 to
-// 256 experts, 1 to 4096 tokens, 2 or 8 experts each, some experts more popular): 3 %
+// full, and an uneven load fills a quarter of a round more.  Fitted to 186 loads (8 to
+// 256 experts, 1 to 4096 tokens, 2 or 8 experts each, some experts more popular): 2 %
 // longer than the best on average.  us: 64 tokens, 8 of 256 experts of 4096 x 2048
-// 64x256 243, 32x64 315, 128x128 284; 2048 tokens, 8 of 64 of 2048 x 4096 256x256
-// 190, 128x256 195, 128x128 253; 1 token, 8 of 256 of 2048 x 4096 32x64 15.2, 64x256 20.6.
+// 64x256 241, 32x64 325, 128x128 284; 2048 tokens, 8 of 64 of 2048 x 4096 256x256
+// 184, 128x256 195, 128x128 252; 1 token, 8 of 256 of 2048 x 4096 32x64 15.2, 64x256 19.7.
 double estimate_experts(const I8Config &d, int64_t pairs, int experts, int64_t N, int64_t K)
 {
     const double hit = (double)std::min<int64_t>(experts, pairs), rows = (double)pairs / hit;
     const double tiles = hit * std::max(1.0, rows / d.block_m + 0.5) * (double)ceil_div(N, d.block_n);
     const double fixed = d.experts_fixed, steps = (double)ceil_div(K, d.stages > 0 ? kI8BlockK : 8 * kI8StreamK);
-    const double memory = (hit * (double)N * (double)K + 2.0 * (double)pairs * (double)N) / 14e6 +
-                          tiles * (double)K * (std::min((double)d.block_m, rows) + d.block_n) / 16e6;
-    return std::max(std::max(1.0, tiles / (256.0 * d.resident) + 0.36) * (fixed + steps * d.experts_step), fixed + memory);
+    const double memory = (hit * (double)N * (double)K + 2.0 * (double)pairs * (double)N) / 12e6 +
+                          tiles * (double)K * (std::min((double)d.block_m, rows) + d.block_n) / 14e6;
+    return std::max(std::max(1.0, tiles / (256.0 * d.resident) + 0.25) * (fixed + steps * d.experts_step), fixed + memory);
 }
 
 // Choices that this thread made last, so that a program that repeats its shapes

@@ -26,7 +26,7 @@ namespace {
 // over them would move the accumulator out of the matrix unit's registers.
 enum { kStaged, kPartial, kPieces };
 
-template <int BM, int BN, int WM, int WN, int STAGES, int PARTS, int OUT, bool EXPERTS>
+template <int BM, int BN, int WM, int WN, int STAGES, int OUT, bool EXPERTS>
 __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
 i8_tile_kernel(I8Args p)
 {
@@ -142,10 +142,9 @@ i8_tile_kernel(I8Args p)
                 __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);      // one global load
         }
     };
-    static_assert(PARTS == 1 || PARTS == 2, "a slice is requested in one or both half steps");
-    const auto issue = [&](int kt, half_t *a, half_t *b, int part, int parts) __attribute__((always_inline)) {
-        opa.issue(kt, a, wave, part, parts);
-        opb.issue(kt, b, wave, part, parts);
+    const auto issue = [&](int kt, half_t *a, half_t *b) __attribute__((always_inline)) {
+        opa.issue(kt, a, wave);
+        opb.issue(kt, b, wave);
     };
     // One slice, read from (rd_a, rd_b) while slice `next` is requested into
     // (wr_a, wr_b).  Fragments are read one 64-deep step ahead of their products:
@@ -153,17 +152,15 @@ i8_tile_kernel(I8Args p)
     Frags f0, f1 = {};
     const auto step = [&](auto first, const half_t *__restrict__ rd_a, const half_t *__restrict__ rd_b, half_t *__restrict__ wr_a,
                           half_t *__restrict__ wr_b, int next) __attribute__((always_inline)) {
-        issue(next, wr_a, wr_b, 0, PARTS);
+        issue(next, wr_a, wr_b);
         load_frags(f0, rd_a, rd_b, 0);
         if constexpr (!decltype(first)::value)
             mma(f1);
-        interleave(LOADS / PARTS);
+        interleave(LOADS);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (PARTS == 2)
-            issue(next, wr_a, wr_b, 1, PARTS);
         load_frags(f1, rd_a, rd_b, 1);
         mma(f0);
-        interleave(PARTS == 2 ? LOADS / PARTS : 0);
+        interleave(0);
         __builtin_amdgcn_sched_barrier(0);
     };
     // Slice kt has landed for every wave, and every wave is done with the stage
@@ -344,11 +341,11 @@ i8_tile_kernel(I8Args p)
 
 } // namespace
 
-template <int BM, int BN, int WM, int WN, int STAGES, int PARTS>
+template <int BM, int BN, int WM, int WN, int STAGES>
 static hipError_t launch_tile(const I8Args &a, int64_t grid, bool experts, hipStream_t s)
 {
 #define GEMM_F16_I8(OUT, EXPERTS)                                                                                        \
-    hipLaunchKernelGGL((i8_tile_kernel<BM, BN, WM, WN, STAGES, PARTS, OUT, EXPERTS>), dim3((unsigned)grid),             \
+    hipLaunchKernelGGL((i8_tile_kernel<BM, BN, WM, WN, STAGES, OUT, EXPERTS>), dim3((unsigned)grid),             \
                        dim3(64 * WM * WN), 0, s, a)
     if (experts && a.vec_c == 8)
         GEMM_F16_I8(kStaged, true);
@@ -370,15 +367,15 @@ static hipError_t launch_config(int config, const I8Args &a, int64_t grid, bool 
 {
     switch (config) {
     case 0: return launch_i8_stream(a, grid, experts, s);
-    case 1: return launch_tile<32, 32, 2, 2, 8, 1>(a, grid, experts, s);
-    case 2: return launch_tile<32, 64, 1, 4, 6, 1>(a, grid, experts, s);
-    case 3: return launch_tile<64, 64, 2, 2, 6, 1>(a, grid, experts, s);
-    case 4: return launch_tile<64, 128, 2, 2, 4, 1>(a, grid, experts, s);
-    case 5: return launch_tile<64, 256, 1, 4, 3, 1>(a, grid, experts, s);
-    case 6: return launch_tile<128, 128, 2, 2, 4, 1>(a, grid, experts, s);
-    case 7: return launch_tile<128, 256, 2, 2, 3, 1>(a, grid, experts, s);
-    case 8: return launch_tile<256, 128, 2, 2, 3, 1>(a, grid, experts, s);
-    case 9: return launch_tile<256, 256, 2, 2, 2, 2>(a, grid, experts, s);
+    case 1: return launch_tile<32, 32, 2, 2, 8>(a, grid, experts, s);
+    case 2: return launch_tile<32, 64, 1, 4, 6>(a, grid, experts, s);
+    case 3: return launch_tile<64, 64, 2, 4, 6>(a, grid, experts, s);
+    case 4: return launch_tile<64, 128, 2, 4, 4>(a, grid, experts, s);
+    case 5: return launch_tile<64, 256, 1, 8, 3>(a, grid, experts, s);
+    case 6: return launch_tile<128, 128, 2, 4, 4>(a, grid, experts, s);
+    case 7: return launch_tile<128, 256, 2, 4, 3>(a, grid, experts, s);
+    case 8: return launch_tile<256, 128, 2, 2, 3>(a, grid, experts, s);
+    case 9: return launch_tile<256, 256, 4, 2, 2>(a, grid, experts, s);
     default: return hipErrorInvalidValue;
     }
 }
