@@ -50,7 +50,14 @@ hipError_t launch_i8(int config, const I8Args &a, int64_t grid, hipStream_t)
     check_args(config, a, grid);
     const I8Config &d = kI8Configs[config];
     const int step = d.stages > 0 ? kI8BlockK : kI8StreamK;
-    CHECK(a.M > 0 && (int64_t)a.tiles_m * d.block_m >= a.M && grid == (int64_t)a.tiles_m * a.tiles_n * a.splits);
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    CHECK(a.M > 0 && (int64_t)a.tiles_m * d.block_m >= a.M);
+    if (d.block_m == 256 && d.block_n == 256 && a.splits == 1) {   // a last round in quarters, for all of its tiles
+        CHECK(a.uncut <= tiles && tiles - a.uncut <= kI8Cut && (a.uncut == tiles || a.uncut % 256 == 0));
+        CHECK(a.uncut == tiles ? grid == tiles : grid - a.uncut == 4 * 8 * ((tiles - a.uncut + 7) / 8));
+    } else {
+        CHECK(grid == tiles * a.splits);
+    }
     CHECK((int64_t)d.block_m * a.a_pitch < (int64_t)1 << 31);
     CHECK((a.splits > 1) == (a.partial != nullptr) && a.splits <= GEMM_F16_MAX_SPLITS);
     CHECK((int64_t)a.splits * a.k_split >= a.K && (a.K == 0 || (int64_t)(a.splits - 1) * a.k_split < a.K));
@@ -62,7 +69,12 @@ hipError_t launch_i8_experts(int config, const I8Args &a, int64_t grid, hipStrea
     check_args(config, a, grid);
     CHECK(a.order && a.starts && a.experts > 0 && a.pairs > 0 && a.pairs_per_row > 0 && a.splits == 1 && !a.partial && a.k_split >= a.K);
     CHECK((int64_t)a.M * a.pairs_per_row == a.pairs && (int64_t)a.M * a.a_pitch < (int64_t)1 << 31);
-    CHECK(grid == (int64_t)a.tiles_m * a.tiles_n && a.tiles_m <= a.pairs);
+    const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+    CHECK(a.tiles_m <= a.pairs);
+    if (kI8Configs[config].block_m == 256 && kI8Configs[config].block_n == 256)
+        CHECK(a.uncut >= tiles && a.uncut % 8 == 0 && grid - a.uncut >= 4 * std::min<int64_t>(tiles, kI8Cut) && (grid - a.uncut) % 32 == 0);
+    else
+        CHECK(grid == tiles);
     // loads of experts and none, one pair in every tile but one of them, fit the grid
     const int64_t bins = std::min<int64_t>(a.pairs, a.experts + 1), rows = kI8Configs[config].block_m;
     CHECK(bins - 1 + (a.pairs - (bins - 1) + rows - 1) / rows <= a.tiles_m);

@@ -91,6 +91,18 @@ def test_as_the_dense_product_bit_for_bit(config):
         assert torch.equal(got[:, 0], g.gemm_i8(a, g.I8Matrix(w.codes[e], w.scales[e], 300), alpha=0.3))
 
 
+@pytest.mark.parametrize("tokens,experts,n", [(2048, 4, 4100), (2000, 3, 4096), (3000, 5, 2056), (2300, 2, 3500)])
+def test_last_round_in_quarters(tokens, experts, n):
+    """More tiles of 256 x 256 than CUs: whatever the counts, the last round (and what is cut of it) misses no row."""
+    a, w = held((tokens,), 200, 3)[0], held((experts, n), 200, 4)[0]
+    for seed in range(6):
+        order = g.expert_order(torch.from_numpy(some_ids(tokens, 2, experts, seed, skew=seed % 2 == 1)).to(DEV), experts)
+        got, want = (torch.full((tokens, 2, n), 5.0, dtype=torch.float16, device=DEV) for _ in range(2))
+        g.gemm_i8_experts(a, w, order, out=got, config=g.i8_num_configs() - 1, alpha=0.3)
+        g.gemm_i8_experts(a, w, order, out=want, config=6, alpha=0.3)
+        assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("config", range(g.i8_num_configs()))
 def test_no_expert_and_empty(config):
     a, w = held((9,), 64, 3)[0], held((4, 40), 64, 4)[0]

@@ -66,6 +66,20 @@ def test_every_config_gives_the_same_bits(config):
             assert torch.equal(g.gemm_i8(a, w, config=config, splits=splits, alpha=0.3), want)
 
 
+@pytest.mark.parametrize("m,n", [(4200, 4096), (4100, 4104), (4100, 4100), (4353, 4301), (2100, 8000), (4096, 4096)])
+def test_last_round_in_quarters(m, n):
+    """More tiles of 256 x 256 than CUs by a few: the last ones are cut in four."""
+    last = g.i8_num_configs() - 1
+    p = g.plan_i8(m, n, 300, config=last)
+    assert p["block_m"] == p["block_n"] == 256
+    print(f"[i8] {m}x{n} tiles={p['tiles_m'] * p['tiles_n']} grid={p['grid']}", flush=True)
+    a, w = held(m, 300, 1)[0], held(n, 300, 2)[0]
+    room = torch.full((m * n + 128,), 9.0, dtype=torch.float16, device=DEV)
+    got = g.gemm_i8(a, w, config=last, alpha=0.3, epilogue="relu", out=room[64:-64].view(m, n))
+    assert torch.equal(got, g.gemm_i8(a, w, config=6, alpha=0.3, epilogue="relu"))
+    assert bool((room[:64] == 9).all()) and bool((room[-64:] == 9).all())
+
+
 @pytest.mark.parametrize("config", range(g.i8_num_configs()))
 def test_pitches_and_alignment(config):
     check(20, 40, 100, config=config, a_pitch=256, w_pitch=128)

@@ -84,6 +84,11 @@ void describe(int c, gemm_f16_plan_t *p)
                                 : d.waves * d.block_n * 64;
 }
 
+// Whether a configuration's last round may be cut into quarters of its tiles,
+// and the workgroups for those (eight tiles at a time, one for each XCD).
+bool cuts(const I8Config &d) { return d.block_m == 256 && d.block_n == 256; }
+int64_t quarters(int64_t tiles) { return 4 * 8 * ceil_div(tiles, 8); }
+
 // A product's time in us, for the choice of a configuration and split: rounds of
 // workgroups over 256 CUs, or the time to bring W from memory and the tiles'
 // operands from the L2s if that is longer, and a split's partial sums and second
@@ -103,6 +108,8 @@ double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
     const int64_t step_k = d.stages > 0 ? kI8BlockK : 8 * kI8StreamK;
     const double fixed = d.fixed, steps = (double)ceil_div(ceil_div(K, splits), step_k);
     double rounds = (double)ceil_div(tiles, 256 * d.resident);
+    if (cuts(d) && splits == 1 && tiles % 256 > 0 && tiles % 256 <= kI8Cut)
+        rounds += (tiles % 256 <= kI8Cut / 2 ? 0.45 : 0.9) - 1.0;   // one or two rounds of quarters
     if (d.stages == 0 && tiles > 256 && tiles < 448)
         rounds = 1.5;
     const double memory = ((double)N * K + 2.0 * M * N) / 16e6 +
@@ -207,7 +214,8 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
         return GEMM_F16_ERROR_UNSUPPORTED_SIZE;
     p->k_tiles = per;
     p->k_split = p->splits > 1 ? per * p->block_k : K;
-    p->grid = tiles * p->splits;
+    p->grid = cuts(d) && p->splits == 1 && tiles <= INT32_MAX ? i8_uncut((int)tiles) + quarters(tiles - i8_uncut((int)tiles))
+                                                              : tiles * p->splits;
     p->workspace_bytes = p->splits > 1 ? (int64_t)p->splits * M * N * 4 : 0;
     return launchable(p->grid, p->threads) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
 }
@@ -255,7 +263,8 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
     p->min_bytes = ((double)experts * (double)N + (double)(pairs / per_row)) * ((double)K + 4.0) + 2.0 * (double)pairs * (double)N;
     p->tiles_m = most_tiles(pairs, experts, d.block_m);
     p->tiles_n = ceil_div(N, d.block_n);
-    p->grid = p->tiles_m * p->tiles_n;
+    const int64_t tiles = p->tiles_m * p->tiles_n;
+    p->grid = cuts(d) ? ceil_div(tiles, 8) * 8 + quarters(std::min<int64_t>(tiles, kI8Cut)) : tiles;
     return launchable(p->grid, p->threads) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
 }
 
@@ -384,6 +393,8 @@ gemm_f16_status_t gemm_f16_i8(int64_t M, int64_t N, int64_t K, const void *A, in
     I8Args a = arguments(A, a_pitch, a_scales, W, w_pitch, w_scales, C, N, K, alpha, epilogue, plan);
     a.M = (int)M;
     a.partial = plan.splits > 1 ? (int *)workspace : nullptr;
+    if (cuts(kI8Configs[plan.config]))
+        a.uncut = i8_uncut(a.tiles_m * a.tiles_n);
     const hipError_t e = launch_i8(plan.config, a, plan.grid, (hipStream_t)stream);
     if (e != hipSuccess || plan.splits == 1)
         return status_of(e);
@@ -514,6 +525,8 @@ gemm_f16_status_t gemm_f16_i8_experts(int64_t pairs, int64_t pairs_per_row, int 
     a.experts = experts;
     a.pairs = (int)pairs;
     a.pairs_per_row = (int)pairs_per_row;
+    if (cuts(kI8Configs[plan.config]))
+        a.uncut = (int)(ceil_div(plan.tiles_m * plan.tiles_n, 8) * 8);
     return status_of(launch_i8_experts(plan.config, a, plan.grid, (hipStream_t)stream));
 }
 

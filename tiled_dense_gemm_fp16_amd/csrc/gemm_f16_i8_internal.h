@@ -28,6 +28,11 @@ constexpr int kI8StreamK = 256;      // k of a step of the kernel for few rows
 constexpr int kNumI8Configs = 10;
 extern const I8Config kI8Configs[kNumI8Configs];
 
+// The largest tile: where its last round over the 256 CUs has kI8Cut tiles or
+// fewer, those are cut into quarters of 128 x 128.  How many are not:
+constexpr int kI8Cut = 128;
+__host__ __device__ inline int i8_uncut(int tiles) { return tiles % 256 <= kI8Cut ? tiles - tiles % 256 : tiles; }
+
 struct I8Args {
     const int8_t *A, *W;
     const float *a_scales, *w_scales;
@@ -37,6 +42,7 @@ struct I8Args {
     int M, N, K;           // M rows of A; K rounded up to a multiple of 16
     int tiles_m, tiles_n;  // (experts: tiles_m is what the grid has room for)
     int splits, k_split;   // k of a split, a multiple of the configuration's step; >= K unless split
+    int uncut;             // the largest tile: its workgroups for whole tiles, those behind are for quarters of tiles
     float alpha;
     int relu;
     int vec_c;             // 8: C's rows take 16-byte stores; 4: 8-byte; 1: 2-byte

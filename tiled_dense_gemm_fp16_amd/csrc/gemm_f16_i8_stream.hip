@@ -32,20 +32,21 @@ __global__ void __launch_bounds__(64 * kWaves) i8_stream_kernel(I8Args p)
     const float *w_scales = p.w_scales;
     int pair, row;   // of lane i's row of A; -1: none
     if constexpr (EXPERTS) {
-        if (!i8_find_tile<16>(p, blockIdx.x, lane, t))
+        bool quarter;
+        if (!i8_find_tile<16, 16 * NB, false>(p, blockIdx.x, lane, t, quarter))
             return;
         pair = i8_pair(p, t, i);
         row = pair < 0 ? -1 : pair / p.pairs_per_row;
         W += (int64_t)t.expert * p.N * p.w_pitch;
         w_scales += (int64_t)t.expert * p.N;
     } else {
-        t.tn = blockIdx.x % p.tiles_n;
-        t.tm = blockIdx.x / p.tiles_n % p.tiles_m;
-        t.rows = min(16, p.M - 16 * t.tm);
-        row = i < t.rows ? 16 * t.tm + i : -1;
+        t.n0 = blockIdx.x % p.tiles_n * (16 * NB);
+        t.first = blockIdx.x / p.tiles_n % p.tiles_m * 16;
+        t.rows = min(16, p.M - t.first);
+        row = i < t.rows ? t.first + i : -1;
         pair = row;
     }
-    const int n0 = t.tn * 16 * NB;
+    const int n0 = t.n0;
     const int split = EXPERTS ? 0 : blockIdx.x / p.tiles_n / p.tiles_m;
     const int k_begin = split * p.k_split, k_end = min(p.K, k_begin + p.k_split);
     const bool none = EXPERTS && t.expert >= p.experts;   // pairs of no expert: zeros
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(64 * kWaves) i8_stream_kernel(I8Args p)
         // (experts: all of A, less than 2^31 bytes)
         const __amdgpu_buffer_rsrc_t a =
             EXPERTS ? make_rsrc(p.A, (uint32_t)p.M * (uint32_t)p.a_pitch)
-                    : make_rsrc(p.A + (int64_t)(16 * t.tm) * p.a_pitch, (uint32_t)t.rows * (uint32_t)p.a_pitch);
+                    : make_rsrc(p.A + (int64_t)t.first * p.a_pitch, (uint32_t)t.rows * (uint32_t)p.a_pitch);
         const uint32_t a_off = row < 0 ? 0x80000000u
                                        : (uint32_t)(EXPERTS ? row : i) * (uint32_t)p.a_pitch + 16u * g;
         const uint32_t w_off = (uint32_t)i * (uint32_t)p.w_pitch + 16u * g;

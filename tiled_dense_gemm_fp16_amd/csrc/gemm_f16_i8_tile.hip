@@ -26,9 +26,20 @@ namespace {
 // over them would move the accumulator out of the matrix unit's registers.
 enum { kStaged, kPartial, kPieces };
 
+// Words behind the stages, and all of a tile's LDS in halves.
+template <int BM, int BN, int STAGES, int OUT, bool EXPERTS>
+struct I8Lds {
+    static constexpr int STAGE_HALVES = STAGES * (BM + BN) * (kI8BlockK / 2), OUT_HALVES = OUT == kStaged ? BM * BN : 0;
+    static constexpr int TABLE_AT = STAGE_HALVES > OUT_HALVES ? STAGE_HALVES : OUT_HALVES;
+    static constexpr int HALVES = TABLE_AT + 2 * ((EXPERTS ? 2 * BM : BM) + BN);
+    static_assert(HALVES * 2 <= 163840, "LDS budget");
+};
+
+// A tile of C, or of a split's sums.  (lds is one array: with several, the compiler
+// no longer sees that the loads into one stage leave the others alone, and waits
+// for them before every read: 8192^3 425 us, 628 so.)
 template <int BM, int BN, int WM, int WN, int STAGES, int OUT, bool EXPERTS>
-__global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
-i8_tile_kernel(I8Args p)
+__device__ __forceinline__ void i8_tile(const I8Args &p, half_t *lds, const I8Tile &t, int split)
 {
     constexpr int WAVES = WM * WN, THREADS = 64 * WAVES;
     constexpr int BK = kI8BlockK / 2;                     // of a slice, as pairs of codes
@@ -36,40 +47,27 @@ i8_tile_kernel(I8Args p)
     using Op_a = Operand<true, BM, BK, THREADS, true, 8, true>;
     using Op_b = Operand<true, BN, BK, THREADS, true, 8, true>;
     constexpr int A_STAGE = Op_a::STAGE, B_STAGE = Op_b::STAGE, LOADS = Op_a::LOADS + Op_b::LOADS;
-    constexpr int STAGE_HALVES = STAGES * (A_STAGE + B_STAGE), OUT_HALVES = OUT == kStaged ? BM * BN : 0;
-    constexpr int LDS_HALVES = STAGE_HALVES > OUT_HALVES ? STAGE_HALVES : OUT_HALVES;
-    constexpr int TABLE = (EXPERTS ? 2 * BM : BM) + BN;   // words behind the stages
-    static_assert(LDS_HALVES * 2 + TABLE * 4 <= 163840, "LDS budget");
-    // (One array: with several, the compiler no longer sees that the loads into
-    // one stage leave the others alone, and waits for them before every read:
-    // 8192^3 425 us, 628 so.)
-    __shared__ __attribute__((aligned(1024))) half_t lds[LDS_HALVES + 2 * TABLE];
-    float *const column_scale = reinterpret_cast<float *>(lds + LDS_HALVES), *const row_factor = column_scale + BN;
-    int *const pairs = reinterpret_cast<int *>(row_factor + BM);   // experts
     half_t *const As = lds, *const Bs = lds + STAGES * A_STAGE;
+    float *const column_scale = reinterpret_cast<float *>(lds + I8Lds<BM, BN, STAGES, OUT, EXPERTS>::TABLE_AT);
+    float *const row_factor = column_scale + BN;
+    int *const pairs = reinterpret_cast<int *>(row_factor + BM);   // experts
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm0 = (wave / WN) * (BM / WM), wn0 = (wave % WN) * (BN / WN);
 
     constexpr int MINE = (BM + THREADS - 1) / THREADS;   // rows tid, tid + THREADS, ... of the tile
-    int m0 = 0, n0, rows, split = 0, my_pair[MINE], my_row[MINE];
+    const int n0 = t.n0, rows = t.rows, m0 = EXPERTS ? 0 : t.first;
+    int my_pair[MINE], my_row[MINE];
     const int8_t *W = p.W;
     const float *w_scales = p.w_scales;
-    bool none = false;
     if constexpr (EXPERTS) {
-        I8Tile t;
-        if (!i8_find_tile<BM>(p, blockIdx.x, lane, t))
-            return;
-        rows = t.rows;
-        n0 = t.tn * BN;
 #pragma unroll
         for (int i = 0; i < MINE; ++i)
             my_pair[i] = i8_pair(p, t, tid + i * THREADS);
-        none = t.expert >= p.experts;
         W += (int64_t)t.expert * p.N * p.w_pitch;
         w_scales += (int64_t)t.expert * p.N;
-        if (none) {   // pairs of no expert: zeros
+        if (t.expert >= p.experts) {   // pairs of no expert: zeros
 #pragma unroll
             for (int i = 0; i < MINE; ++i)
                 if (tid + i * THREADS < BM)
@@ -84,12 +82,6 @@ i8_tile_kernel(I8Args p)
             }
             return;
         }
-    } else {
-        int tm, tn;
-        tile_coords(blockIdx.x, gridDim.x, p.tiles_m, p.tiles_n, 4, tm, tn, split);
-        m0 = tm * BM;
-        n0 = tn * BN;
-        rows = min(BM, p.M - m0);
     }
 
     const int k_begin = split * p.k_split, k_end = min(p.K, k_begin + p.k_split);
@@ -339,24 +331,78 @@ i8_tile_kernel(I8Args p)
     }
 }
 
+// CUT: the tiles of a last round that does not fill the card may be cut into
+// quarters of BM / 2 by BN / 2, by as many waves with twice the stages, so that
+// every CU has one.
+template <int BM, int BN, int WM, int WN, int STAGES, int OUT, bool EXPERTS, bool CUT>
+__global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+i8_tile_kernel(I8Args p)
+{
+    using Whole = I8Lds<BM, BN, STAGES, OUT, EXPERTS>;
+    using Quarter = I8Lds<BM / 2, BN / 2, 2 * STAGES, OUT, EXPERTS>;
+    constexpr int HALVES = CUT && Quarter::HALVES > Whole::HALVES ? Quarter::HALVES : Whole::HALVES;
+    __shared__ __attribute__((aligned(1024))) half_t lds[HALVES];
+    I8Tile t;
+    bool quarter = false;
+    int split = 0;
+    if constexpr (EXPERTS) {
+        if (!i8_find_tile<BM, BN, CUT>(p, blockIdx.x, threadIdx.x & 63, t, quarter))
+            return;
+    } else {
+        const int tiles = p.tiles_m * p.tiles_n;
+        int id, tm, tn, part = 0;
+        quarter = CUT && (int)blockIdx.x >= p.uncut;
+        if (quarter) {   // the quarters of a tile to one XCD
+            const int w = (int)blockIdx.x - p.uncut;
+            id = p.uncut + w % 8 + w / 32 * 8;
+            part = w / 8 % 4;
+            if (id >= tiles)
+                return;
+        } else {
+            id = i8_place(blockIdx.x, CUT ? p.uncut : (int)gridDim.x);
+            split = id / tiles;
+            id -= split * tiles;
+        }
+        i8_walk(id, p.tiles_m, p.tiles_n, tm, tn);
+        t.first = tm * BM + part / 2 * (BM / 2);
+        t.n0 = tn * BN + part % 2 * (BN / 2);
+        t.rows = min(quarter ? BM / 2 : BM, p.M - t.first);
+        t.expert = 0;
+        if (t.rows <= 0 || t.n0 >= p.N)
+            return;
+    }
+    if constexpr (CUT) {
+        if (quarter) {
+            i8_tile<BM / 2, BN / 2, WN, WM, 2 * STAGES, OUT, EXPERTS>(p, lds, t, split);
+            return;
+        }
+    }
+    i8_tile<BM, BN, WM, WN, STAGES, OUT, EXPERTS>(p, lds, t, split);
+}
+
 } // namespace
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int WM, int WN, int STAGES, bool CUT = false>
 static hipError_t launch_tile(const I8Args &a, int64_t grid, bool experts, hipStream_t s)
 {
-#define GEMM_F16_I8(OUT, EXPERTS)                                                                                        \
-    hipLaunchKernelGGL((i8_tile_kernel<BM, BN, WM, WN, STAGES, OUT, EXPERTS>), dim3((unsigned)grid),             \
+#define GEMM_F16_I8(OUT, EXPERTS, CUT_)                                                                                  \
+    hipLaunchKernelGGL((i8_tile_kernel<BM, BN, WM, WN, STAGES, OUT, EXPERTS, CUT_>), dim3((unsigned)grid),              \
                        dim3(64 * WM * WN), 0, s, a)
+    const bool cut = CUT && a.uncut < grid;
     if (experts && a.vec_c == 8)
-        GEMM_F16_I8(kStaged, true);
+        GEMM_F16_I8(kStaged, true, CUT);
     else if (experts)
-        GEMM_F16_I8(kPieces, true);
+        GEMM_F16_I8(kPieces, true, CUT);
     else if (a.partial)
-        GEMM_F16_I8(kPartial, false);
+        GEMM_F16_I8(kPartial, false, false);
+    else if (a.vec_c == 8 && cut)
+        GEMM_F16_I8(kStaged, false, CUT);
     else if (a.vec_c == 8)
-        GEMM_F16_I8(kStaged, false);
+        GEMM_F16_I8(kStaged, false, false);
+    else if (cut)
+        GEMM_F16_I8(kPieces, false, CUT);
     else
-        GEMM_F16_I8(kPieces, false);
+        GEMM_F16_I8(kPieces, false, false);
 #undef GEMM_F16_I8
     return hipGetLastError();
 }
@@ -375,7 +421,7 @@ static hipError_t launch_config(int config, const I8Args &a, int64_t grid, bool 
     case 6: return launch_tile<128, 128, 2, 4, 4>(a, grid, experts, s);
     case 7: return launch_tile<128, 256, 2, 4, 3>(a, grid, experts, s);
     case 8: return launch_tile<256, 128, 2, 2, 3>(a, grid, experts, s);
-    case 9: return launch_tile<256, 256, 4, 2, 2>(a, grid, experts, s);
+    case 9: return launch_tile<256, 256, 4, 2, 2, true>(a, grid, experts, s);
     default: return hipErrorInvalidValue;
     }
 }
