@@ -33,9 +33,10 @@ SPARSE_METRIC = ("2:4-sparse fp16 GEMM TFLOP/s at 1 MI355X (2 flop per product o
                  "M N K per call) and % of dense FP16 MFMA peak")
 PROFILES = os.path.join(ROOT, "profiles")
 CSRC = os.path.join(ROOT, "tiled_dense_gemm_fp16_amd", "csrc")
-# what the timed products are built from (not the probe, nor the 4-bit operators)
+# what the timed products are built from (not the probe, nor the 4-bit and 8-bit operators and the Python modules)
+OTHER_SOURCES = ("mfma_probe", "gemm_f16_q4", "q4_", "gemm_f16_i8", "i8_", "gemm_f16_route", "binding")
 KERNEL_SOURCES = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
-                        if f.endswith((".hip", ".h", ".cpp")) and not f.startswith(("mfma_probe", "gemm_f16_q4", "q4_")))
+                        if f.endswith((".hip", ".h", ".cpp")) and not f.startswith(OTHER_SOURCES))
 
 
 def kernel_source_hash() -> str:

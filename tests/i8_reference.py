@@ -42,7 +42,7 @@ def near(got, want):
     over = np.abs(want) >= 65520 * (1 + 2.0 ** -22)
     edge = (np.abs(want) >= 65504) & ~over          # either the largest number or infinity
     fine = np.abs(got - want) <= bound(want)
-    return np.where(over, got == np.sign(want) * np.inf, fine | (edge & (np.abs(got) >= 65504) & (np.sign(got) == np.sign(want))))
+    return np.where(over, got == np.copysign(np.inf, want), fine | (edge & (np.abs(got) >= 65504) & (np.sign(got) == np.sign(want))))
 
 
 def scores(logits, bias, kind):
