@@ -11,6 +11,16 @@
 // Sums are int32 and exact.  The product is computed transposed (W's fragment
 // first), so a lane holds four neighbouring columns of one row of C.
 //
+// Tiles of 64 rows and more are computed by eight waves, two for each SIMD: their
+// waits for loads overlap (four waves: 4096^3 58.8 us, eight 56.6; 64 tokens over 256
+// experts 261, 241); 256 x 128 keeps four (1000 x 5000 x 4100 39.7 us, 41.7).  At
+// 8192^3 (411 us, 2670 TOP/s; a library product reaches 2000) the matrix cores are busy
+// 0.68 of the cycles and the clock falls to 1.8 GHz; smaller and colder products
+// wait for memory (1000 x 5000 x 4100 busy 0.52, waves wait 0.29 of theirs; 2048 tokens
+// over 64 experts 0.52, 0.44).  Slices of 64 bytes, of which twice as many are in
+// flight, lose (4096^3 68 us; 2048 tokens 231, 194): half a cache line a row, and two
+// barriers for one.
+//
 // Experts: a tile's rows of A are those of up to BM pairs of one expert, each
 // fetched from where its row is (a direct load takes an address of its own
 // for every 16 bytes anyway), and its rows of C go where their pairs are.
