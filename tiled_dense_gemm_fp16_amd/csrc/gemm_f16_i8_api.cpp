@@ -99,9 +99,9 @@ int64_t quarters(int64_t tiles) { return 4 * 8 * ceil_div(tiles, 8); }
 // a few shapes.  (The kernel for few rows keeps a CU's loads busy by itself, so
 // where some CUs have two of its workgroups and the others one, it is half as fast:
 // (16, 5000 x 4096) 10.8 us, 32x32 7.9.)  us of some choices and others: (1, 28672 x
-// 8192) 16x16 44, 32x64 52; (32, 8192 x 8192) 32x64 20, 32x32 16, 64x64 21; (64, 8192 x
+// 8192) 16x16 41, 32x64 52; (32, 8192 x 8192) 32x64 20, 32x32 16, 64x64 21; (64, 8192 x
 // 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 256x128 31, 128x128 40,
-// 256x256 49; (8192, 8192 x 8192) 256x256 414, 256x128 455, 128x128 559.
+// 256x256 49; (8192, 8192 x 8192) 256x256 411, 256x128 455, 128x128 559.
 double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
 {
     const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n) * splits;
