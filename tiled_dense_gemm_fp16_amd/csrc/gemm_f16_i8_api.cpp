@@ -20,6 +20,7 @@ const I8Config kI8Configs[kNumI8Configs] = {
     {"i8_64x128_s4", 64, 128, 8, 4, 1, 0.353f, 3.7f, 0.38f, 3.8f},
     {"i8_64x256_s3", 64, 256, 8, 3, 1, 0.542f, 4.6f, 0.71f, 3.6f},
     {"i8_128x128_s4", 128, 128, 8, 4, 1, 0.495f, 4.6f, 0.5f, 4.6f},
+    {"i8_128x192_s3", 128, 192, 8, 3, 1, 0.62f, 5.0f, 0.66f, 6.2f},
     {"i8_128x256_s3", 128, 256, 8, 3, 1, 0.766f, 4.9f, 0.74f, 5.2f},
     {"i8_256x128_s3", 256, 128, 4, 3, 1, 0.736f, 6.0f, 0.69f, 6.7f},
     {"i8_256x256_s2", 256, 256, 8, 2, 1, 1.25f, 7.2f, 1.3f, 8.6f},
@@ -100,8 +101,8 @@ int64_t quarters(int64_t tiles) { return 4 * 8 * ceil_div(tiles, 8); }
 // where some CUs have two of its workgroups and the others one, it is half as fast:
 // (16, 5000 x 4096) 10.8 us, 32x32 7.9.)  us of some choices and others: (1, 28672 x
 // 8192) 16x16 41, 32x64 52; (32, 8192 x 8192) 32x64 20, 32x32 16, 64x64 21; (64, 8192 x
-// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 256x128 31, 128x128 40,
-// 256x256 49; (8192, 8192 x 8192) 256x256 411, 256x128 455, 128x128 559.
+// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 128x192 27, 128x256 30,
+// 128x128 39, 256x256 40; (8192, 8192 x 8192) 256x256 411, 256x128 455, 128x128 559.
 double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
 {
     const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n) * splits;

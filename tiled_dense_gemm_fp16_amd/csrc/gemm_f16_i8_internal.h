@@ -25,7 +25,7 @@ struct I8Config {
 };
 constexpr int kI8BlockK = 128;       // k of a tile's step
 constexpr int kI8StreamK = 256;      // k of a step of the kernel for few rows
-constexpr int kNumI8Configs = 10;
+constexpr int kNumI8Configs = 11;
 extern const I8Config kI8Configs[kNumI8Configs];
 
 // The largest tile: where its last round over the 256 CUs has kI8Cut tiles or

@@ -16,10 +16,13 @@
 // experts 261, 241); 256 x 128 keeps four (1000 x 5000 x 4100 39.7 us, 41.7).  At
 // 8192^3 (411 us, 2670 TOP/s; a library product reaches 2000) the matrix cores are busy
 // 0.68 of the cycles and the clock falls to 1.8 GHz; smaller and colder products
-// wait for memory (1000 x 5000 x 4100 busy 0.52, waves wait 0.29 of theirs; 2048 tokens
+// wait for memory (1000 x 5000 x 4100 busy 0.46, waves wait 0.32 of theirs; 2048 tokens
 // over 64 experts 0.52, 0.44).  Slices of 64 bytes, of which twice as many are in
 // flight, lose (4096^3 68 us; 2048 tokens 231, 194): half a cache line a row, and two
 // barriers for one.
+//
+// 192 columns are there for products whose tiles of 256 leave CUs idle (1000 x 5000 x
+// 4100 28 us in 216 workgroups, 32 in 160; 512 x 5000 x 8192 36, 38).
 //
 // Experts: a tile's rows of A are those of up to BM pairs of one expert, each
 // fetched from where its row is (a direct load takes an address of its own
@@ -288,7 +291,8 @@ __device__ __forceinline__ void i8_tile(const I8Args &p, half_t *lds, const I8Ti
         };
         if constexpr (OUT == kStaged) {
             // [BM][BN] in LDS, 8-byte units XOR-ed by row as in gemm_f16_tile.h
-            constexpr int UNITS = BN / 4, UMASK = (UNITS < 32 ? UNITS : 32) - 1;
+            // (within the largest power of two, up to 32, of which a row has a multiple)
+            constexpr int UNITS = BN / 4, UMASK = (UNITS % 32 == 0 ? 32 : UNITS % 16 == 0 ? 16 : 8) - 1;
             wait_lgkm0();
             __builtin_amdgcn_s_barrier();   // every wave is done with the stages
 #pragma unroll
@@ -429,9 +433,10 @@ static hipError_t launch_config(int config, const I8Args &a, int64_t grid, bool 
     case 4: return launch_tile<64, 128, 2, 4, 4>(a, grid, experts, s);
     case 5: return launch_tile<64, 256, 1, 8, 3>(a, grid, experts, s);
     case 6: return launch_tile<128, 128, 2, 4, 4>(a, grid, experts, s);
-    case 7: return launch_tile<128, 256, 2, 4, 3>(a, grid, experts, s);
-    case 8: return launch_tile<256, 128, 2, 2, 3>(a, grid, experts, s);
-    case 9: return launch_tile<256, 256, 4, 2, 2, true>(a, grid, experts, s);
+    case 7: return launch_tile<128, 192, 2, 4, 3>(a, grid, experts, s);
+    case 8: return launch_tile<128, 256, 2, 4, 3>(a, grid, experts, s);
+    case 9: return launch_tile<256, 128, 2, 2, 3>(a, grid, experts, s);
+    case 10: return launch_tile<256, 256, 4, 2, 2, true>(a, grid, experts, s);
     default: return hipErrorInvalidValue;
     }
 }
