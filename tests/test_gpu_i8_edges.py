@@ -102,7 +102,7 @@ def test_offsets_beyond_32_bits():
     del w, got
     m, n = 70000, 40000
     a, w = g.I8Matrix(codes(m, 16), torch.ones(m, device=DEV), 16), g.I8Matrix(codes(n, 16), torch.full((n,), 1e-3, device=DEV), 16)
-    for config in (5, 9):
+    for config in (5, g.i8_num_configs() - 1):
         got = g.gemm_i8(a, w, config=config)
         at = slice(m - 260, m)
         want = ref.product(ref.host(a.codes[at]), np.ones(260, np.float32), ref.host(w.codes), np.full(n, 1e-3, np.float32))

@@ -161,3 +161,28 @@ def test_compressed_product_is_near_the_dense_one():
     xd, wd = x.double().numpy(), w.double().numpy()
     most = np.abs(xd).sum(1)[:, None] * dw.T + dx * np.abs(wd).sum(1)[None] + 1000 * dx * dw.T
     assert (np.abs(got - xd @ wd.T) <= most * (1 + 2.0 ** -20) + ref.bound(xd @ wd.T) + most * 2.0 ** -10).all()
+
+
+def test_splits_captured_and_replayed():
+    """Two captured products with workspaces of their own, replayed with eager ones of other inputs between."""
+    one, two = ((held(70, 2000, s), held(300, 2000, s + 1)) for s in (1, 3))
+    want = [g.gemm_i8(a[0], w[0], splits=4) for a, w in (one, two)]
+    (a, _, _), (w, _, _) = one
+    codes, scales = a.codes.clone(), a.scales.clone()
+    mine, s, graphs = g.I8Matrix(codes, scales, a.k), torch.cuda.Stream(), []
+    for config in (3, 6):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            out = g.gemm_i8(mine, w, splits=4, config=config)
+        graphs.append((graph, out))
+    other = g.gemm_i8(two[0][0], w, splits=4)
+    for i in range(6):
+        now = (one, two)[i % 2][0][0]
+        codes.copy_(now.codes)
+        scales.copy_(now.scales)
+        for graph, out in graphs:
+            out.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, other if i % 2 else want[0])
+            assert torch.equal(g.gemm_i8(two[0][0], two[1][0], splits=4), want[1])
