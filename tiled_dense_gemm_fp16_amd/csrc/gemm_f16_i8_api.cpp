@@ -67,7 +67,7 @@ int vec_of(const void *C, int64_t N)
     return N % 8 == 0 && (uintptr_t)C % 16 == 0 ? 8 : N % 4 == 0 && (uintptr_t)C % 8 == 0 ? 4 : 1;
 }
 
-void describe(int c, gemm_f16_plan_t *p)
+void describe(int c, bool experts, gemm_f16_plan_t *p)
 {
     const I8Config &d = kI8Configs[c];
     memset(p, 0, sizeof(*p));
@@ -81,8 +81,7 @@ void describe(int c, gemm_f16_plan_t *p)
     p->vec_a = p->vec_b = 16;
     p->vec_c = 8;
     p->trans_b = 1;
-    p->lds_bytes = d.stages > 0 ? std::max<int64_t>(d.stages * (d.block_m + d.block_n) * kI8BlockK, 2 * d.block_m * d.block_n)
-                                : d.waves * d.block_n * 64;
+    p->lds_bytes = d.stages > 0 ? i8_lds_bytes(d.block_m, d.block_n, d.stages, experts) : d.waves * d.block_n * 64;
 }
 
 // Whether a configuration's last round may be cut into quarters of its tiles,
@@ -202,7 +201,7 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
         last.splits = splits;
     }
     const I8Config &d = kI8Configs[c];
-    describe(c, p);
+    describe(c, false, p);
     p->flops = 2.0 * (double)M * (double)N * (double)K;
     p->min_bytes = ((double)M + (double)N) * ((double)K + 4.0) + 2.0 * (double)M * (double)N;
     p->tiles_m = ceil_div(M, d.block_m);
@@ -256,7 +255,7 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
         last.config = c;
     }
     const I8Config &d = kI8Configs[c];
-    describe(c, p);
+    describe(c, true, p);
     p->splits = 1;
     p->k_split = K;
     p->k_tiles = ceil_div(K, p->block_k);

@@ -28,6 +28,14 @@ constexpr int kI8StreamK = 256;      // k of a step of the kernel for few rows
 constexpr int kNumI8Configs = 11;
 extern const I8Config kI8Configs[kNumI8Configs];
 
+// LDS of a workgroup that works in tiles: the stages, a factor for each row and a scale
+// for each column, and over experts each row's pair.  (A tile of C on its way out
+// fits into the stages, and the quarters of a tile take less than all of it.)
+constexpr int i8_lds_bytes(int block_m, int block_n, int stages, bool experts)
+{
+    return stages * (block_m + block_n) * kI8BlockK + 4 * ((experts ? 2 : 1) * block_m + block_n);
+}
+
 // The largest tile: where its last round over the 256 CUs has kI8Cut tiles or
 // fewer, those are cut into quarters of 128 x 128.  How many are not:
 constexpr int kI8Cut = 128;

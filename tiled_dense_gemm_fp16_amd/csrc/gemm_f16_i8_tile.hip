@@ -356,6 +356,7 @@ i8_tile_kernel(I8Args p)
     using Quarter = I8Lds<BM / 2, BN / 2, 2 * STAGES, OUT, EXPERTS>;
     constexpr int HALVES = CUT && Quarter::HALVES > Whole::HALVES ? Quarter::HALVES : Whole::HALVES;
     __shared__ __attribute__((aligned(1024))) half_t lds[HALVES];
+    static_assert(sizeof(lds) == i8_lds_bytes(BM, BN, STAGES, EXPERTS), "as planned");
     I8Tile t;
     bool quarter = false;
     int split = 0;
