@@ -72,8 +72,8 @@ gemm_f16_status_t gemm_f16_i8(int64_t M, int64_t N, int64_t K, const void *A, in
                               int config, int splits, void *workspace, int64_t workspace_bytes, void *stream);
 
 /* How that call would run (no HIP call).  block_k is the k of one step,
- * k_tiles the steps of a split; flops 2 M N K; min_bytes codes, scales and C
- * once. */
+ * k_tiles the steps of a split; vec_c is that of a 16-byte aligned C; flops
+ * 2 M N K; min_bytes codes, scales and C once. */
 gemm_f16_status_t gemm_f16_plan_i8(int64_t M, int64_t N, int64_t K, int config, int splits, gemm_f16_plan_t *plan);
 
 int gemm_f16_i8_num_configs(void);
@@ -146,7 +146,7 @@ gemm_f16_status_t gemm_f16_i8_experts(int64_t pairs, int64_t pairs_per_row, int 
                                       const int32_t *starts, void *C, float alpha, int epilogue, int config, void *stream);
 
 /* How that call would run (no HIP call): tiles_m and grid are upper bounds,
- * flops 2 pairs N K; min_bytes all experts' codes and scales, A and C once. */
+ * vec_c is that of a 16-byte aligned C, flops 2 pairs N K; min_bytes all experts' codes and scales, A and C once. */
 gemm_f16_status_t gemm_f16_plan_i8_experts(int64_t pairs, int64_t pairs_per_row, int experts, int64_t N, int64_t K,
                                            int config, gemm_f16_plan_t *plan);
 

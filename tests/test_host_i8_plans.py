@@ -27,3 +27,16 @@ def test_lds_bytes(config):
             assert p["lds_bytes"] == want and e["lds_bytes"] == want + 4 * bm <= 163840
         else:
             assert p["lds_bytes"] == e["lds_bytes"] == 8 * 64 * 16
+
+
+@pytest.mark.parametrize("config", range(g.i8_num_configs()))
+@pytest.mark.parametrize("n,vec", [(40, 8), (44, 4), (42, 1), (41, 1)])
+def test_vec_c(config, n, vec):
+    """Elements for each store of C, were it 16-byte aligned: rows of C start where N lets them.  A split's sum stores four
+    at most, and the kernel for few rows one at a time."""
+    whole = g.plan_i8(300, n, 4100, config=config)
+    assert whole["vec_c"] == (vec if whole["direct_lds"] else 1)
+    split = g.plan_i8(300, n, 4100, config=config, splits=4)
+    assert split["splits"] == 4 and split["vec_c"] == min(vec, 4)
+    experts = g.plan_i8_experts(600, 2, 16, n, 4100, config=config)
+    assert experts["vec_c"] == (vec if experts["direct_lds"] else 1)

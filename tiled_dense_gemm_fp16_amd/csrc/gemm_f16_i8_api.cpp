@@ -67,6 +67,14 @@ int vec_of(const void *C, int64_t N)
     return N % 8 == 0 && (uintptr_t)C % 16 == 0 ? 8 : N % 4 == 0 && (uintptr_t)C % 8 == 0 ? 4 : 1;
 }
 
+// Elements that a store of a 16-byte aligned C takes, for a plan: a split's sum
+// stores four at most, and the kernel for few rows one at a time.
+int planned_vec_c(const I8Config &d, int64_t N, int splits)
+{
+    const int most = splits > 1 ? 4 : d.stages > 0 ? 8 : 1;
+    return std::min(vec_of(nullptr, N), most);
+}
+
 void describe(int c, bool experts, gemm_f16_plan_t *p)
 {
     const I8Config &d = kI8Configs[c];
@@ -79,7 +87,6 @@ void describe(int c, bool experts, gemm_f16_plan_t *p)
     p->threads = 64 * d.waves;
     p->direct_lds = d.stages > 0;
     p->vec_a = p->vec_b = 16;
-    p->vec_c = 8;
     p->trans_b = 1;
     p->lds_bytes = d.stages > 0 ? i8_lds_bytes(d.block_m, d.block_n, d.stages, experts) : d.waves * d.block_n * 64;
 }
@@ -217,6 +224,7 @@ gemm_f16_status_t plan_product(int64_t M, int64_t N, int64_t K, int config, int 
     p->grid = cuts(d) && p->splits == 1 && tiles <= INT32_MAX ? i8_uncut((int)tiles) + quarters(tiles - i8_uncut((int)tiles))
                                                               : tiles * p->splits;
     p->workspace_bytes = p->splits > 1 ? (int64_t)p->splits * M * N * 4 : 0;
+    p->vec_c = planned_vec_c(d, N, p->splits);
     return launchable(p->grid, p->threads) ? GEMM_F16_SUCCESS : GEMM_F16_ERROR_UNSUPPORTED_SIZE;
 }
 
@@ -257,6 +265,7 @@ gemm_f16_status_t plan_experts(int64_t pairs, int64_t per_row, int experts, int6
     const I8Config &d = kI8Configs[c];
     describe(c, true, p);
     p->splits = 1;
+    p->vec_c = planned_vec_c(d, N, 1);
     p->k_split = K;
     p->k_tiles = ceil_div(K, p->block_k);
     p->flops = 2.0 * (double)pairs * (double)N * (double)K;
