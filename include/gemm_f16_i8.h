@@ -97,15 +97,18 @@ const char *gemm_f16_i8_config_name(int config);
 /*
  * Choose experts.  In 64 bits:
  *   score[e] = softmax over the token's experts, or sigmoid, of logit[e]
- *   key[e]   = score[e] + bias[e]   (bias NULL: the keys are in the logits' order)
+ *   key[e]   = score[e] + bias[e]
+ * (bias NULL: the keys are the scores in the logits' order, that is, experts
+ * whose scores round to the same number are compared by their logits).
  * An expert whose logit or bias is NaN or -inf is closed: its score is 0 and
  * it is never chosen.  A logit of +inf counts as the largest finite fp32.
  * With groups > 1 (it divides experts) the experts are `groups` blocks of
  * neighbours; the top_groups blocks with the largest sum of their two largest
- * keys (one: that one) stay, those of equal sums with the lowest indexes;
- * blocks without an open expert never do.  ids[token] are the top_k
- * experts with the largest keys among those left, the largest first, equals in
- * the order of their indexes; -1 from where there are no more.
+ * score + bias (one: that one; bias NULL: scores) stay, those of equal sums
+ * with the lowest indexes; blocks without an open expert never do.
+ * ids[token] are the top_k experts with the largest keys among those left, the
+ * largest first, equals in the order of their indexes; -1 from where there are
+ * no more.
  *   weights[token][slot] = scale score[ids]               (renormalise 0)
  *                          scale score[ids] / sum of the chosen scores (1)
  * rounded to fp32; 0 for the id -1 and where the sum is 0.

@@ -131,9 +131,11 @@ def route(logits, top_k: int, score: str = "softmax", bias=None, groups: int = 1
     first, equals in the order of their indexes.
 
     Scores are the softmax or sigmoid of the logits.  What is compared is
-    score + ``bias`` (float32, one for each expert), in 64 bits; with
-    ``groups`` blocks of experts only those of the ``top_groups`` blocks whose
-    two best experts have the largest sum take part.  Weights are the chosen
+    score + ``bias`` (float32, one for each expert), in 64 bits; without a
+    bias the logits, whose order is that of the scores also where these round
+    to the same number.  With ``groups`` blocks of experts only those of the
+    ``top_groups`` blocks whose two largest score + bias (score, without one)
+    have the largest sum take part.  Weights are the chosen
     experts' scores without bias, divided by their sum with ``renormalise``,
     times ``scale``.  An expert whose logit or bias is NaN or -inf is never
     chosen; where none is left the id is -1 and the weight 0."""
