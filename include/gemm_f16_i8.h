@@ -59,8 +59,8 @@ gemm_f16_status_t gemm_f16_i8_expand(int64_t rows, int64_t K, const void *codes,
  * binary16 row-major, 2-byte aligned, for A of M rows and W of N rows by K.
  * Sums are exact integers; a sum rounded to fp32 is multiplied by the fp32
  * product (alpha a_scales[m]) w_scales[n], then rounded once more to binary16.
- * (That product of scales has to be a finite fp32 number for a sum of 0 to
- * give 0.)  K = 0 writes +0.  Limits: M <= GEMM_F16_MAX_DIM, N <=
+ * (That product of scales has to be a finite fp32 number for a sum of 0, and
+ * so for K = 0, to give +0.)  Limits: M <= GEMM_F16_MAX_DIM, N <=
  * GEMM_F16_MAX_N, pitches <= GEMM_F16_MAX_K.
  *   config : GEMM_F16_CONFIG_AUTO or an index below gemm_f16_i8_num_configs();
  *            all give the same bits.
@@ -141,7 +141,8 @@ gemm_f16_status_t gemm_f16_expert_order(int64_t pairs, int experts, const int32_
  * order does not name are left as they were.
  *   order, starts : as gemm_f16_expert_order gives them (starts not decreasing).
  *   config : GEMM_F16_CONFIG_AUTO or an index below gemm_f16_i8_num_configs().
- * Limits as gemm_f16_i8, and A of less than 2^31 bytes.
+ * Limits as gemm_f16_i8, and A of less than 2^31 bytes (for more, call it for
+ * some of the tokens at a time, each time with their own order).
  */
 gemm_f16_status_t gemm_f16_i8_experts(int64_t pairs, int64_t pairs_per_row, int experts, int64_t N, int64_t K,
                                       const void *A, int64_t a_pitch, const float *a_scales, const void *W,

@@ -40,7 +40,8 @@ gemm_f16_status_t status_of(hipError_t e) { return e == hipSuccess ? GEMM_F16_SU
 int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
 
 // Rows that compress writes start on cache lines, but the shortest: 1000 x 5000 x
-// 4100 with rows of 4112 bytes 39.7 us, of 4224 31.7; 8192 x 8192 x 4100 292, 247.
+// 4100 with rows of 4112 bytes 39 us, of 4224 28.5 (operands that are still in a
+// cache 29, 25); 8192 x 8192 x 4100 247, 220.
 int64_t made_pitch(int64_t K) { return K <= 64 ? padded(K) : (K + 127) / 128 * 128; }
 
 // a * b without overflow, beyond kMostBytes where it is more (a, b not negative)
@@ -105,10 +106,13 @@ int64_t quarters(int64_t tiles) { return 4 * 8 * ceil_div(tiles, 8); }
 // right: it took 2 % longer than the best one on average, a quarter at most but for
 // a few shapes.  (The kernel for few rows keeps a CU's loads busy by itself, so
 // where some CUs have two of its workgroups and the others one, it is half as fast:
-// (16, 5000 x 4096) 10.8 us, 32x32 7.9.)  us of some choices and others: (1, 28672 x
-// 8192) 16x16 41, 32x64 52; (32, 8192 x 8192) 32x64 20, 32x32 16, 64x64 21; (64, 8192 x
-// 8192) 64x128 in 4 parts 20, whole 33; (1000, 5000 x 4096) 128x192 27, 128x256 30,
-// 128x128 39, 256x256 40; (8192, 8192 x 8192) 256x256 411, 256x128 455, 128x128 559.
+// (16, 5000 x 4096) 11.6 us, 32x32 9.3.)  us of some choices and others, weights from
+// memory: (1, 28672 x 8192) 16x16 43, 32x64 52; (1000, 5000 x 4096) 128x192 28, 128x256
+// 31, 256x128 32, 128x128 41, 256x256 42; (8192, 8192 x 8192) 256x256 420, 256x128 459,
+// 128x256 464, 128x128 570.  Where the choice depends on whether the weights are still
+// in a cache, it is the best one if they are: (64, 8192 x 8192) 32x64 14.3, 64x128 in 4
+// parts 17.7, but from memory 23 and 21; (32, 8192 x 8192) 32x64 14.1, from memory 24
+// (32x32 19).
 double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
 {
     const int64_t tiles = ceil_div(M, d.block_m) * ceil_div(N, d.block_n) * splits;
@@ -129,8 +133,9 @@ double estimate(const I8Config &d, int64_t M, int64_t N, int64_t K, int splits)
 // full, and an uneven load fills a quarter of a round more.  Fitted to 186 loads (8 to
 // 256 experts, 1 to 4096 tokens, 2 or 8 experts each, some experts more popular): 2 %
 // longer than the best on average.  us: 64 tokens, 8 of 256 experts of 4096 x 2048
-// 64x256 241, 32x64 325, 128x128 284; 2048 tokens, 8 of 64 of 2048 x 4096 256x256
-// 184, 128x256 195, 128x128 252; 1 token, 8 of 256 of 2048 x 4096 32x64 15.2, 64x256 19.7.
+// 64x256 254, 32x64 326, 128x128 291; 2048 tokens, 8 of 64 of 2048 x 4096 256x256
+// 197 to 206, 128x256 200, 128x128 254; 1 token, 8 of 256 of 2048 x 4096 32x64 15.1,
+// 64x256 19.6.
 double estimate_experts(const I8Config &d, int64_t pairs, int experts, int64_t N, int64_t K)
 {
     const double hit = (double)std::min<int64_t>(experts, pairs), rows = (double)pairs / hit;

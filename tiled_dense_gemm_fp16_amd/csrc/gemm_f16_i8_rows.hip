@@ -59,8 +59,9 @@ __device__ __forceinline__ int code_of(float x, float m, float inverse)
 
 // THREADS threads take a row, 16 elements each at a time; up to HELD of those stay
 // in registers between the search for the largest magnitude and the rounding,
-// longer rows are read again.  Bound by memory where rows are many (8192 x 8192 33
-// us, 6 TB/s), else by the latency of load, search and store (13 x 4100 4.1 us).
+// longer rows are read again.  Bound by memory where rows are many (8192 x 8192 37 us
+// from memory, 5.4 TB/s; 32 where X is still in a cache), else by the latency of load,
+// search and store (13 x 4100 4.1 us).
 constexpr int block_of(int threads) { return threads > 256 ? threads : 256; }
 template <int THREADS, int HELD>
 __global__ void __launch_bounds__(block_of(THREADS)) i8_compress_kernel(const half_t *__restrict__ X, int64_t stride, int8_t *__restrict__ codes,
@@ -144,7 +145,7 @@ __device__ __forceinline__ int64_t quotient(int64_t i, int64_t n, int64_t items)
     return items < (int64_t)1 << 31 ? (int64_t)((uint32_t)i / (uint32_t)n) : i / n;
 }
 
-// Sixteen codes of a row a thread.  Bound by memory: 8192 x 8192 30 us, 6.6 TB/s.
+// Sixteen codes of a row a thread.  Bound by memory: 8192 x 8192 39 us, 5.2 TB/s; 30 where the codes were just written.
 __global__ void __launch_bounds__(256) i8_expand_kernel(const int8_t *__restrict__ codes, int64_t pitch,
                                                         const float *__restrict__ scales, half_t *__restrict__ X, int64_t items,
                                                         int64_t K, int64_t per_row)
@@ -255,7 +256,7 @@ hipError_t launch_i8_compress(const _Float16 *X, int64_t stride, int8_t *codes, 
     else if (K <= 8192)
         hipLaunchKernelGGL((i8_compress_kernel<256, 2>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, pitch, scales,
                            rows, K);
-    else if (K <= 16384 && rows >= 256)   // (8192 x 14336: 1024 threads 110 us)
+    else if (K <= 16384 && rows >= 256)   // (8192 x 14336: 73 us, 1024 threads 110)
         hipLaunchKernelGGL((i8_compress_kernel<256, 4>), dim3((unsigned)rows), dim3(256), 0, s, X, stride, codes, pitch, scales,
                            rows, K);
     else   // (1 x 28672: 256 threads, which hold 8192 elements, 7.8 us; 5.6 so)

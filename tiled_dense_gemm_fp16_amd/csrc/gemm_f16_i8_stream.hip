@@ -12,8 +12,8 @@
 // Loads are buffer loads: rows past the last, and chunks past K (whole 16-byte
 // chunks: K is a multiple of 16 here), read zeros without a branch.
 //
-// Bound by memory: 1 x 28672 x 8192 41 us, 5.7 TB/s; by the launch where W is small:
-// 1 x 1024 x 1024 3.7 us.
+// Bound by memory: 1 x 28672 x 8192 41 to 44 us, 5.3 to 5.7 TB/s; by the launch where W
+// is small: 1 x 1024 x 1024 3.3 us.
 #include "gemm_f16_i8_device.h"
 
 namespace gemm_f16_impl {
@@ -23,7 +23,8 @@ namespace {
 constexpr int kWaves = 8;
 constexpr int kChunks = kI8StreamK / 64;   // matrix instructions of a step for each 16 rows of W
 
-// (As written it takes 55 registers, which leaves room for four workgroups on a CU.
+// (As written it takes 55 registers, which leaves room for four workgroups on a CU; over
+// experts 79, for three.
 // Forms that take 83, for two workgroups, need 48 us for 1 x 28672 x 8192, with one
 // step at a time 43 to 45.)
 constexpr int NB = 1;      // blocks of 16 rows of W for a workgroup: 2 and 4 take 53 and 57 us there

@@ -14,7 +14,7 @@
 // Tiles of 64 rows and more are computed by eight waves, two for each SIMD: their
 // waits for loads overlap (four waves: 4096^3 58.8 us, eight 56.6; 64 tokens over 256
 // experts 261, 241); 256 x 128 keeps four (1000 x 5000 x 4100 39.7 us, 41.7).  At
-// 8192^3 (411 us, 2670 TOP/s; a library product reaches 2000) the matrix cores are busy
+// 8192^3 (410 to 420 us, 2650 TOP/s; a library product reaches 2000) the matrix cores are busy
 // 0.68 of the cycles and the clock falls to 1.8 GHz; smaller and colder products
 // wait for memory (1000 x 5000 x 4100 busy 0.46, waves wait 0.32 of theirs; 2048 tokens
 // over 64 experts 0.52, 0.44).  Slices of 64 bytes, of which twice as many are in
@@ -22,7 +22,7 @@
 // barriers for one.
 //
 // 192 columns are there for products whose tiles of 256 leave CUs idle (1000 x 5000 x
-// 4100 28 us in 216 workgroups, 32 in 160; 512 x 5000 x 8192 36, 38).
+// 4100, rows of 4224 bytes, 28 us in 216 workgroups, 32 in 160; 512 x 5000 x 8192 37, 40).
 //
 // Experts: a tile's rows of A are those of up to BM pairs of one expert, each
 // fetched from where its row is (a direct load takes an address of its own
@@ -178,7 +178,9 @@ __device__ __forceinline__ void i8_tile(const I8Args &p, half_t *lds, const I8Ti
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
     };
-    // The first requests: W's, which need no pairs, before A's.
+    // The first requests.  (Over experts W's come before A's, whose rows have to pass
+    // through LDS; which rows those are, and the expert, is known by now: the test for
+    // pairs of none has waited for `order`.)
     if (nk > 0)
         opb.issue(0, Bs, wave);
     if constexpr (EXPERTS) {
@@ -219,7 +221,8 @@ __device__ __forceinline__ void i8_tile(const I8Args &p, half_t *lds, const I8Ti
                 opb.issue(s, Bs + s * B_STAGE, wave);
         }
     // the factors of the tile's rows and columns, for the end (past the edges:
-    // any, their products are not stored)
+    // any, their products are not stored).  Loads arrive in order, so the waits for
+    // these are waits for all slices requested above, too.
     if constexpr (OUT != kPartial) {
 #pragma unroll
         for (int i = 0; i < MINE; ++i)

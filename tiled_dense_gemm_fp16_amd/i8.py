@@ -156,8 +156,9 @@ def gemm_i8_experts(a: I8Matrix, w: I8Matrix, order: ExpertOrder, epilogue: str 
     """tokens x top_k x n float16: epi(alpha * (row @ w[expert]^T)) for each
     pair of ``order``, zeros for the pairs of no expert.  ``w`` holds experts x
     n rows; ``a`` one row for each token (which its top_k pairs share) or one
-    for each pair (tokens x top_k x k, as the first product's result has).
-    Computed as by gemm_i8, bit for bit."""
+    for each pair (tokens x top_k x k, as the first product's result has);
+    its codes are limited to 2 GiB, so more tokens take several calls, each
+    with the order of its own ids.  Computed as by gemm_i8, bit for bit."""
     return _call("experts", stream, a, w, order, _epilogue(epilogue), out, config, alpha)
 
 
